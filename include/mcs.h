@@ -240,6 +240,116 @@ mcs_status mcs_residual_store(const mcs_desc *desc, const void *o_dense, const v
 mcs_status mcs_residual_apply(const mcs_desc *desc, const void *o_sparse, const void *r, void *o,
                               mcs_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the attention call: rotary positions, per-head norms of queries and
+ * keys, and the projections before and after. The method's pages take q, k, v
+ * as given; these entry points produce them from a block's hidden states in the
+ * layout the calls above take, and project the attention output back.
+ */
+
+/* Rotary positions with up to three axes (time, height, width). The elements of
+ * a head turn in pairs; pair j of axis a (0 <= j < dims[a] / 2) turns by
+ *   angle = (start[a] + p_a) * scale[a] * theta^(-2 j / dims[a])
+ * for a token at position p_a on that axis: (x0, x1) becomes (x0 cos - x1 sin,
+ * x0 sin + x1 cos). The axes' pairs follow one another: with R = sum of dims,
+ * pair i (0 <= i < R / 2) is elements (2i, 2i + 1) for MCS_ROPE_INTERLEAVED and
+ * elements (i, i + R / 2) for MCS_ROPE_HALF. Elements from R on do not turn.
+ * dims: even, at least 2, R <= d (R == d for MCS_ROPE_HALF); len: positions per
+ * axis, each at least 1; unused axes (index >= axes) are ignored. start and
+ * scale may be fractional. Angles are computed in 64 bits.
+ * Positions of tokens, with pos == NULL: tokens first .. first + len[0] * len[1]
+ * * len[2] - 1 are the grid in (t, y, x) order, the last axis fastest, and the
+ * other tokens (a text prefix or suffix) do not turn. With pos: int32 [B, N,
+ * axes], 16-byte aligned, every entry in [0, len[a]); a token with an entry
+ * outside is left unwritten and flagged MCS_ERR_DEVICE_BOUNDS (`first` is
+ * ignored). */
+typedef enum { MCS_ROPE_INTERLEAVED = 0, MCS_ROPE_HALF = 1 } mcs_rope_style;
+typedef struct {
+  int axes;            /* 1 .. 3 */
+  int dims[3];
+  int len[3];
+  int style;           /* mcs_rope_style */
+  int first;
+  double start[3];
+  double scale[3];
+  double theta;        /* finite, > 0 */
+} mcs_rope;
+
+/* Element strides of a [B, H, N, d] view whose d elements are contiguous; each
+ * a multiple of 16 bytes. A packed projection [B, N, 3, H, d] is three views
+ * with batch = N*3*H*d, head = d, token = 3*H*d. The stride of a dimension of
+ * size 1 is ignored. Views that are written may not overlap themselves. */
+typedef struct { int64_t batch, head, token; } mcs_strides;
+
+/* The cosines and sines of every position of every axis, fp32 (cos, sin) pairs:
+ * axis after axis, position after position, dims[a] / 2 pairs each. A table is
+ * made once per geometry and kept by the caller. mcs_rope_table_size: its bytes
+ * (0 for an invalid description; host only). table: device output. */
+size_t mcs_rope_table_size(const mcs_rope *rope);
+mcs_status mcs_rope_table(const mcs_rope *rope, float *table, mcs_stream stream);
+
+/* Rotation of one tensor: out = R x, or R^T x (the inverse, which is also the
+ * gradient) with inverse != 0. x, out: [B,H,N,d] views in the I/O dtype with
+ * strides xs, os (NULL: contiguous); out may be x with equal strides. One pass,
+ * fp32 arithmetic, one rounding. Errors: MCS_ERR_INVALID_ARG for a bad pointer,
+ * stride or grid (the grid must fit in N), MCS_ERR_UNSUPPORTED for a rope
+ * outside the set above. desc->C, scale and pddp_iters have no effect here. */
+mcs_status mcs_rope_apply(const mcs_desc *desc, const mcs_rope *rope, const float *table, const int32_t *pos,
+                          const void *x, const mcs_strides *xs, void *out, const mcs_strides *os, int inverse,
+                          mcs_stream stream);
+
+/* Norms of queries and keys for each head, the rotation, and the layout change,
+ * in one pass: q_out = R (q * rstd * wq) with rstd = 1 / sqrt(mean(q^2) + eps)
+ * over the d elements of each token and head, k likewise, and v copied, all
+ * rounded once. q, k, v: views with the strides `in` (NULL: contiguous), e.g. the
+ * packed output of a projection; q_out, k_out, v_out: contiguous [B,H,N,d], what
+ * mcs_dense_attn and the others take. Each of the three may be absent (input and
+ * output both NULL), not all. wq, wk: [d] in the I/O dtype, or NULL for 1.
+ * eps: finite, > 0. */
+mcs_status mcs_qk_norm_rope(const mcs_desc *desc, const mcs_rope *rope, const float *table, const int32_t *pos,
+                            const void *q, const void *k, const void *v, const mcs_strides *in, const void *wq,
+                            const void *wk, float eps, void *q_out, void *k_out, void *v_out, mcs_stream stream);
+
+/* Gradient of mcs_qk_norm_rope. dq_out, dk_out, dv_out: gradients of its outputs,
+ * contiguous [B,H,N,d]; q, k: its inputs (strides `in`); dq, dk, dv: gradients of
+ * its inputs, written with the same strides `in`; dwq, dwk: fp32 [d] gradients of
+ * the weights (overwritten), or NULL. With g = R^T dq_out and xhat = q * rstd:
+ * dwq = sum over b, h, n of g * xhat; dq = rstd * (g wq - xhat * mean(g wq xhat)).
+ * dv is dv_out in the layout of `in`. Each of the three groups may be absent.
+ * Sums are fp32 in a fixed order: equal calls give equal bits. Tokens with a
+ * position out of range are left unwritten, flagged, and add nothing to dwq, dwk.
+ * ws: at least mcs_qk_norm_rope_bwd_workspace_size(desc) bytes (0 for an invalid
+ * description); calls that may run at the same time need one each. */
+size_t mcs_qk_norm_rope_bwd_workspace_size(const mcs_desc *desc);
+mcs_status mcs_qk_norm_rope_bwd(const mcs_desc *desc, const mcs_rope *rope, const float *table, const int32_t *pos,
+                                const void *q, const void *k, const mcs_strides *in, const void *wq, const void *wk,
+                                float eps, const void *dq_out, const void *dk_out, const void *dv_out, void *dq,
+                                void *dk, void *dv, float *dwq, float *dwk, void *ws, size_t ws_bytes,
+                                mcs_stream stream);
+
+/* Matrix product with its epilogue: y = residual + gate_b * act(x w^T + bias),
+ * sums, activation and epilogue in fp32, one rounding.
+ * x: [B, N, in] contiguous, or with heads > 0 the attention's own output layout
+ * [B, heads, N, in / heads] (in / heads 64 or 128), so that an output projection
+ * needs no transposed copy. w: [out, in]. bias: [out] or NULL. gate: [B, out],
+ * one row per batch, or NULL for 1. residual: [B, N, out] or NULL for 0. y:
+ * [B, N, out]; y may be residual. All in the I/O dtype, 16-byte aligned. act:
+ * mcs_act; MCS_ACT_GELU_TANH is z / (1 + exp(-2 sqrt(2/pi) (z + 0.044715 z^3))),
+ * MCS_ACT_GELU_ERF z/2 (1 + erf(z / sqrt 2)), MCS_ACT_SILU z / (1 + exp(-z)).
+ * Supported: in a multiple of 8 (BF16) or 4 (F32), out any; in, out <= 2^20,
+ * B * N < 2^31 - 256, else MCS_ERR_UNSUPPORTED. BF16 runs on the tensor cores,
+ * F32 in fp32 SIMT arithmetic. No workspace. Equal calls give equal bits. */
+typedef enum { MCS_ACT_NONE = 0, MCS_ACT_GELU_TANH = 1, MCS_ACT_GELU_ERF = 2, MCS_ACT_SILU = 3 } mcs_act;
+typedef struct {
+  int B, N;
+  int in, out;
+  int heads;           /* 0: x is [B, N, in] */
+  int dtype;           /* mcs_dtype */
+  int act;             /* mcs_act */
+} mcs_linear_desc;
+mcs_status mcs_linear(const mcs_linear_desc *desc, const void *x, const void *w, const void *bias, const void *gate,
+                      const void *residual, void *y, mcs_stream stream);
+
 /* Synchronises `stream`, then reports (and clears) the device-side flags raised
  * since the last call: MCS_ERR_DEVICE_BOUNDS, MCS_ERR_DEVICE_TIMEOUT, or a
  * sticky CUDA error as MCS_ERR_CUDA. MCS_OK if none. */

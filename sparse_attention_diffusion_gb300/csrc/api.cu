@@ -242,6 +242,11 @@ mcs_status anchor_select_rows(const mcs_desc* desc, const void* q, const void* k
 }
 
 void note_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }
+mcs_status validate_desc(const mcs_desc* desc) {
+  Dims dm;
+  return check_desc(desc, &dm);
+}
+mcs_status current_device(uint32_t** status, int* sms) { return device_state(status, sms); }
 uint32_t* status_word_for_current_device() {
   uint32_t* st = nullptr;
   return device_state(&st, nullptr) == MCS_OK ? st : nullptr;

@@ -17,4 +17,9 @@ mcs_status anchor_select_rows(const mcs_desc* desc, const void* q, const void* k
                               const float* lse, int K, int32_t* idx, float* mass, float* scores, size_t score_bytes,
                               cudaStream_t stream);
 
+// The checks every entry point makes of its mcs_desc (api.cu).
+mcs_status validate_desc(const mcs_desc* desc);
+// Status word and SM count of the current device.
+mcs_status current_device(uint32_t** status, int* sms);
+
 }  // namespace mcs

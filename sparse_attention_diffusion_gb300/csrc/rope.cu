@@ -1,0 +1,420 @@
+// Rotary positions with several axes, and the norms of queries and keys for
+// each head with the rotation in the same pass (forward and backward).
+//
+//   y = R(n) (x * rstd * w),  rstd = 1 / sqrt(mean(x^2) + eps)
+//
+// with R(n) turning the head's element pairs by the token's angles. Everything
+// here reads its rows once and writes them once: HBM bounds it, the table of
+// cosines and sines (a few hundred KB at most on a video grid) stays in L1/L2.
+// The angles come from a table because a position far from the origin needs
+// 64-bit angles, which are too slow to make for every token.
+//
+// A row (one token of one head, d elements) is held by D * sizeof(T) / 16 lanes
+// of one warp, 16 bytes a lane; a lane always holds both elements of a pair, so
+// the rotation needs no exchange, and the norm only the shuffle sum over the
+// row's lanes. The lanes of a row keep their token's cosines and sines in
+// registers and walk over its heads.
+#include "rope.h"
+
+#include "common.cuh"
+#include "kernels.h"
+#include "status.cuh"
+
+namespace mcs {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int D>
+struct Row {
+  static constexpr int E = 16 / int(sizeof(T));  // elements a lane
+  static constexpr int L = D / E;                // lanes a row
+  static constexpr int NP = E / 2;               // pairs a lane
+  static constexpr int kTokens = kThreads / L;   // rows a block holds at once
+};
+
+// 16 bytes of a row as loaded: interleaved pairs are one 16-byte piece, halves
+// are 8 bytes of the first half and the matching 8 bytes of the second.
+struct Raw {
+  uint32_t w[4];
+};
+
+template <typename T, int D, bool kHalf>
+__device__ __forceinline__ Raw load_raw(const T* row, int lane) {
+  Raw r;
+  if constexpr (kHalf) {
+    const uint2 a = *reinterpret_cast<const uint2*>(row + lane * Row<T, D>::NP);
+    const uint2 b = *reinterpret_cast<const uint2*>(row + D / 2 + lane * Row<T, D>::NP);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = b.x, r.w[3] = b.y;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(row + lane * Row<T, D>::E);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+  }
+  return r;
+}
+template <typename T, int D, bool kHalf>
+__device__ __forceinline__ void store_raw(T* row, int lane, const Raw& r) {
+  if constexpr (kHalf) {
+    *reinterpret_cast<uint2*>(row + lane * Row<T, D>::NP) = make_uint2(r.w[0], r.w[1]);
+    *reinterpret_cast<uint2*>(row + D / 2 + lane * Row<T, D>::NP) = make_uint2(r.w[2], r.w[3]);
+  } else {
+    *reinterpret_cast<uint4*>(row + lane * Row<T, D>::E) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  }
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Raw words <-> the lane's pairs (a[j], b[j]).
+template <typename T, bool kHalf, int NP>
+__device__ __forceinline__ void unpack(const Raw& r, float (&a)[NP], float (&b)[NP]) {
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (kHalf) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[2 * i] = bf16_lo(r.w[i]), a[2 * i + 1] = bf16_hi(r.w[i]);
+        b[2 * i] = bf16_lo(r.w[2 + i]), b[2 * i + 1] = bf16_hi(r.w[2 + i]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = bf16_lo(r.w[j]), b[j] = bf16_hi(r.w[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      a[j] = __uint_as_float(r.w[kHalf ? j : 2 * j]);
+      b[j] = __uint_as_float(r.w[kHalf ? 2 + j : 2 * j + 1]);
+    }
+  }
+}
+template <typename T, bool kHalf, int NP>
+__device__ __forceinline__ Raw pack(const float (&a)[NP], const float (&b)[NP]) {
+  Raw r;
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (kHalf) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        r.w[i] = bf16_pair(a[2 * i], a[2 * i + 1]);
+        r.w[2 + i] = bf16_pair(b[2 * i], b[2 * i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[j] = bf16_pair(a[j], b[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      r.w[kHalf ? j : 2 * j] = __float_as_uint(a[j]);
+      r.w[kHalf ? 2 + j : 2 * j + 1] = __float_as_uint(b[j]);
+    }
+  }
+  return r;
+}
+
+// Cosines and sines of the pairs lane * NP .. + NP - 1 of token n of batch b.
+// Returns false when a listed position is out of range (nothing is read then).
+template <int NP>
+__device__ __forceinline__ bool load_angles(const RopeGeom& g, const float2* table, const int32_t* pos, int b, int N,
+                                            int n, int lane, float (&c)[NP], float (&s)[NP]) {
+  int p[3] = {0, 0, 0};
+  bool turns = true;
+  if (pos != nullptr) {
+    const int32_t* row = pos + (size_t(b) * N + n) * g.axes;
+    for (int a = 0; a < g.axes; ++a) {
+      p[a] = row[a];
+      if (p[a] < 0 || p[a] >= g.len[a]) return false;
+    }
+  } else {
+    int i = n - g.first;
+    turns = i >= 0 && i < g.ngrid;
+    for (int a = g.axes - 1; a > 0; --a) {
+      p[a] = i % g.len[a];
+      i /= g.len[a];
+    }
+    p[0] = i;
+  }
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    c[j] = 1.f, s[j] = 0.f;
+    int pr = lane * NP + j;
+    if (turns && pr < g.npairs) {
+      int a = 0;
+      while (pr >= g.pairs[a]) pr -= g.pairs[a++];
+      const float2 t = __ldg(table + g.toff[a] + p[a] * g.pairs[a] + pr);
+      c[j] = t.x, s[j] = t.y;
+    }
+  }
+  return true;
+}
+
+template <int L>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The lane's norm weights in pair order (1 where absent).
+template <typename T, int D, bool kHalf, int NP>
+__device__ __forceinline__ void load_weights(const void* w, int lane, float (&a)[NP], float (&b)[NP]) {
+#pragma unroll
+  for (int j = 0; j < NP; ++j) a[j] = b[j] = 1.f;
+  if (w != nullptr) unpack<T, kHalf, NP>(load_raw<T, D, kHalf>(static_cast<const T*>(w), lane), a, b);
+}
+
+__global__ void rope_table_kernel(const RopeTableParams p) {
+  const int a = blockIdx.y;
+  const long long total = static_cast<long long>(p.g.len[a]) * p.g.pairs[a];
+  for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < total;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int pos = int(i / p.g.pairs[a]), j = int(i % p.g.pairs[a]);
+    const double f = pow(p.theta, -double(j) / p.g.pairs[a]);
+    double sn, cs;
+    sincos((p.start[a] + pos) * p.scale[a] * f, &sn, &cs);
+    p.table[p.g.toff[a] + i] = make_float2(float(cs), float(sn));
+  }
+}
+
+// Heads whose rows one lane has in flight at once.
+constexpr int kUnroll = 4;
+
+template <typename T, int D, bool kHalf, bool kNorm>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) {
+  using R = Row<T, D>;
+  constexpr int NP = R::NP;
+  const int lane = threadIdx.x % R::L;
+  const int n = blockIdx.x * R::kTokens + threadIdx.x / R::L, b = blockIdx.z;
+  const int h_beg = blockIdx.y * p.heads_per_block, h_end = min(p.H, h_beg + p.heads_per_block);
+  float c[NP], s[NP];
+  bool live = n < p.N;
+  if (live && !load_angles<NP>(p.g, p.table, p.pos, b, p.N, n, lane, c, s)) {
+    live = false;
+    raise_status(p.status, kStatusBounds);
+  }
+  if (!live) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) c[j] = s[j] = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NP; ++j) s[j] *= p.sin_sign;
+  const long long in_off = b * p.in.b + n * p.in.n, out_off = b * p.out.b + n * p.out.n;
+#pragma unroll
+  for (int st = 0; st < (kNorm ? 3 : 1); ++st) {
+    if (p.src[st] == nullptr) continue;
+    const T* src = static_cast<const T*>(p.src[st]) + in_off;
+    T* dst = static_cast<T*>(p.dst[st]) + out_off;
+    float wa[NP], wb[NP];
+    if constexpr (kNorm) {
+      if (st < 2) load_weights<T, D, kHalf, NP>(p.w[st], lane, wa, wb);
+    }
+    for (int h0 = h_beg; h0 < h_end; h0 += kUnroll) {
+      Raw r[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        r[u] = Raw{};
+        if (live && h0 + u < h_end) r[u] = load_raw<T, D, kHalf>(src + (h0 + u) * p.in.h, lane);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (st < 2) {
+          float x[NP], y[NP];
+          unpack<T, kHalf, NP>(r[u], x, y);
+          if constexpr (kNorm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < NP; ++j) ss += x[j] * x[j] + y[j] * y[j];
+            const float rstd = rsqrtf(row_sum<R::L>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) x[j] *= rstd * wa[j], y[j] *= rstd * wb[j];
+          }
+          float xr[NP], yr[NP];
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            xr[j] = x[j] * c[j] - y[j] * s[j];
+            yr[j] = x[j] * s[j] + y[j] * c[j];
+          }
+          r[u] = pack<T, kHalf, NP>(xr, yr);
+        }
+        if (live && h0 + u < h_end) store_raw<T, D, kHalf>(dst + (h0 + u) * p.out.h, lane, r[u]);
+      }
+    }
+  }
+}
+
+// Gradient of norm + rotation. Blocks walk over (batch, token tile) pairs; a
+// lane's share of dw (its own pairs, all its tokens and heads) stays in
+// registers, is summed over the block's rows through shared memory, and goes to
+// partial[block]; norm_bwd_reduce_kernel adds the blocks in order.
+template <typename T, int D, bool kHalf>
+__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdParams p) {
+  using R = Row<T, D>;
+  constexpr int NP = R::NP;
+  __shared__ float red[R::kTokens][D];
+  const int lane = threadIdx.x % R::L, row = threadIdx.x / R::L;
+  const int tiles = (p.N + R::kTokens - 1) / R::kTokens;
+  const long long units = static_cast<long long>(tiles) * p.B * p.H;
+#pragma unroll 1
+  for (int st = 0; st < 3; ++st) {
+    if (p.dy[st] == nullptr) continue;
+    float da[NP], db[NP], wa[NP], wb[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) da[j] = db[j] = 0.f;
+    if (st < 2) load_weights<T, D, kHalf, NP>(p.w[st], lane, wa, wb);
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+      const int h = int(u % p.H);
+      const long long bt = u / p.H;
+      const int b = int(bt / tiles), n = int(bt % tiles) * R::kTokens + row;
+      float c[NP], s[NP];
+      bool live = n < p.N;
+      if (live && !load_angles<NP>(p.g, p.table, p.pos, b, p.N, n, lane, c, s)) {
+        live = false;
+        raise_status(p.status, kStatusBounds);
+      }
+      const long long off = b * p.in.b + n * p.in.n + h * p.in.h;
+      const T* dy = static_cast<const T*>(p.dy[st]) + ((static_cast<long long>(b) * p.H + h) * p.N + n) * D;
+      T* dx = static_cast<T*>(p.dx[st]) + off;
+      Raw ry{}, rx{};
+      if (live) ry = load_raw<T, D, kHalf>(dy, lane);
+      if (st == 2) {
+        if (live) store_raw<T, D, kHalf>(dx, lane, ry);
+        continue;
+      }
+      if (live) rx = load_raw<T, D, kHalf>(static_cast<const T*>(p.x[st]) + off, lane);
+      float x[NP], y[NP], gx[NP], gy[NP];
+      unpack<T, kHalf, NP>(rx, x, y);
+      unpack<T, kHalf, NP>(ry, gx, gy);
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) ss += x[j] * x[j] + y[j] * y[j];
+      const float rstd = rsqrtf(row_sum<R::L>(ss) * (1.f / D) + p.eps);
+      float dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const float cj = live ? c[j] : 0.f, sj = live ? s[j] : 0.f;
+        const float ga = gx[j] * cj + gy[j] * sj, gb = gy[j] * cj - gx[j] * sj;
+        x[j] *= rstd, y[j] *= rstd;  // normalised row
+        da[j] += ga * x[j], db[j] += gb * y[j];
+        gx[j] = ga * wa[j], gy[j] = gb * wb[j];
+        dot += gx[j] * x[j] + gy[j] * y[j];
+      }
+      dot = row_sum<R::L>(dot) * (1.f / D);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        gx[j] = rstd * (gx[j] - x[j] * dot);
+        gy[j] = rstd * (gy[j] - y[j] * dot);
+      }
+      if (live) store_raw<T, D, kHalf>(dx, lane, pack<T, kHalf, NP>(gx, gy));
+    }
+    if (st < 2 && p.dw[st] != nullptr) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int pr = lane * NP + j;
+        red[row][kHalf ? pr : 2 * pr] = da[j];
+        red[row][kHalf ? D / 2 + pr : 2 * pr + 1] = db[j];
+      }
+      __syncthreads();
+      if (threadIdx.x < D) {
+        float v = 0.f;
+        for (int i = 0; i < R::kTokens; ++i) v += red[i][threadIdx.x];
+        p.partial[(size_t(blockIdx.x) * 2 + st) * D + threadIdx.x] = v;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// dw[st][e] = sum over blocks of partial[block][st][e], in a fixed order.
+__global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float* partial, int nblk, int D, float* dwq,
+                                                               float* dwk) {
+  __shared__ float red[1024];
+  const int st = blockIdx.x, e = threadIdx.x % D, part = threadIdx.x / D, parts = blockDim.x / D;
+  float* dw = st == 0 ? dwq : dwk;
+  if (dw == nullptr) return;
+  float v = 0.f;
+  for (int i = part; i < nblk; i += parts) v += partial[(size_t(i) * 2 + st) * D + e];
+  red[threadIdx.x] = v;
+  __syncthreads();
+  if (part == 0) {
+    for (int i = 1; i < parts; ++i) v += red[i * D + e];
+    dw[e] = v;
+  }
+}
+
+template <typename T, int D, bool kHalf, bool kNorm>
+cudaError_t launch_rotate(RotateParams p, int num_sms, cudaStream_t s) {
+  using R = Row<T, D>;
+  const int tiles = (p.N + R::kTokens - 1) / R::kTokens;
+  // all heads of a token in one block when the tokens alone fill the GPU;
+  // otherwise the heads are split until about two blocks per SM are there
+  const long long rows = static_cast<long long>(tiles) * p.B;
+  long long chunks = (2ll * num_sms + rows - 1) / rows;
+  if (chunks > p.H) chunks = p.H;
+  p.heads_per_block = int((p.H + chunks - 1) / chunks);
+  const dim3 grid(tiles, (p.H + p.heads_per_block - 1) / p.heads_per_block, p.B);
+  rotate_kernel<T, D, kHalf, kNorm><<<grid, kThreads, 0, s>>>(p);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, bool kHalf>
+cudaError_t launch_bwd(const NormBwdParams& p, int num_sms, cudaStream_t s) {
+  using R = Row<T, D>;
+  const long long units = static_cast<long long>((p.N + R::kTokens - 1) / R::kTokens) * p.B * p.H;
+  long long blocks = 4ll * num_sms;
+  if (blocks > kNormBwdMaxBlocks) blocks = kNormBwdMaxBlocks;
+  if (blocks > units) blocks = units;
+  norm_bwd_kernel<T, D, kHalf><<<int(blocks), kThreads, 0, s>>>(p);
+  note_launches(1);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (p.dw[0] == nullptr && p.dw[1] == nullptr)) return e;
+  norm_bwd_reduce_kernel<<<2, 1024, 0, s>>>(p.partial, int(blocks), D, p.dw[0], p.dw[1]);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t rotate_td(bool half_style, bool norm, const RotateParams& p, int num_sms, cudaStream_t s) {
+  if (half_style)
+    return norm ? launch_rotate<T, D, true, true>(p, num_sms, s) : launch_rotate<T, D, true, false>(p, num_sms, s);
+  return norm ? launch_rotate<T, D, false, true>(p, num_sms, s) : launch_rotate<T, D, false, false>(p, num_sms, s);
+}
+template <typename T, int D>
+cudaError_t bwd_td(bool half_style, const NormBwdParams& p, int num_sms, cudaStream_t s) {
+  return half_style ? launch_bwd<T, D, true>(p, num_sms, s) : launch_bwd<T, D, false>(p, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t rope_table(const RopeTableParams& p, cudaStream_t s) {
+  long long most = 0;
+  for (int a = 0; a < p.g.axes; ++a) {
+    const long long n = static_cast<long long>(p.g.len[a]) * p.g.pairs[a];
+    if (n > most) most = n;
+  }
+  const long long blocks = (most + 127) / 128;
+  const dim3 grid(unsigned(blocks < 4096 ? blocks : 4096), p.g.axes);
+  rope_table_kernel<<<grid, 128, 0, s>>>(p);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t rotate(bool bf16, int d, bool half_style, bool norm, RotateParams p, int num_sms, cudaStream_t s) {
+  if (bf16)
+    return d == 128 ? rotate_td<__nv_bfloat16, 128>(half_style, norm, p, num_sms, s)
+                    : rotate_td<__nv_bfloat16, 64>(half_style, norm, p, num_sms, s);
+  return d == 128 ? rotate_td<float, 128>(half_style, norm, p, num_sms, s)
+                  : rotate_td<float, 64>(half_style, norm, p, num_sms, s);
+}
+
+cudaError_t qk_norm_rope_bwd(bool bf16, int d, bool half_style, const NormBwdParams& p, int num_sms, cudaStream_t s) {
+  if (bf16)
+    return d == 128 ? bwd_td<__nv_bfloat16, 128>(half_style, p, num_sms, s)
+                    : bwd_td<__nv_bfloat16, 64>(half_style, p, num_sms, s);
+  return d == 128 ? bwd_td<float, 128>(half_style, p, num_sms, s) : bwd_td<float, 64>(half_style, p, num_sms, s);
+}
+
+}  // namespace mcs

@@ -26,7 +26,9 @@ EXPORTS = ("mcs_workspace_size", "mcs_group_pddp", "mcs_dense_attn", "mcs_anchor
            "mcs_selftest_tma_gather", "mcs_anchor_select_noalloc", "mcs_sparse_attn_gather_host",
            "mcs_sparse_attn_gather_host_workspace_size", "mcs_cache_entry_bytes", "mcs_cache_ring_create",
            "mcs_cache_ring_acquire", "mcs_cache_ring_release", "mcs_cache_ring_destroy",
-           "mcs_selftest_wait_timeout", "mcs_pddp_dirs_size", "mcs_group_pddp_warm", "mcs_selftest_ex2_rate")
+           "mcs_selftest_wait_timeout", "mcs_pddp_dirs_size", "mcs_group_pddp_warm", "mcs_selftest_ex2_rate",
+           "mcs_rope_table_size", "mcs_rope_table", "mcs_rope_apply", "mcs_qk_norm_rope",
+           "mcs_qk_norm_rope_bwd_workspace_size", "mcs_qk_norm_rope_bwd", "mcs_linear")
 
 
 class McsError(RuntimeError):
@@ -40,6 +42,25 @@ class mcs_desc(ctypes.Structure):
                 ("C", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
                 ("pddp_iters", ctypes.c_int)]
 
+
+class mcs_rope(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int), ("dims", ctypes.c_int * 3), ("len", ctypes.c_int * 3), ("style", ctypes.c_int),
+                ("first", ctypes.c_int), ("start", ctypes.c_double * 3), ("scale", ctypes.c_double * 3),
+                ("theta", ctypes.c_double)]
+
+
+class mcs_strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class mcs_linear_desc(ctypes.Structure):
+    # "in" and "out" of the C struct are in_features and out_features here
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("in_features", ctypes.c_int),
+                ("out_features", ctypes.c_int), ("heads", ctypes.c_int), ("dtype", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+ROPE_STYLES = {"interleaved": 0, "half": 1}
+ACTIVATIONS = {"none": 0, "gelu_tanh": 1, "gelu_erf": 2, "silu": 3}
 
 _lib = None
 
@@ -60,6 +81,7 @@ def load(build_if_missing: bool = False):
     L = ctypes.CDLL(_build.LIB)
     P, I, Z, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
     D = ctypes.POINTER(mcs_desc)
+    R, V, F = ctypes.POINTER(mcs_rope), ctypes.POINTER(mcs_strides), ctypes.c_float
     sig = {
         "mcs_workspace_size": (Z, [D, I]),
         "mcs_group_pddp": (I, [D, P, P, P, P, Z, S]),
@@ -87,6 +109,13 @@ def load(build_if_missing: bool = False):
                                        ctypes.POINTER(ctypes.c_void_p)]),
         "mcs_cache_ring_release": (I, [P, I, I, S]),
         "mcs_cache_ring_destroy": (I, [P]),
+        "mcs_rope_table_size": (Z, [R]),
+        "mcs_rope_table": (I, [R, P, S]),
+        "mcs_rope_apply": (I, [D, R, P, P, P, V, P, V, I, S]),
+        "mcs_qk_norm_rope": (I, [D, R, P, P, P, P, P, V, P, P, F, P, P, P, S]),
+        "mcs_qk_norm_rope_bwd_workspace_size": (Z, [D]),
+        "mcs_qk_norm_rope_bwd": (I, [D, R, P, P, P, P, V, P, P, F, P, P, P, P, P, P, P, P, P, Z, S]),
+        "mcs_linear": (I, [ctypes.POINTER(mcs_linear_desc), P, P, P, P, P, P, S]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -367,6 +396,164 @@ def ex2_per_clock_per_sm(iters=1 << 14):
 def mcs_selftest_tma_gather(src, rows, out, stream=None):
     _check("mcs_selftest_tma_gather", load().mcs_selftest_tma_gather(_ptr(src), int(src.shape[0]), _ptr(rows), _ptr(out),
                                                                      _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the attention call
+def rope_desc(dims, lens, theta=10000.0, start=(0.0, 0.0, 0.0), scale=(1.0, 1.0, 1.0), style="interleaved",
+              first=0) -> mcs_rope:
+    """Rotary positions with one to three axes: dims[a] elements of the head turn with axis a, which has
+    lens[a] positions start[a], start[a] + 1, ... (times scale[a]); tokens first .. first + prod(lens) - 1
+    are the grid, last axis fastest."""
+    n = len(dims)
+    if not 1 <= n <= 3 or len(lens) != n or len(start) < n or len(scale) < n:
+        raise ValueError("dims and lens need one entry for each of one to three axes, start and scale at least as many")
+    if style not in ROPE_STYLES:
+        raise ValueError(f"style: one of {sorted(ROPE_STYLES)}, got {style!r}")
+
+    def three(v, cast):
+        return tuple(cast(x) for x in v[:n]) + (cast(0),) * (3 - n)
+
+    return mcs_rope(n, three(dims, int), three(lens, int), ROPE_STYLES[style], int(first), three(start, float),
+                    three(scale, float), float(theta))
+
+
+def rope_table(rope: mcs_rope, device="cuda", stream=None) -> torch.Tensor:
+    """The rope's fp32 (cos, sin) table [entries, 2], filled on `stream`."""
+    n = int(load().mcs_rope_table_size(ctypes.byref(rope)))
+    if n == 0:
+        raise McsError("mcs_rope_table_size", 1)
+    table = torch.empty((n // 8, 2), dtype=torch.float32, device=device)
+    mcs_rope_table(rope, table, stream)
+    return table
+
+
+def mcs_rope_table(rope, table, stream=None):
+    n = int(load().mcs_rope_table_size(ctypes.byref(rope)))
+    if n and (table.dtype != torch.float32 or table.numel() * 4 < n):
+        raise ValueError(f"table: expected {n // 4} fp32 elements, got {table.numel()} {table.dtype}")
+    _check("mcs_rope_table", load().mcs_rope_table(ctypes.byref(rope), _here(table), _stream(stream)))
+
+
+def _here(t):
+    """Pointer of a contiguous tensor on the current device (None passes through)."""
+    if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"libmcs launches on the current device, tensor is on {t.device}")
+    return _ptr(t)
+
+
+def _view(desc, name, t):
+    """Pointer and strides of a [B,H,N,d] view with contiguous d (None passes through)."""
+    if t is None:
+        return None, None
+    shape = (desc.B, desc.H, desc.N, desc.d)
+    if tuple(t.shape) != shape or t.dtype != _io_dtype(desc):
+        raise ValueError(f"{name}: expected {shape} {_io_dtype(desc)}, got {tuple(t.shape)} {t.dtype}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: libmcs takes tensors on the current device, got {t.device}")
+    sb, sh, sn, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {sd}")
+    size = (desc.B, desc.H, desc.N)
+    return ctypes.c_void_p(t.data_ptr()), tuple(s if n > 1 else 0 for s, n in zip((sb, sh, sn), size))
+
+
+def _views(desc, **tensors):
+    """Pointers of views that must share one set of strides, and those strides."""
+    ptrs, common = [], None
+    for name, t in tensors.items():
+        p, st = _view(desc, name, t)
+        ptrs.append(p)
+        if st is not None:
+            if common is not None and st != common:
+                raise ValueError(f"{name}: strides {st} differ from {common}; the views must share their strides")
+            common = st
+    return ptrs, common
+
+
+def _positions(desc, rope, table, pos):
+    """Host check of a rope's table and listed positions."""
+    n = int(load().mcs_rope_table_size(ctypes.byref(rope)))
+    if n and (table.dtype != torch.float32 or table.numel() * 4 < n):
+        raise ValueError(f"table: expected {n // 4} fp32 elements, got {table.numel()} {table.dtype}")
+    want = (desc.B, desc.N, rope.axes)
+    if pos is not None and (tuple(pos.shape) != want or pos.dtype != torch.int32):
+        raise ValueError(f"pos: expected {want} torch.int32, got {tuple(pos.shape)} {pos.dtype}")
+
+
+def _vector(name, t, n, dtype):
+    if t is not None and (tuple(t.shape) != (n,) or t.dtype != dtype):
+        raise ValueError(f"{name}: expected ({n},) {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def mcs_rope_apply(desc, rope, table, pos, x, out, inverse=False, stream=None):
+    """out = R x (or R^T x): x, out are [B,H,N,d] views with contiguous d; out may be x."""
+    _positions(desc, rope, table, pos)
+    xp, xs = _view(desc, "x", x)
+    op, os_ = _view(desc, "out", out)
+    _check("mcs_rope_apply", load().mcs_rope_apply(ctypes.byref(desc), ctypes.byref(rope), _here(table), _here(pos),
+                                                   xp, mcs_strides(*xs), op, mcs_strides(*os_), int(bool(inverse)),
+                                                   _stream(stream)))
+
+
+def mcs_qk_norm_rope(desc, rope, table, pos, q, k, v, wq, wk, eps, q_out, k_out, v_out, stream=None):
+    """Per-head RMS norm of q and k, rotation, and the copy of q, k, v (views that share their strides, e.g. of a
+    packed [B, N, 3, H, d] projection) into contiguous [B,H,N,d] tensors. Each of the three may be None."""
+    _positions(desc, rope, table, pos)
+    _expect(desc, q_out=q_out, k_out=k_out, v_out=v_out)
+    _vector("wq", wq, desc.d, _io_dtype(desc))
+    _vector("wk", wk, desc.d, _io_dtype(desc))
+    (qp, kp, vp), st = _views(desc, q=q, k=k, v=v)
+    _check("mcs_qk_norm_rope", load().mcs_qk_norm_rope(
+        ctypes.byref(desc), ctypes.byref(rope), _here(table), _here(pos), qp, kp, vp,
+        None if st is None else mcs_strides(*st), _here(wq), _here(wk), float(eps), _here(q_out), _here(k_out),
+        _here(v_out), _stream(stream)))
+
+
+def qk_norm_rope_bwd_workspace(desc, device="cuda") -> torch.Tensor:
+    n = int(load().mcs_qk_norm_rope_bwd_workspace_size(ctypes.byref(desc)))
+    if n == 0:
+        raise McsError("mcs_qk_norm_rope_bwd_workspace_size", 2)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mcs_qk_norm_rope_bwd(desc, rope, table, pos, q, k, wq, wk, eps, dq_out, dk_out, dv_out, dq, dk, dv, dwq, dwk, ws,
+                         stream=None):
+    """Gradients of mcs_qk_norm_rope: dq, dk, dv are written as views that share the strides of q and k; dwq, dwk are
+    fp32 [d] or None. Each group (q, dq_out, dq), (k, dk_out, dk), (dv_out, dv) may be None."""
+    _positions(desc, rope, table, pos)
+    _expect(desc, dq_out=dq_out, dk_out=dk_out, dv_out=dv_out)
+    _vector("wq", wq, desc.d, _io_dtype(desc))
+    _vector("wk", wk, desc.d, _io_dtype(desc))
+    _vector("dwq", dwq, desc.d, torch.float32)
+    _vector("dwk", dwk, desc.d, torch.float32)
+    (qp, kp, dqp, dkp, dvp), st = _views(desc, q=q, k=k, dq=dq, dk=dk, dv=dv)
+    _check("mcs_qk_norm_rope_bwd", load().mcs_qk_norm_rope_bwd(
+        ctypes.byref(desc), ctypes.byref(rope), _here(table), _here(pos), qp, kp,
+        None if st is None else mcs_strides(*st), _here(wq), _here(wk), float(eps), _here(dq_out), _here(dk_out),
+        _here(dv_out), dqp, dkp, dvp, _here(dwq), _here(dwk), _here(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def linear_desc(B, N, in_features, out_features, dtype, act="none", heads=0) -> mcs_linear_desc:
+    """Projection of B x N rows; heads > 0: the input is the attention's [B, heads, N, in_features / heads]."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: one of {sorted(ACTIVATIONS)}, got {act!r}")
+    dt = MCS_BF16 if dtype in (torch.bfloat16, "bf16", MCS_BF16) else MCS_F32
+    return mcs_linear_desc(int(B), int(N), int(in_features), int(out_features), int(heads), dt, ACTIVATIONS[act])
+
+
+def mcs_linear(desc, x, w, bias, gate, residual, y, stream=None):
+    """y = residual + gate * act(x w^T + bias); x [B, N, in] or [B, heads, N, in / heads], w [out, in], bias [out],
+    gate [B, out], residual and y [B, N, out] (bias, gate, residual may be None; y may be residual)."""
+    B, N, I, O, h = desc.B, desc.N, desc.in_features, desc.out_features, desc.heads
+    dt = _io_dtype(desc)
+    xs = (B, N, I) if h == 0 else (B, h, N, I // h)
+    for name, t, shape in (("x", x, xs), ("w", w, (O, I)), ("bias", bias, (O,)), ("gate", gate, (B, O)),
+                           ("residual", residual, (B, N, O)), ("y", y, (B, N, O))):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dt):
+            raise ValueError(f"{name}: expected {shape} {dt}, got {tuple(t.shape)} {t.dtype}")
+    _check("mcs_linear", load().mcs_linear(ctypes.byref(desc), _here(x), _here(w), _here(bias), _here(gate),
+                                           _here(residual), _here(y), _stream(stream)))
 
 
 # ---------------------------------------------------------------- convenience: buffers for one layer
