@@ -245,10 +245,13 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) 
   }
 }
 
-// Gradient of norm + rotation. Blocks walk over (batch, token tile) pairs; a
-// lane's share of dw (its own pairs, all its tokens and heads) stays in
-// registers, is summed over the block's rows through shared memory, and goes to
-// partial[block]; norm_bwd_reduce_kernel adds the blocks in order.
+// Gradient of norm + rotation. Blocks walk over (batch, token tile, head chunk)
+// units, the heads of a unit with the token's angles in registers; a lane's share
+// of dw (its own pairs, all its tokens and heads) stays in registers, is summed
+// over the block's rows through shared memory, and goes to partial[block];
+// norm_bwd_reduce_kernel adds the blocks in order.
+constexpr int kBwdUnroll = 2;
+
 template <typename T, int D, bool kHalf>
 __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdParams p) {
   using R = Row<T, D>;
@@ -256,7 +259,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdParams 
   __shared__ float red[R::kTokens][D];
   const int lane = threadIdx.x % R::L, row = threadIdx.x / R::L;
   const int tiles = (p.N + R::kTokens - 1) / R::kTokens;
-  const long long units = static_cast<long long>(tiles) * p.B * p.H;
+  const int chunks = (p.H + p.heads_per_unit - 1) / p.heads_per_unit;
+  const long long units = static_cast<long long>(tiles) * p.B * chunks;
 #pragma unroll 1
   for (int st = 0; st < 3; ++st) {
     if (p.dy[st] == nullptr) continue;
@@ -265,49 +269,63 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdParams 
     for (int j = 0; j < NP; ++j) da[j] = db[j] = 0.f;
     if (st < 2) load_weights<T, D, kHalf, NP>(p.w[st], lane, wa, wb);
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-      const int h = int(u % p.H);
-      const long long bt = u / p.H;
+      const long long bt = u / chunks;
       const int b = int(bt / tiles), n = int(bt % tiles) * R::kTokens + row;
+      const int h_beg = int(u % chunks) * p.heads_per_unit, h_end = min(p.H, h_beg + p.heads_per_unit);
       float c[NP], s[NP];
       bool live = n < p.N;
       if (live && !load_angles<NP>(p.g, p.table, p.pos, b, p.N, n, lane, c, s)) {
         live = false;
         raise_status(p.status, kStatusBounds);
       }
-      const long long off = b * p.in.b + n * p.in.n + h * p.in.h;
-      const T* dy = static_cast<const T*>(p.dy[st]) + ((static_cast<long long>(b) * p.H + h) * p.N + n) * D;
+      if (!live) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) c[j] = s[j] = 0.f;
+      }
+      const long long off = b * p.in.b + n * p.in.n;
+      const T* dy = static_cast<const T*>(p.dy[st]) + (static_cast<long long>(b) * p.H * p.N + n) * D;
+      const T* px = st < 2 ? static_cast<const T*>(p.x[st]) + off : nullptr;
       T* dx = static_cast<T*>(p.dx[st]) + off;
-      Raw ry{}, rx{};
-      if (live) ry = load_raw<T, D, kHalf>(dy, lane);
-      if (st == 2) {
-        if (live) store_raw<T, D, kHalf>(dx, lane, ry);
-        continue;
-      }
-      if (live) rx = load_raw<T, D, kHalf>(static_cast<const T*>(p.x[st]) + off, lane);
-      float x[NP], y[NP], gx[NP], gy[NP];
-      unpack<T, kHalf, NP>(rx, x, y);
-      unpack<T, kHalf, NP>(ry, gx, gy);
-      float ss = 0.f;
+      for (int h0 = h_beg; h0 < h_end; h0 += kBwdUnroll) {
+        Raw ry[kBwdUnroll], rx[kBwdUnroll];
 #pragma unroll
-      for (int j = 0; j < NP; ++j) ss += x[j] * x[j] + y[j] * y[j];
-      const float rstd = rsqrtf(row_sum<R::L>(ss) * (1.f / D) + p.eps);
-      float dot = 0.f;
+        for (int i = 0; i < kBwdUnroll; ++i) {
+          ry[i] = rx[i] = Raw{};
+          if (live && h0 + i < h_end) {
+            ry[i] = load_raw<T, D, kHalf>(dy + static_cast<long long>(h0 + i) * p.N * D, lane);
+            if (st < 2) rx[i] = load_raw<T, D, kHalf>(px + (h0 + i) * p.in.h, lane);
+          }
+        }
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const float cj = live ? c[j] : 0.f, sj = live ? s[j] : 0.f;
-        const float ga = gx[j] * cj + gy[j] * sj, gb = gy[j] * cj - gx[j] * sj;
-        x[j] *= rstd, y[j] *= rstd;  // normalised row
-        da[j] += ga * x[j], db[j] += gb * y[j];
-        gx[j] = ga * wa[j], gy[j] = gb * wb[j];
-        dot += gx[j] * x[j] + gy[j] * y[j];
-      }
-      dot = row_sum<R::L>(dot) * (1.f / D);
+        for (int i = 0; i < kBwdUnroll; ++i) {
+          if (st < 2) {
+            float x[NP], y[NP], gx[NP], gy[NP];
+            unpack<T, kHalf, NP>(rx[i], x, y);
+            unpack<T, kHalf, NP>(ry[i], gx, gy);
+            float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        gx[j] = rstd * (gx[j] - x[j] * dot);
-        gy[j] = rstd * (gy[j] - y[j] * dot);
+            for (int j = 0; j < NP; ++j) ss += x[j] * x[j] + y[j] * y[j];
+            const float rstd = rsqrtf(row_sum<R::L>(ss) * (1.f / D) + p.eps);
+            float dot = 0.f;
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              const float ga = gx[j] * c[j] + gy[j] * s[j], gb = gy[j] * c[j] - gx[j] * s[j];
+              x[j] *= rstd, y[j] *= rstd;  // normalised row
+              da[j] += ga * x[j], db[j] += gb * y[j];
+              gx[j] = ga * wa[j], gy[j] = gb * wb[j];
+              dot += gx[j] * x[j] + gy[j] * y[j];
+            }
+            dot = row_sum<R::L>(dot) * (1.f / D);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              gx[j] = rstd * (gx[j] - x[j] * dot);
+              gy[j] = rstd * (gy[j] - y[j] * dot);
+            }
+            ry[i] = pack<T, kHalf, NP>(gx, gy);
+          }
+          if (live && h0 + i < h_end) store_raw<T, D, kHalf>(dx + (h0 + i) * p.in.h, lane, ry[i]);
+        }
       }
-      if (live) store_raw<T, D, kHalf>(dx, lane, pack<T, kHalf, NP>(gx, gy));
     }
     if (st < 2 && p.dw[st] != nullptr) {
 #pragma unroll
@@ -361,11 +379,16 @@ cudaError_t launch_rotate(RotateParams p, int num_sms, cudaStream_t s) {
 }
 
 template <typename T, int D, bool kHalf>
-cudaError_t launch_bwd(const NormBwdParams& p, int num_sms, cudaStream_t s) {
+cudaError_t launch_bwd(NormBwdParams p, int num_sms, cudaStream_t s) {
   using R = Row<T, D>;
-  const long long units = static_cast<long long>((p.N + R::kTokens - 1) / R::kTokens) * p.B * p.H;
+  const long long tiles = static_cast<long long>((p.N + R::kTokens - 1) / R::kTokens) * p.B;
   long long blocks = 4ll * num_sms;
   if (blocks > kNormBwdMaxBlocks) blocks = kNormBwdMaxBlocks;
+  // few tokens: the heads are split until every block has a unit
+  long long chunks = (blocks + tiles - 1) / tiles;
+  if (chunks > p.H) chunks = p.H;
+  p.heads_per_unit = int((p.H + chunks - 1) / chunks);
+  const long long units = tiles * ((p.H + p.heads_per_unit - 1) / p.heads_per_unit);
   if (blocks > units) blocks = units;
   norm_bwd_kernel<T, D, kHalf><<<int(blocks), kThreads, 0, s>>>(p);
   note_launches(1);

@@ -64,6 +64,7 @@ struct NormBwdParams {
   const int32_t* pos;
   RopeGeom g;
   int B, H, N;
+  int heads_per_unit;      // set by the launcher
   uint32_t* status;
 };
 // Upper bound of the blocks (rows of `partial`) a backward launch uses.
