@@ -12,23 +12,68 @@ namespace mcs {
 // The gates of SiLU and of the tanh form of GELU are logistic functions, z /
 // (1 + exp(-t)): no cancellation for negative z, and exp overflowing to
 // infinity gives the right limit 0. GELU's erf form uses erfc for the same reason.
-__device__ __forceinline__ float activate(int act, float z) {
-  if (act == MCS_ACT_NONE) return z;
-  if (act == MCS_ACT_GELU_ERF) return 0.5f * z * erfcf(z * -0.70710678f);
-  // sqrt(8 / pi) = 1.5957691216
-  const float t = act == MCS_ACT_SILU ? z : 1.5957691216f * (z + 0.044715f * z * z * z);
-  return __fdividef(z, 1.f + __expf(-t));
+__device__ __forceinline__ float logistic_gate(float z, float t) { return __fdividef(z, 1.f + __expf(-t)); }
+template <int n>
+__device__ __forceinline__ void activate(int act, float (&v)[n]) {
+  if (act == MCS_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < n; ++i)  // sqrt(8 / pi) = 1.5957691216
+      v[i] = logistic_gate(v[i], 1.5957691216f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+  } else if (act == MCS_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = logistic_gate(v[i], v[i]);
+  } else if (act == MCS_ACT_GELU_ERF) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678f);
+  }
 }
 
 // One output element from its sum (any alignment).
 template <typename T>
 __device__ __forceinline__ void finish_one(const LinearParams& p, int m, int o, float acc) {
   if (p.bias) acc += to_f32(static_cast<const T*>(p.bias)[o]);
-  acc = activate(p.act, acc);
+  float v[1] = {acc};
+  activate(p.act, v);
+  acc = v[0];
   if (p.gate) acc *= to_f32(static_cast<const T*>(p.gate)[size_t(m / p.N) * p.O + o]);
   const size_t at = size_t(m) * p.O + o;
   if (p.residual) acc += to_f32(static_cast<const T*>(p.residual)[at]);
   static_cast<T*>(p.y)[at] = from_f32<T>(acc);
+}
+
+// Eight consecutive bf16 outputs of one row from their sums; bias8 and res8 hold
+// the bias and residual there (ignored where absent). Needs O % 8 == 0.
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void finish_eight(const LinearParams& p, int m, int o, float (&v)[8], const uint4& bias8,
+                                             const uint4& res8) {
+  float t[8];
+  if (p.bias) {
+    unpack8(bias8, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  activate(p.act, v);
+  if (p.gate) {
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.gate) + size_t(m / p.N) * p.O + o), t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= t[i];
+  }
+  if (p.residual) {
+    unpack8(res8, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + size_t(m) * p.O + o) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace mcs

@@ -69,6 +69,18 @@ __device__ __forceinline__ void tc_mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// D[tmem of both CTAs] (+)= A[smem of both] * B[smem of both]^T (cta_group::2): each
+// CTA holds half of A's rows and half of B's rows at the same shared-memory offsets.
+__device__ __forceinline__ void tc_mma_ss_lo_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                                  uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+
 // Warp-wide forms: every lane of the issuing warp executes the statement with
 // the same (warp-uniform) operands and only the lane with `issue` set issues the
 // MMA or the commit, so the operands can live in uniform registers.
