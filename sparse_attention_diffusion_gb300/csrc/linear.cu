@@ -11,7 +11,8 @@
 // tile's rows of w, so every operand byte in shared memory feeds two tensor
 // cores, which halves the shared-memory and L2 traffic of w against one-CTA
 // tiles. 384 threads:
-//   warp 0       TMA producer (both CTAs, each its own half), six 64-column stages
+//   warp 0       TMA producer (both CTAs, each its own half), six or more 64-column
+//                stages
 //   warp 1       MMA issuer (even CTA only, for both)
 //   warp 2       tensor-memory allocation
 //   warps 4-11   epilogue: 32 x 32 pieces of the accumulator through a swizzled
@@ -25,6 +26,8 @@
 #include "common.cuh"
 #include "linear.h"
 #include "linear_epi.cuh"
+#include "launch.cuh"
+#include "linear_few.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 #include "tma.cuh"
@@ -32,12 +35,12 @@
 namespace mcs {
 namespace {
 
-constexpr int kStages = 6;
+constexpr int kMaxStages = 9;
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kHalfTile = 128 * 128;  // bytes of 128 rows x 64 columns
-constexpr int kStageBytes = 2 * kHalfTile;
-constexpr int kPatchOff = kStages * kStageBytes;
+constexpr int kRing = 6 * 2 * kHalfTile;  // six stages of the widest tile, more of narrower ones
+constexpr int kPatchOff = kRing;
 constexpr int kPatch = 32 * 32 * 4;
 constexpr int kBarOff = kPatchOff + kEpiWarps * kPatch;
 constexpr int kSmemAlloc = kBarOff + 256 + 1024;
@@ -48,8 +51,9 @@ constexpr int kBand = 8;
 // 256 rows a section; columns in `cols` tiles of `bn` outputs.
 struct Tiling {
   int rows, tiles, sections;
-  int head_dim;  // 0: token-major
+  int col_mask, head_shift;  // column k of x is column k & col_mask of head k >> head_shift (token-major: one head)
   int bn, cols;
+  int stages, stage_bytes;
   int total;
 };
 struct Tile {
@@ -63,6 +67,17 @@ __device__ __forceinline__ Tile tile_at(const Tiling& t, int i) {
   return {rt / t.tiles, (rt % t.tiles) * 256, col * t.bn};
 }
 
+// Eight sums of a row of an epilogue patch (rows of 128 bytes, 16-byte pieces swizzled).
+__device__ __forceinline__ void patch_row(uint32_t patch, int row, int col, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
+                 : "r"(patch + row * 128 + (((col / 4 + h) ^ (row & 7)) << 4))
+                 : "memory");
+}
+
+template <int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const LinearParams p, const Tiling tl) {
@@ -70,18 +85,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // even CTA: both CTAs' copies of a stage landed
-  uint64_t* empty = full + kStages;                              // each CTA: the MMAs of a stage are done
-  uint64_t* acc_full = empty + kStages;                          // [2] each CTA: accumulator written
+  uint64_t* empty = full + kMaxStages;                              // each CTA: the MMAs of a stage are done
+  uint64_t* acc_full = empty + kMaxStages;                          // [2] each CTA: accumulator written
   uint64_t* acc_empty = acc_full + 2;                            // [2] even CTA: accumulator read by both CTAs
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = int(cluster_rank());
+  const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+  const int rank = blockIdx.x & 1;  // of the cluster {2, 1, 1}
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int nk = (p.K + 63) / 64;
   uint32_t* st = p.status;
+  if (tid == 32) {
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_w);
+  }
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    for (int s = 0; s < tl.stages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
     for (int b = 0; b < 2; ++b) mbar_init(acc_full + b, 1), mbar_init(acc_empty + b, 2 * kEpiWarps);
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -94,60 +113,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = warp_uniform(*tmem_slot);
+  grid_inputs_ready();
+  grid_let_next_start();
 
   if (warp == 0) {
-    if (lane == 0) {
-      const int bn2 = tl.bn / 2;
-      bool ok = true;
-      int u = 0;  // stage uses so far
-      for (int t = pair; t < tl.total && ok; t += pairs) {
-        const Tile ti = tile_at(tl, t);
-        for (int i = 0; i < nk; ++i, ++u) {
-          const int s = u % kStages;
-          if (!(ok = mbar_wait(empty + s, ((u / kStages) & 1) ^ 1, st))) break;
-          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * (kHalfTile + bn2 * 128));
-          const uint32_t bar = cluster_map(smem_u32(full + s), 0);
-          const int k = i * 64;
-          const int c = tl.head_dim ? k % tl.head_dim : k;
-          const int z = tl.head_dim ? ti.sec * p.heads + k / tl.head_dim : 0;
-          tma_load_3d_pair(sbase + s * kStageBytes, &map_x, c, ti.row0 + rank * 128, z, bar);
-          tma_load_3d_pair(sbase + s * kStageBytes + kHalfTile, &map_w, k, ti.o0 + rank * bn2, 0, bar);
+    const int bn2 = tl.bn / 2;
+    const uint32_t bytes = uint32_t(2 * (kHalfTile + bn2 * 128));
+    bool ok = true;
+    int s = 0;
+    uint32_t phase = 0;
+    for (int t = pair; t < tl.total && ok; t += pairs) {
+      const Tile ti = tile_at(tl, t);
+      const int xrow = ti.row0 + rank * 128, wrow = ti.o0 + rank * bn2, z0 = ti.sec * p.heads;
+      for (int i = 0; i < nk; ++i) {
+        if (!(ok = warp_all(mbar_wait(empty + s, phase ^ 1, st)))) break;
+        const int k = i * 64;
+        const uint32_t bar = cluster_map(smem_u32(full + s), 0);
+        const uint32_t dst = sbase + s * tl.stage_bytes;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+          tma_load_3d_pair(dst, &map_x, k & tl.col_mask, xrow, z0 + (k >> tl.head_shift), bar);
+          tma_load_3d_pair(dst + kHalfTile, &map_w, k, wrow, 0, bar);
         }
+        __syncwarp();
+        if (++s == tl.stages) s = 0, phase ^= 1;
       }
-      if (!ok) raise_status(st, kStatusTimeout);
-      // let the armed copies of both CTAs land before the pair can exit
-      if (rank == 0)
-        for (int v = u > kStages ? u - kStages : 0; v < u; ++v) mbar_drain(full + v % kStages, (v / kStages) & 1);
     }
+    if (!ok && lane == 0) raise_status(st, kStatusTimeout);
+    // let the armed copies of both CTAs land before the pair can exit: the stages from s on carry the
+    // ring's previous phase, those before s the current one (a stage never used has nothing to wait for)
+    if (rank == 0 && lane == 0 && !ok)
+      for (int v = 0; v < tl.stages; ++v) mbar_drain(full + v, v < s ? phase : phase ^ 1);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t idesc = idesc_bf16_f32(256, 0, 0, 0) | (uint32_t(tl.bn >> 3) << 17);
       bool ok = true, issued = false;
-      int u = 0, it = 0;
+      int s = 0, it = 0;
+      uint32_t phase = 0;
       for (int t = pair; t < tl.total && ok; t += pairs, ++it) {
         const int b = it & 1;
-        if (!(ok = mbar_wait(acc_empty + b, ((it >> 1) & 1) ^ 1, st))) break;
-        for (int i = 0; i < nk; ++i, ++u) {
-          const int s = u % kStages;
-          if (!(ok = mbar_wait(full + s, (u / kStages) & 1, st))) break;
+        if (!(ok = warp_all(mbar_wait(acc_empty + b, ((it >> 1) & 1) ^ 1, st)))) break;
+        for (int i = 0; i < nk; ++i) {
+          if (!(ok = warp_all(mbar_wait(full + s, phase, st)))) break;
           tc_fence_after();
           issued = true;
-          const uint32_t a = desc_lo_kmajor(sbase + s * kStageBytes);
-          const uint32_t w = desc_lo_kmajor(sbase + s * kStageBytes + kHalfTile);
+          const uint32_t a = desc_lo_kmajor(sbase + s * tl.stage_bytes);
+          const uint32_t w = desc_lo_kmajor(sbase + s * tl.stage_bytes + kHalfTile);
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma_ss_lo_pair(tmem + b * 256, a + kstep_kmajor(ks), w + kstep_kmajor(ks), idesc,
-                              (i > 0 || ks > 0) ? 1u : 0u);
-          tc_commit_pair(empty + s);
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ss_lo_pair(tmem + b * 256, a + kstep_kmajor(ks), w + kstep_kmajor(ks), idesc,
+                                (i > 0 || ks > 0) ? 1u : 0u);
+            tc_commit_pair(empty + s);
+            if (i == nk - 1) tc_commit_pair(acc_full + b);
+          }
+          __syncwarp();
+          if (++s == tl.stages) s = 0, phase ^= 1;
         }
-        if (ok) tc_commit_pair(acc_full + b);
       }
       if (!ok) {
-        raise_status(st, kStatusTimeout);
+        if (lane == 0) raise_status(st, kStatusTimeout);
         if (issued) {
-          tc_commit_pair(drain);
+          if (elect_one()) tc_commit_pair(drain);
+          __syncwarp();
           mbar_drain(drain, 0);
         }
       }
@@ -163,28 +193,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int it = 0;
     for (int t = pair; t < tl.total; t += pairs, ++it) {
       const int b = it & 1;
+      const Tile ti = tile_at(tl, t);
       ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st));
       if (!ok) break;
       tc_fence_after();
-      const Tile ti = tile_at(tl, t);
       const int n0 = ti.row0 + rank * 128 + quarter * 32;
       const int m0 = ti.sec * tl.rows + n0;
       const int nchunks = tl.bn / 32;
       if (half >= nchunks) {  // nothing of this accumulator for this warp
         tc_fence_before();
-        if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(acc_empty + b), 0));
+        if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
       }
       for (int cc = half; cc < nchunks; cc += 2) {
         const int o = ti.o0 + cc * 32 + pcol;
-        uint4 bias8{}, res8[4] = {};
-        if (vec && o < p.O) {
-          if (p.bias) bias8 = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bias) + o);
-          if (p.residual) {
+        const bool cols = vec && o < p.O, add = p.residual != nullptr;
+        const size_t at = size_t(m0 + prow) * p.O + o;  // this lane's first row; the others follow eight rows apart
+        float bias[8] = {};
+        uint4 res8[4] = {};
+        if (cols) {
+          if (p.bias) unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bias) + o), bias);
+          if (add) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (n0 + i * 8 + prow < tl.rows)
-                res8[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) +
-                                                          size_t(m0 + i * 8 + prow) * p.O + o);
+                res8[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + at +
+                                                          size_t(8 * i) * p.O);
           }
         }
         uint32_t r[32];
@@ -192,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (cc + 2 >= nchunks) {  // last read of this accumulator by this warp
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(acc_empty + b), 0));
+          if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -200,22 +233,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        "r"(r[4 * q]), "r"(r[4 * q + 1]), "r"(r[4 * q + 2]), "r"(r[4 * q + 3])
                        : "memory");
         __syncwarp();
+        if (vec) {
+          float v[4][8];  // all four row groups before the first store, so that their latencies overlap
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = i * 8 + prow;
-          float v[8];
+          for (int i = 0; i < 4; ++i) patch_row(patch, i * 8 + prow, pcol, v[i]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
-                         : "r"(patch + row * 128 + (((pcol / 4 + h) ^ (row & 7)) << 4))
-                         : "memory");
-          if (n0 + row < tl.rows) {
-            if (vec) {
-              if (o < p.O) finish_eight(p, m0 + row, o, v, bias8, res8[i]);
-            } else {
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + prow;
+            if (cols && n0 + row < tl.rows) {
+              const __nv_bfloat16* gate = nullptr;
+              if (p.gate) gate = static_cast<const __nv_bfloat16*>(p.gate) + size_t((m0 + row) / p.N) * p.O + o;
+              finish_eight<kAct>(v[i], bias, gate, add, res8[i], static_cast<__nv_bfloat16*>(p.y) + at + size_t(8 * i) * p.O);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + prow;
+            float v[8];
+            patch_row(patch, row, pcol, v);
+            if (n0 + row < tl.rows) {
+#pragma unroll
               for (int j = 0; j < 8; ++j)
-                if (o + j < p.O) finish_one<__nv_bfloat16>(p, m0 + row, o + j, v[j]);
+                if (o + j < p.O) finish_one<kAct, __nv_bfloat16>(p, m0 + row, o + j, v[j]);
             }
           }
         }
@@ -232,39 +272,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-cudaError_t launch_pair(const LinearParams& p, int num_sms, cudaStream_t s) {
+cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t s) {
   Tiling t{};
   CUtensorMap mx, mw;
   bool ok;
   if (p.heads > 0) {
-    t.head_dim = p.K / p.heads;
+    const int d = p.K / p.heads;
+    t.head_shift = d == 64 ? 6 : 7;
+    t.col_mask = d - 1;
     t.rows = p.N;
     t.sections = p.B;
-    ok = make_tile_map(&mx, p.x, uint64_t(p.B) * p.heads, p.N, t.head_dim, 128);
+    ok = make_tile_map(&mx, p.x, uint64_t(p.B) * p.heads, p.N, d, 128);
   } else {
+    t.head_shift = 31;
+    t.col_mask = INT32_MAX;
     t.rows = p.M;
     t.sections = 1;
     ok = make_tile_map(&mx, p.x, 1, p.M, p.K, 128);
   }
   t.tiles = (t.rows + 255) / 256;
-  t.cols = (p.O + 255) / 256;
-  t.bn = ((p.O + t.cols - 1) / t.cols + 31) / 32 * 32;  // equal column tiles, in steps of 32
+  t.bn = bn;
   t.cols = (p.O + t.bn - 1) / t.bn;
+  t.stage_bytes = kHalfTile + t.bn / 2 * 128;
+  t.stages = kRing / t.stage_bytes < kMaxStages ? kRing / t.stage_bytes : kMaxStages;
   const long long total = static_cast<long long>(t.tiles) * t.sections * t.cols;
   if (total > INT32_MAX - 1024) return cudaErrorInvalidValue;
   t.total = int(total);
   ok = ok && make_tile_map(&mw, p.w, 1, p.O, p.K, t.bn / 2);
   if (!ok) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-  if (e != cudaSuccess) return e;
   const int pairs = t.total < num_sms / 2 ? t.total : num_sms / 2;
-  linear_pair_kernel<<<2 * pairs, kThreads, kSmemAlloc, s>>>(mx, mw, p, t);
-  note_launches(1);
-  return cudaGetLastError();
+  auto launch = [&](auto kern) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kern, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, p, t);
+  };
+  switch (p.act) {
+    case MCS_ACT_GELU_TANH: return launch(linear_pair_kernel<MCS_ACT_GELU_TANH>);
+    case MCS_ACT_GELU_ERF: return launch(linear_pair_kernel<MCS_ACT_GELU_ERF>);
+    case MCS_ACT_SILU: return launch(linear_pair_kernel<MCS_ACT_SILU>);
+    default: return launch(linear_pair_kernel<MCS_ACT_NONE>);
+  }
 }
 
 }  // namespace
 
-cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) { return launch_pair(p, num_sms, s); }
+// Which kernel and tile a problem takes: the smallest estimated time, in SM
+// clocks, with constants from measured sweeps. A 64-column step of a tile costs
+// its MMAs (8,192 FLOP per clock and SM), its loads (62 bytes per clock and SM out
+// of L2) or a ring turn's latency (300), whichever is longest; tiles run in waves
+// over the SMs (or pairs); reading every operand once from HBM (23 bytes per clock
+// and SM) bounds everything; then come the start, the way out of the last tile (20
+// to 35 clocks a column or token) and the exchange between K slices.
+cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
+  const int nk = (p.K + 63) / 64;
+  const long long rows = p.heads > 0 ? p.N : p.M, sections = p.heads > 0 ? p.B : 1;
+  const double hbm = 2.0 * (double(p.M) * p.K + double(p.O) * p.K + double(p.M) * p.O * (p.residual ? 2 : 1)) /
+                     (23.0 * num_sms);
+  auto larger = [](double a, double b) { return a > b ? a : b; };
+  // the longer of two overlapping times, which slow each other down a little
+  auto overlap = [](double a, double b) { return a > b ? a + 0.25 * b : b + 0.25 * a; };
+  double best = 1e300;
+  int pair_bn = 256;
+  const long long row_tiles = (rows + 255) / 256 * sections;
+  for (int widest = 256, last = 0; widest >= 32; widest -= 32) {
+    const int cols = (p.O + widest - 1) / widest;
+    const int bn = ((p.O + cols - 1) / cols + 31) / 32 * 32;  // equal column tiles, in steps of 32
+    if (bn == last) continue;
+    last = bn;
+    const long long tiles = row_tiles * ((p.O + bn - 1) / bn), slots = num_sms / 2;
+    const double step = larger(300, larger(2.0 * bn, (16384 + 64.0 * bn) / 62));
+    const double cost = overlap(double((tiles + slots - 1) / slots) * nk * step, hbm) + 6200 + 28 * bn;
+    if (cost < best) best = cost, pair_bn = bn;
+  }
+  FewPlan few{};
+  const long long otiles = (p.O + 127) / 128;
+  for (int widest = 256, last = 0; widest >= 16 && rows <= 4096; widest -= widest > 64 ? 32 : 16) {
+    const long long tt = (rows + widest - 1) / widest;
+    const int bn = int((rows + tt - 1) / tt + 15) / 16 * 16;  // equal token tiles, in steps of 16
+    if (bn == last) continue;
+    last = bn;
+    const long long tiles = otiles * sections * ((rows + bn - 1) / bn);
+    const double step = larger(300, larger(2.0 * bn, (16384 + 128.0 * bn) / 62));
+    for (int splits = 1; splits <= 8 && splits <= nk; ++splits) {
+      const int slots = few_slots(splits, num_sms);
+      if (splits > 4 && tiles * splits > 64) break;  // clusters of more than four start late on a busy GPU
+      // each CTA's way out is exposed once a wave, unless two CTAs share an SM
+      const double waves = double((tiles * splits + slots - 1) / slots);
+      const double out = splits > 1 ? 3500 + 20 * bn : 35 * bn;
+      const double cost = overlap(waves * ((nk + splits - 1) / splits) * step, hbm) + 6000 +
+                          out * (few_two_per_sm(bn) ? 1.0 : waves);
+      if (cost < best) {
+        best = cost;
+        few.bn = bn;
+        few.splits = splits;
+      }
+    }
+  }
+  return few.bn > 0 ? linear_few(p, few, num_sms, s) : launch_pair(p, pair_bn, num_sms, s);
+}
 
 }  // namespace mcs

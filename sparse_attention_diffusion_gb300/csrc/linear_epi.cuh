@@ -13,27 +13,25 @@ namespace mcs {
 // (1 + exp(-t)): no cancellation for negative z, and exp overflowing to
 // infinity gives the right limit 0. GELU's erf form uses erfc for the same reason.
 __device__ __forceinline__ float logistic_gate(float z, float t) { return __fdividef(z, 1.f + __expf(-t)); }
-template <int n>
-__device__ __forceinline__ void activate(int act, float (&v)[n]) {
-  if (act == MCS_ACT_GELU_TANH) {
+template <int kAct, int n>
+__device__ __forceinline__ void activate(float (&v)[n]) {
 #pragma unroll
-    for (int i = 0; i < n; ++i)  // sqrt(8 / pi) = 1.5957691216
+  for (int i = 0; i < n; ++i) {
+    if constexpr (kAct == MCS_ACT_GELU_TANH)  // sqrt(8 / pi) = 1.5957691216
       v[i] = logistic_gate(v[i], 1.5957691216f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
-  } else if (act == MCS_ACT_SILU) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = logistic_gate(v[i], v[i]);
-  } else if (act == MCS_ACT_GELU_ERF) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678f);
+    else if constexpr (kAct == MCS_ACT_SILU)
+      v[i] = logistic_gate(v[i], v[i]);
+    else if constexpr (kAct == MCS_ACT_GELU_ERF)
+      v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678f);
   }
 }
 
 // One output element from its sum (any alignment).
-template <typename T>
+template <int kAct, typename T>
 __device__ __forceinline__ void finish_one(const LinearParams& p, int m, int o, float acc) {
   if (p.bias) acc += to_f32(static_cast<const T*>(p.bias)[o]);
   float v[1] = {acc};
-  activate(p.act, v);
+  activate<kAct>(v);
   acc = v[0];
   if (p.gate) acc *= to_f32(static_cast<const T*>(p.gate)[size_t(m / p.N) * p.O + o]);
   const size_t at = size_t(m) * p.O + o;
@@ -41,28 +39,27 @@ __device__ __forceinline__ void finish_one(const LinearParams& p, int m, int o, 
   static_cast<T*>(p.y)[at] = from_f32<T>(acc);
 }
 
-// Eight consecutive bf16 outputs of one row from their sums; bias8 and res8 hold
-// the bias and residual there (ignored where absent). Needs O % 8 == 0.
+// Eight bf16 values of a 16-byte word.
 __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
 }
-__device__ __forceinline__ void finish_eight(const LinearParams& p, int m, int o, float (&v)[8], const uint4& bias8,
-                                             const uint4& res8) {
+// Eight consecutive bf16 outputs of one row from their sums: bias (0 where
+// absent), gate words and residual words where the pointers say so, stored at y.
+template <int kAct>
+__device__ __forceinline__ void finish_eight(float (&v)[8], const float (&bias)[8], const __nv_bfloat16* gate, bool add,
+                                             const uint4& res8, __nv_bfloat16* y) {
   float t[8];
-  if (p.bias) {
-    unpack8(bias8, t);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
-  }
-  activate(p.act, v);
-  if (p.gate) {
-    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.gate) + size_t(m / p.N) * p.O + o), t);
+  for (int i = 0; i < 8; ++i) v[i] += bias[i];
+  activate<kAct>(v);
+  if (gate != nullptr) {
+    unpack8(*reinterpret_cast<const uint4*>(gate), t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= t[i];
   }
-  if (p.residual) {
+  if (add) {
     unpack8(res8, t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += t[i];
@@ -73,7 +70,38 @@ __device__ __forceinline__ void finish_eight(const LinearParams& p, int m, int o
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + size_t(m) * p.O + o) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Four consecutive bf16 outputs of one row from their sums; bias4 holds the bias
+// there (ignored where absent). Needs O % 4 == 0.
+__device__ __forceinline__ void unpack4(const uint2& w, float (&v)[4]) {
+  v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+  v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+template <int kAct>
+__device__ __forceinline__ void finish_four(const LinearParams& p, int m, int o, float (&v)[4], const uint2& bias4) {
+  float t[4];
+  const size_t at = size_t(m) * p.O + o;
+  if (p.bias) {
+    unpack4(bias4, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += t[i];
+  }
+  activate<kAct>(v);
+  if (p.gate) {
+    unpack4(*reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.gate) + size_t(m / p.N) * p.O + o), t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= t[i];
+  }
+  if (p.residual) {
+    unpack4(*reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + at), t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += t[i];
+  }
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 }  // namespace mcs

@@ -1,0 +1,287 @@
+// bf16 matrix product with epilogue for few rows of x (a step's modulation
+// vectors, a short text): reading w once is the bound, and the output tiles alone
+// do not fill the GPU. The operands are exchanged, so that the 128 lanes of the
+// tensor core take 128 rows of w (outputs) and the rows of x (tokens, 16 to 256
+// of them) are the MMA's N; K is cut into S slices, one per CTA of a cluster.
+// Each CTA streams its slice of w through a ring of TMA stages into an fp32
+// accumulator [128 outputs x tokens] in tensor memory and leaves it in its shared
+// memory; after a cluster barrier every CTA sums a share of the tokens over the S
+// partial accumulators (distributed shared memory, ranks in order, so that equal
+// calls give equal bits) and applies the epilogue. No workspace, one launch.
+// 192 threads: warp 0 TMA producer, warp 1 MMA issuer and tensor-memory
+// allocation, warps 2-5 the accumulator's way out; all six the final sum.
+#include "attn_tc.h"
+#include "common.cuh"
+#include "linear.h"
+#include "linear_epi.cuh"
+#include "launch.cuh"
+#include "linear_few.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+#include "tma.cuh"
+
+namespace mcs {
+namespace {
+
+constexpr int kThreads = 192, kWarps = kThreads / 32;
+constexpr int kWTile = 128 * 128;  // bytes of 128 rows of w x 64 columns
+constexpr int kBarBytes = 256;     // barriers and the tensor-memory slot, after the ring
+constexpr int kMaxStages = 12;
+
+struct FewArgs {
+  int rows, tiles, sections;  // rows of a section of x, its token tiles
+  int col_mask, head_shift;   // column k of x is column k & col_mask of head k >> head_shift (token-major: one head)
+  int bn, stages, splits;
+  uint32_t tmem_cols;
+};
+
+// A 32-bit word of shared memory as the CTA of rank r holds it.
+__device__ __forceinline__ uint32_t peer_word(uint32_t addr, int r, int splits) {
+  uint32_t v;
+  if (splits == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  else asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_map(addr, r)) : "memory");
+  return v;
+}
+
+// This CTA's share of the outputs: tokens rank, rank + splits, ... over its warps,
+// kTok of them and kRanks partial accumulators at a time, ranks added in order.
+template <int kAct, int kTok, int kRanks>
+__device__ __forceinline__ void final_sums(const LinearParams& p, const FewArgs& a, uint32_t sbase, int rank, int warp,
+                                           int lane, int m0, int ntok, int o0) {
+  const int o = o0 + lane * 4;
+  const bool vec = p.O % 4 == 0;
+  uint2 bias4{};
+  if (vec && p.bias && o < p.O) bias4 = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.bias) + o);
+  const int stride = a.splits * kWarps;
+  for (int c0 = rank + a.splits * warp; c0 < ntok; c0 += kTok * stride) {
+    float v[kTok][4] = {};
+    for (int r0 = 0; r0 < a.splits; r0 += kRanks) {
+      float f[kTok][kRanks][4];
+#pragma unroll
+      for (int t = 0; t < kTok; ++t)
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r) {
+          f[t][r][0] = f[t][r][1] = f[t][r][2] = f[t][r][3] = 0.f;
+          if (c0 + t * stride >= ntok || r0 + r >= a.splits) continue;
+          const uint32_t at = sbase + uint32_t((c0 + t * stride) * 128 + lane * 4) * 4;
+          if constexpr (kRanks == 1)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(f[t][r][0]), "=f"(f[t][r][1]), "=f"(f[t][r][2]), "=f"(f[t][r][3])
+                         : "r"(at));
+          else
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(f[t][r][0]), "=f"(f[t][r][1]), "=f"(f[t][r][2]), "=f"(f[t][r][3])
+                         : "r"(cluster_map(at, r0 + r)));
+        }
+#pragma unroll
+      for (int t = 0; t < kTok; ++t)
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r)  // those past the cluster add zero
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[t][i] += f[t][r][i];
+    }
+#pragma unroll
+    for (int t = 0; t < kTok; ++t) {
+      const int c = c0 + t * stride;
+      if (c >= ntok) break;
+      if (vec) {
+        if (o < p.O) finish_four<kAct>(p, m0 + c, o, v[t], bias4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (o + i < p.O) finish_one<kAct, __nv_bfloat16>(p, m0 + c, o + i, v[t][i]);
+      }
+    }
+  }
+}
+
+template <int kAct>
+__global__ void __launch_bounds__(kThreads)
+    linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                      const LinearParams p, const FewArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int stage_bytes = kWTile + a.bn * 128;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.stages * stage_bytes);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* done = empty + kMaxStages;
+  uint64_t* drain = done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile uint32_t* failed = tmem_slot + 1;  // a wait of this CTA ran out
+  const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+  const int tt = blockIdx.x / a.splits, rank = blockIdx.x % a.splits;  // of the cluster {splits, 1, 1}
+  const int sec = tt / a.tiles, tok0 = (tt % a.tiles) * a.bn, o0 = blockIdx.y * 128;
+  const int nk = (p.K + 63) / 64;
+  const int k_beg = int(static_cast<long long>(nk) * rank / a.splits);
+  const int k_end = int(static_cast<long long>(nk) * (rank + 1) / a.splits);
+  uint32_t* st = p.status;
+  if (tid == 64) {
+    tma_prefetch_map(&map_w);
+    tma_prefetch_map(&map_x);
+  }
+  if (tid == 0) {
+    for (int s = 0; s < a.stages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    mbar_init(done, 1);
+    mbar_init(drain, 1);
+    *failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, a.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = warp_uniform(*tmem_slot);
+  grid_inputs_ready();
+  grid_let_next_start();
+
+  bool ok = true;
+  if (warp == 0) {
+    int s = 0;
+    uint32_t phase = 0;
+    const int z0 = sec * p.heads;
+    for (int i = k_beg; i < k_end; ++i) {
+      if (!(ok = warp_all(mbar_wait(empty + s, phase ^ 1, st)))) break;
+      const int k = i * 64;
+      const uint32_t dst = sbase + s * stage_bytes;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full + s, stage_bytes);
+        tma_load_3d(dst, &map_w, k, o0, 0, smem_u32(full + s));
+        tma_load_3d(dst + kWTile, &map_x, k & a.col_mask, tok0, z0 + (k >> a.head_shift), smem_u32(full + s));
+      }
+      __syncwarp();
+      if (++s == a.stages) s = 0, phase ^= 1;
+    }
+    if (!ok && lane == 0) {
+      *failed = 1;
+      raise_status(st, kStatusTimeout);
+      // let the armed copies land: stages from s on carry the ring's previous phase
+      for (int v = 0; v < a.stages; ++v) mbar_drain(full + v, v < s ? phase : phase ^ 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_bf16_f32(128, 0, 0, 0) | (uint32_t(a.bn >> 3) << 17);
+    bool issued = false;
+    int s = 0;
+    uint32_t phase = 0;
+    for (int i = k_beg; i < k_end; ++i) {
+      if (!(ok = warp_all(mbar_wait(full + s, phase, st)))) break;
+      tc_fence_after();
+      issued = true;
+      const uint32_t w = desc_lo_kmajor(sbase + s * stage_bytes);
+      const uint32_t x = desc_lo_kmajor(sbase + s * stage_bytes + kWTile);
+      if (elect_one()) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma_ss_lo(tmem, w + kstep_kmajor(ks), x + kstep_kmajor(ks), idesc, (i > k_beg || ks > 0) ? 1u : 0u);
+        tc_commit(empty + s);
+        if (i == k_end - 1) tc_commit(done);
+      }
+      __syncwarp();
+      if (++s == a.stages) s = 0, phase ^= 1;
+    }
+    if (!ok) {
+      if (lane == 0) {
+        *failed = 1;
+        raise_status(st, kStatusTimeout);
+      }
+      if (issued) {
+        if (elect_one()) tc_commit(drain);
+        __syncwarp();
+        mbar_drain(drain, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    // every MMA has read its stages when `done` completes, so the ring is free
+    ok = warp_all(mbar_wait(done, 0, st));
+    tc_fence_after();
+    if (ok) {
+      const int quarter = warp & 3;
+      float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+      for (int c = 0; c < a.bn; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + (uint32_t(quarter * 32) << 16) + c, r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < a.bn) part[(c + i) * 128] = __uint_as_float(r[i]);
+      }
+    } else if (lane == 0) {
+      *failed = 1;
+      raise_status(st, kStatusTimeout);
+    }
+  }
+  tc_fence_before();
+  // partial accumulators complete in every CTA of the cluster (all threads of all of them come here)
+  if (a.splits > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, a.tmem_cols);
+  }
+  // sums with a failed CTA's share are not written anywhere
+  ok = true;
+  for (int r = 0; r < a.splits; ++r) ok = ok && peer_word(smem_u32(tmem_slot + 1), r, a.splits) == 0;
+  const int ntok = min(a.bn, a.rows - tok0);
+  // several reads in flight: a remote one takes several hundred clocks
+  if (ok) {
+    if (a.splits == 1) final_sums<kAct, 4, 1>(p, a, sbase, rank, warp, lane, sec * a.rows + tok0, ntok, o0);
+    else final_sums<kAct, 2, 4>(p, a, sbase, rank, warp, lane, sec * a.rows + tok0, ntok, o0);
+  }
+  if (a.splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
+}
+
+}  // namespace
+
+cudaError_t linear_few(const LinearParams& p, const FewPlan& plan, int num_sms, cudaStream_t s) {
+  FewArgs a{};
+  CUtensorMap mx, mw;
+  bool ok;
+  if (p.heads > 0) {
+    const int d = p.K / p.heads;
+    a.head_shift = d == 64 ? 6 : 7;
+    a.col_mask = d - 1;
+    a.rows = p.N;
+    a.sections = p.B;
+    ok = make_tile_map(&mx, p.x, uint64_t(p.B) * p.heads, p.N, d, plan.bn);
+  } else {
+    a.head_shift = 31;
+    a.col_mask = INT32_MAX;
+    a.rows = p.M;
+    a.sections = 1;
+    ok = make_tile_map(&mx, p.x, 1, p.M, p.K, plan.bn);
+  }
+  ok = ok && make_tile_map(&mw, p.w, 1, p.O, p.K, 128);
+  if (!ok) return cudaErrorInvalidValue;
+  a.bn = plan.bn;
+  a.splits = plan.splits;
+  a.tiles = (a.rows + a.bn - 1) / a.bn;
+  a.tmem_cols = 32;
+  while (int(a.tmem_cols) < a.bn) a.tmem_cols *= 2;
+  // the ring takes an SM's shared memory when every CTA has an SM to itself, half of it otherwise; it ends
+  // up holding the partial accumulator
+  const int stage = kWTile + a.bn * 128;
+  const long long ctas = static_cast<long long>(a.splits) * a.tiles * a.sections * ((p.O + 127) / 128);
+  const bool half = ctas > few_slots(a.splits, num_sms) && few_two_per_sm(a.bn);
+  a.stages = (half ? kFewHalfSm : 226 * 1024 - kBarBytes - 1024) / stage;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  const size_t smem = size_t(a.stages) * stage + kBarBytes + 1024;
+  const dim3 grid(unsigned(a.splits) * a.tiles * a.sections, (p.O + 127) / 128);
+  auto launch = [&](auto kern) {
+    // one value for every call: threads launching other plans at the same time share the attribute
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kern, grid, kThreads, smem, s, unsigned(a.splits), mx, mw, p, a);
+  };
+  switch (p.act) {
+    case MCS_ACT_GELU_TANH: return launch(linear_few_kernel<MCS_ACT_GELU_TANH>);
+    case MCS_ACT_GELU_ERF: return launch(linear_few_kernel<MCS_ACT_GELU_ERF>);
+    case MCS_ACT_SILU: return launch(linear_few_kernel<MCS_ACT_SILU>);
+    default: return launch(linear_few_kernel<MCS_ACT_NONE>);
+  }
+}
+
+}  // namespace mcs

@@ -1,0 +1,27 @@
+// Host-side interface of the few-rows matrix product.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "linear.h"
+
+namespace mcs {
+
+struct FewPlan {
+  int bn;      // tokens per tile: a multiple of 16, 16 .. 256
+  int splits;  // K slices = CTAs of a cluster, 1 .. 8
+};
+// CTAs that run at once, one per SM: clusters of more than two leave SMs of a GPU
+// processing cluster over (144 CTAs in clusters of three took two waves on 152 SMs).
+inline int few_slots(int splits, int num_sms) {
+  return splits <= 2 ? num_sms : int(0.85 * num_sms) / splits * splits;
+}
+// Half of an SM's shared memory holds three stages (16 KB of w and bn x 128 bytes of x
+// each) and the bn x 512 bytes of the partial accumulator.
+constexpr int kFewHalfSm = 112 * 1024 - 1280;
+inline bool few_two_per_sm(int bn) {
+  const int stage = 16384 + bn * 128;
+  return kFewHalfSm / stage >= 3 && kFewHalfSm / stage * stage >= bn * 512;
+}
+cudaError_t linear_few(const LinearParams& p, const FewPlan& plan, int num_sms, cudaStream_t s);
+
+}  // namespace mcs

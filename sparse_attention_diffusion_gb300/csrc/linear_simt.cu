@@ -1,5 +1,6 @@
 // fp32 matrix product with epilogue in SIMT arithmetic: 64 x 64 output tiles,
 // K in steps of 16 through shared memory, 4 x 4 outputs per thread.
+#include "launch.cuh"
 #include "linear.h"
 #include "linear_epi.cuh"
 
@@ -16,11 +17,14 @@ __device__ __forceinline__ const float* x_at(const LinearParams& p, int m, int k
   return x + ((size_t(b) * p.heads + k / d) * p.N + n) * d + k % d;
 }
 
+template <int kAct>
 __global__ void __launch_bounds__(256) linear_simt_kernel(const LinearParams p) {
   __shared__ float xs[kBK][kT + 4], wsm[kBK][kT + 4];
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
   const int m0 = blockIdx.x * kT, o0 = blockIdx.y * kT;
   const int lr = tid / 4, lk = (tid % 4) * 4;  // this thread's row and first k of the loads
+  grid_inputs_ready();
+  grid_let_next_start();
   float acc[4][4] = {};
   for (int k0 = 0; k0 < p.K; k0 += kBK) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
@@ -49,7 +53,7 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(const LinearParams p) 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int m = m0 + ty * 4 + i, o = o0 + tx * 4 + j;
-      if (m < p.M && o < p.O) finish_one<float>(p, m, o, acc[i][j]);
+      if (m < p.M && o < p.O) finish_one<kAct, float>(p, m, o, acc[i][j]);
     }
 }
 
@@ -58,9 +62,12 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(const LinearParams p) 
 cudaError_t linear_simt(const LinearParams& p, int num_sms, cudaStream_t s) {
   (void)num_sms;
   const dim3 grid((p.M + kT - 1) / kT, (p.O + kT - 1) / kT);
-  linear_simt_kernel<<<grid, 256, 0, s>>>(p);
-  note_launches(1);
-  return cudaGetLastError();
+  switch (p.act) {
+    case MCS_ACT_GELU_TANH: return launch_overlapped(linear_simt_kernel<MCS_ACT_GELU_TANH>, grid, 256, 0, s, 0, p);
+    case MCS_ACT_GELU_ERF: return launch_overlapped(linear_simt_kernel<MCS_ACT_GELU_ERF>, grid, 256, 0, s, 0, p);
+    case MCS_ACT_SILU: return launch_overlapped(linear_simt_kernel<MCS_ACT_SILU>, grid, 256, 0, s, 0, p);
+    default: return launch_overlapped(linear_simt_kernel<MCS_ACT_NONE>, grid, 256, 0, s, 0, p);
+  }
 }
 
 }  // namespace mcs

@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "status.cuh"
 
 namespace mcs {
@@ -191,6 +192,8 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) 
   const int h_beg = blockIdx.y * p.heads_per_block, h_end = min(p.H, h_beg + p.heads_per_block);
   float c[NP], s[NP];
   bool live = n < p.N;
+  grid_inputs_ready();
+  grid_let_next_start();
   if (live && !load_angles<NP>(p.g, p.table, p.pos, b, p.N, n, lane, c, s)) {
     live = false;
     raise_status(p.status, kStatusBounds);
@@ -261,6 +264,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdParams 
   const int tiles = (p.N + R::kTokens - 1) / R::kTokens;
   const int chunks = (p.H + p.heads_per_unit - 1) / p.heads_per_unit;
   const long long units = static_cast<long long>(tiles) * p.B * chunks;
+  grid_inputs_ready();
+  grid_let_next_start();
 #pragma unroll 1
   for (int st = 0; st < 3; ++st) {
     if (p.dy[st] == nullptr) continue;
@@ -351,6 +356,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float* part
   __shared__ float red[1024];
   const int st = blockIdx.x, e = threadIdx.x % D, part = threadIdx.x / D, parts = blockDim.x / D;
   float* dw = st == 0 ? dwq : dwk;
+  grid_inputs_ready();
+  grid_let_next_start();
   if (dw == nullptr) return;
   float v = 0.f;
   for (int i = part; i < nblk; i += parts) v += partial[(size_t(i) * 2 + st) * D + e];
@@ -373,9 +380,7 @@ cudaError_t launch_rotate(RotateParams p, int num_sms, cudaStream_t s) {
   if (chunks > p.H) chunks = p.H;
   p.heads_per_block = int((p.H + chunks - 1) / chunks);
   const dim3 grid(tiles, (p.H + p.heads_per_block - 1) / p.heads_per_block, p.B);
-  rotate_kernel<T, D, kHalf, kNorm><<<grid, kThreads, 0, s>>>(p);
-  note_launches(1);
-  return cudaGetLastError();
+  return launch_overlapped(rotate_kernel<T, D, kHalf, kNorm>, grid, kThreads, 0, s, 0, p);
 }
 
 template <typename T, int D, bool kHalf>
@@ -390,13 +395,9 @@ cudaError_t launch_bwd(NormBwdParams p, int num_sms, cudaStream_t s) {
   p.heads_per_unit = int((p.H + chunks - 1) / chunks);
   const long long units = tiles * ((p.H + p.heads_per_unit - 1) / p.heads_per_unit);
   if (blocks > units) blocks = units;
-  norm_bwd_kernel<T, D, kHalf><<<int(blocks), kThreads, 0, s>>>(p);
-  note_launches(1);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_overlapped(norm_bwd_kernel<T, D, kHalf>, dim3(unsigned(blocks)), kThreads, 0, s, 0, p);
   if (e != cudaSuccess || (p.dw[0] == nullptr && p.dw[1] == nullptr)) return e;
-  norm_bwd_reduce_kernel<<<2, 1024, 0, s>>>(p.partial, int(blocks), D, p.dw[0], p.dw[1]);
-  note_launches(1);
-  return cudaGetLastError();
+  return launch_overlapped(norm_bwd_reduce_kernel, dim3(2), 1024, 0, s, 0, p.partial, int(blocks), D, p.dw[0], p.dw[1]);
 }
 
 template <typename T, int D>
