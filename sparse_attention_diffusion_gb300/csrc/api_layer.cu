@@ -30,6 +30,7 @@ mcs_status check_rope(const mcs_rope* r, mcs::RopeGeom* g, long long* entries) {
     if (!std::isfinite(r->start[a]) || !std::isfinite(r->scale[a])) return MCS_ERR_INVALID_ARG;
     g->pairs[a] = r->dims[a] / 2;
     g->len[a] = r->len[a];
+    g->by[a] = mcs::Divisor(r->len[a]);
     g->toff[a] = int(off);
     g->npairs += g->pairs[a];
     off += static_cast<long long>(r->len[a]) * g->pairs[a];

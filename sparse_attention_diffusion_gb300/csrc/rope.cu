@@ -19,6 +19,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "ptx.cuh"
 #include "status.cuh"
 
 namespace mcs {
@@ -116,6 +117,22 @@ __device__ __forceinline__ Raw pack(const float (&a)[NP], const float (&b)[NP]) 
   return r;
 }
 
+// The same with two pairs per 64-bit register: (a[2i], a[2i + 1]), (b[2i], b[2i + 1]).
+template <typename T, bool kHalf, int N2>
+__device__ __forceinline__ void unpack2(const Raw& r, uint64_t (&a)[N2], uint64_t (&b)[N2]) {
+  float x[2 * N2], y[2 * N2];
+  unpack<T, kHalf, 2 * N2>(r, x, y);
+#pragma unroll
+  for (int i = 0; i < N2; ++i) a[i] = f2_pack(x[2 * i], x[2 * i + 1]), b[i] = f2_pack(y[2 * i], y[2 * i + 1]);
+}
+template <typename T, bool kHalf, int N2>
+__device__ __forceinline__ Raw pack2(const uint64_t (&a)[N2], const uint64_t (&b)[N2]) {
+  float x[2 * N2], y[2 * N2];
+#pragma unroll
+  for (int i = 0; i < N2; ++i) f2_unpack(a[i], x[2 * i], x[2 * i + 1]), f2_unpack(b[i], y[2 * i], y[2 * i + 1]);
+  return pack<T, kHalf, 2 * N2>(x, y);
+}
+
 // Cosines and sines of the pairs lane * NP .. + NP - 1 of token n of batch b.
 // Returns false when a listed position is out of range (nothing is read then).
 template <int NP>
@@ -132,11 +149,14 @@ __device__ __forceinline__ bool load_angles(const RopeGeom& g, const float2* tab
   } else {
     int i = n - g.first;
     turns = i >= 0 && i < g.ngrid;
-    for (int a = g.axes - 1; a > 0; --a) {
-      p[a] = i % g.len[a];
-      i /= g.len[a];
+    if (turns) {
+      for (int a = g.axes - 1; a > 0; --a) {
+        const int q = g.by[a].div(i);
+        p[a] = i - q * g.len[a];
+        i = q;
+      }
+      p[0] = i;
     }
-    p[0] = i;
   }
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
@@ -248,35 +268,55 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) 
   }
 }
 
-// Gradient of norm + rotation. Blocks walk over (batch, token tile, head chunk)
-// units, the heads of a unit with the token's angles in registers; a lane's share
-// of dw (its own pairs, all its tokens and heads) stays in registers, is summed
+// Gradient of norm + rotation. The work is a list of units, a unit being one
+// stream's (q, k or the copy of v) heads_per_unit heads of one token tile, with
+// the tokens' angles in registers; blocks take every gridDim.x-th unit, stream
+// after stream. A lane's share of dw (its own pairs, all its tokens and heads)
+// stays in registers until the block's units of that stream are done, is summed
 // over the block's rows through shared memory, and goes to partial[block];
 // norm_bwd_reduce_kernel adds the blocks in order.
-constexpr int kBwdUnroll = 2;
+//
+// With g = R^T dy and t = g * x, the sums over the row are ss = sum x^2 and
+// dot = sum w t, taken together; then dw += rstd t and
+// dx = rstd (g w) - (rstd^3 dot / d) x. Instructions bound this (two row sums and
+// the conversions beside 48 bytes a lane), so pairs of pairs go through packed
+// fp32 operations.
+// Heads in flight per lane, at three blocks an SM (480p layer, 12 heads of 128: two
+// heads 165 us, three 149, four 144; as halves, whose rows are two loads, three 150,
+// four 179; four blocks of two heads 168, two blocks of four 158).
+template <bool kHalf>
+constexpr int kBwdUnroll = kHalf ? 3 : 4;
+constexpr int kBwdBlocksPerSm = 3;
 
 template <typename T, int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_bwd_kernel(const NormBwdParams p) {
   using R = Row<T, D>;
-  constexpr int NP = R::NP;
+  constexpr int NP = R::NP, U = kBwdUnroll<kHalf>;
   __shared__ float red[R::kTokens][D];
   const int lane = threadIdx.x % R::L, row = threadIdx.x / R::L;
   const int tiles = (p.N + R::kTokens - 1) / R::kTokens;
   const int chunks = (p.H + p.heads_per_unit - 1) / p.heads_per_unit;
-  const long long units = static_cast<long long>(tiles) * p.B * chunks;
+  const int units = tiles * p.B * chunks;  // of a stream; fewer than 2^31 rows
+  int u = blockIdx.x;                      // counted from the current stream's first unit
   grid_inputs_ready();
   grid_let_next_start();
 #pragma unroll 1
   for (int st = 0; st < 3; ++st) {
     if (p.dy[st] == nullptr) continue;
-    float da[NP], db[NP], wa[NP], wb[NP];
+    constexpr int N2 = NP / 2;
+    uint64_t da[N2], db[N2], wa[N2], wb[N2];  // two pairs each
+    {
+      float a[NP], b[NP];
+      load_weights<T, D, kHalf, NP>(st < 2 ? p.w[st] : nullptr, lane, a, b);
 #pragma unroll
-    for (int j = 0; j < NP; ++j) da[j] = db[j] = 0.f;
-    if (st < 2) load_weights<T, D, kHalf, NP>(p.w[st], lane, wa, wb);
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-      const long long bt = u / chunks;
-      const int b = int(bt / tiles), n = int(bt % tiles) * R::kTokens + row;
-      const int h_beg = int(u % chunks) * p.heads_per_unit, h_end = min(p.H, h_beg + p.heads_per_unit);
+      for (int j = 0; j < N2; ++j) {
+        wa[j] = f2_pack(a[2 * j], a[2 * j + 1]), wb[j] = f2_pack(b[2 * j], b[2 * j + 1]);
+        da[j] = db[j] = f2_pack(0.f, 0.f);
+      }
+    }
+    for (; u < units; u += gridDim.x) {
+      const int bt = p.by_chunks.div(u), b = p.by_tiles.div(bt), n = (bt - b * tiles) * R::kTokens + row;
+      const int h_beg = (u - bt * chunks) * p.heads_per_unit, h_end = min(p.H, h_beg + p.heads_per_unit);
       float c[NP], s[NP];
       bool live = n < p.N;
       if (live && !load_angles<NP>(p.g, p.table, p.pos, b, p.N, n, lane, c, s)) {
@@ -287,14 +327,20 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdParams 
 #pragma unroll
         for (int j = 0; j < NP; ++j) c[j] = s[j] = 0.f;
       }
+      uint64_t c2[N2], s2[N2], n2[N2];
+#pragma unroll
+      for (int j = 0; j < N2; ++j) {
+        c2[j] = f2_pack(c[2 * j], c[2 * j + 1]), s2[j] = f2_pack(s[2 * j], s[2 * j + 1]);
+        n2[j] = f2_pack(-s[2 * j], -s[2 * j + 1]);
+      }
       const long long off = b * p.in.b + n * p.in.n;
       const T* dy = static_cast<const T*>(p.dy[st]) + (static_cast<long long>(b) * p.H * p.N + n) * D;
       const T* px = st < 2 ? static_cast<const T*>(p.x[st]) + off : nullptr;
       T* dx = static_cast<T*>(p.dx[st]) + off;
-      for (int h0 = h_beg; h0 < h_end; h0 += kBwdUnroll) {
-        Raw ry[kBwdUnroll], rx[kBwdUnroll];
+      for (int h0 = h_beg; h0 < h_end; h0 += U) {
+        Raw ry[U], rx[U];
 #pragma unroll
-        for (int i = 0; i < kBwdUnroll; ++i) {
+        for (int i = 0; i < U; ++i) {
           ry[i] = rx[i] = Raw{};
           if (live && h0 + i < h_end) {
             ry[i] = load_raw<T, D, kHalf>(dy + static_cast<long long>(h0 + i) * p.N * D, lane);
@@ -302,42 +348,54 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdParams 
           }
         }
 #pragma unroll
-        for (int i = 0; i < kBwdUnroll; ++i) {
+        for (int i = 0; i < U; ++i) {
           if (st < 2) {
-            float x[NP], y[NP], gx[NP], gy[NP];
-            unpack<T, kHalf, NP>(rx[i], x, y);
-            unpack<T, kHalf, NP>(ry[i], gx, gy);
-            float ss = 0.f;
+            uint64_t x[N2], y[N2], ga[N2], gb[N2];
+            unpack2<T, kHalf, N2>(rx[i], x, y);
+            unpack2<T, kHalf, N2>(ry[i], ga, gb);
+            uint64_t ss = f2_pack(0.f, 0.f), dot = ss, ta[N2], tb[N2];
 #pragma unroll
-            for (int j = 0; j < NP; ++j) ss += x[j] * x[j] + y[j] * y[j];
-            const float rstd = rsqrtf(row_sum<R::L>(ss) * (1.f / D) + p.eps);
-            float dot = 0.f;
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-              const float ga = gx[j] * c[j] + gy[j] * s[j], gb = gy[j] * c[j] - gx[j] * s[j];
-              x[j] *= rstd, y[j] *= rstd;  // normalised row
-              da[j] += ga * x[j], db[j] += gb * y[j];
-              gx[j] = ga * wa[j], gy[j] = gb * wb[j];
-              dot += gx[j] * x[j] + gy[j] * y[j];
+            for (int j = 0; j < N2; ++j) {
+              ss = f2_fma(y[j], y[j], f2_fma(x[j], x[j], ss));
+              const uint64_t g = ga[j];
+              ga[j] = f2_fma(gb[j], s2[j], f2_mul(g, c2[j]));
+              gb[j] = f2_fma(g, n2[j], f2_mul(gb[j], c2[j]));
+              ta[j] = f2_mul(ga[j], x[j]), tb[j] = f2_mul(gb[j], y[j]);
+              dot = f2_fma(wb[j], tb[j], f2_fma(wa[j], ta[j], dot));
             }
-            dot = row_sum<R::L>(dot) * (1.f / D);
+            float s0, s1, d0, d1;
+            f2_unpack(ss, s0, s1);
+            f2_unpack(dot, d0, d1);
+            s0 += s1, d0 += d1;
 #pragma unroll
-            for (int j = 0; j < NP; ++j) {
-              gx[j] = rstd * (gx[j] - x[j] * dot);
-              gy[j] = rstd * (gy[j] - y[j] * dot);
+            for (int o = R::L / 2; o > 0; o >>= 1) {
+              s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+              d0 += __shfl_xor_sync(0xffffffffu, d0, o);
             }
-            ry[i] = pack<T, kHalf, NP>(gx, gy);
+            const float rstd = rsqrtf(s0 * (1.f / D) + p.eps), k = -rstd * rstd * rstd * d0 * (1.f / D);
+            const uint64_t r2 = f2_pack(rstd, rstd), k2 = f2_pack(k, k);
+#pragma unroll
+            for (int j = 0; j < N2; ++j) {
+              da[j] = f2_fma(r2, ta[j], da[j]), db[j] = f2_fma(r2, tb[j], db[j]);
+              ga[j] = f2_fma(r2, f2_mul(ga[j], wa[j]), f2_mul(k2, x[j]));
+              gb[j] = f2_fma(r2, f2_mul(gb[j], wb[j]), f2_mul(k2, y[j]));
+            }
+            ry[i] = pack2<T, kHalf, N2>(ga, gb);
           }
           if (live && h0 + i < h_end) store_raw<T, D, kHalf>(dx + (h0 + i) * p.in.h, lane, ry[i]);
         }
       }
     }
+    u -= units;
     if (st < 2 && p.dw[st] != nullptr) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const int pr = lane * NP + j;
-        red[row][kHalf ? pr : 2 * pr] = da[j];
-        red[row][kHalf ? D / 2 + pr : 2 * pr + 1] = db[j];
+        float lo, hi;
+        f2_unpack(da[j / 2], lo, hi);
+        red[row][kHalf ? pr : 2 * pr] = j & 1 ? hi : lo;
+        f2_unpack(db[j / 2], lo, hi);
+        red[row][kHalf ? D / 2 + pr : 2 * pr + 1] = j & 1 ? hi : lo;
       }
       __syncthreads();
       if (threadIdx.x < D) {
@@ -387,14 +445,25 @@ template <typename T, int D, bool kHalf>
 cudaError_t launch_bwd(NormBwdParams p, int num_sms, cudaStream_t s) {
   using R = Row<T, D>;
   const long long tiles = static_cast<long long>((p.N + R::kTokens - 1) / R::kTokens) * p.B;
-  long long blocks = 4ll * num_sms;
+  long long blocks = static_cast<long long>(kBwdBlocksPerSm) * num_sms;
   if (blocks > kNormBwdMaxBlocks) blocks = kNormBwdMaxBlocks;
-  // few tokens: the heads are split until every block has a unit
-  long long chunks = (blocks + tiles - 1) / tiles;
-  if (chunks > p.H) chunks = p.H;
-  p.heads_per_unit = int((p.H + chunks - 1) / chunks);
-  const long long units = tiles * ((p.H + p.heads_per_unit - 1) / p.heads_per_unit);
+  // heads a unit: the fewest rounds of units over the blocks, a unit costing its heads plus about
+  // two more for the token's angles
+  int streams = 0;
+  for (int i = 0; i < 3; ++i) streams += p.dy[i] != nullptr;
+  constexpr int kU = kBwdUnroll<kHalf>;
+  const int groups = (p.H + kU - 1) / kU;
+  long long best = 0, units = 0;
+  for (int c = 1; c <= groups; ++c) {
+    const int heads = (groups + c - 1) / c * kU;
+    const long long n = tiles * ((p.H + heads - 1) / heads) * streams;
+    const long long cost = (n + blocks - 1) / blocks * (heads + 2);
+    if (best == 0 || cost < best) best = cost, units = n, p.heads_per_unit = heads;
+  }
+  if (p.heads_per_unit > p.H) p.heads_per_unit = p.H;
   if (blocks > units) blocks = units;
+  p.by_chunks = Divisor((p.H + p.heads_per_unit - 1) / p.heads_per_unit);
+  p.by_tiles = Divisor((p.N + R::kTokens - 1) / R::kTokens);
   const cudaError_t e = launch_overlapped(norm_bwd_kernel<T, D, kHalf>, dim3(unsigned(blocks)), kThreads, 0, s, 0, p);
   if (e != cudaSuccess || (p.dw[0] == nullptr && p.dw[1] == nullptr)) return e;
   return launch_overlapped(norm_bwd_reduce_kernel, dim3(2), 1024, 0, s, 0, p.partial, int(blocks), D, p.dw[0], p.dw[1]);

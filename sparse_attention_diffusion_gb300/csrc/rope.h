@@ -6,6 +6,23 @@
 
 namespace mcs {
 
+// Division of n < 2^31 by a divisor known at launch: with l = ceil(log2 d) and
+// m = floor(2^(31 + l) / d) + 1, n / d = (n m) >> (31 + l) (Granlund and Montgomery).
+struct Divisor {
+  uint32_t mul = 0;
+  int shift = 0;
+  Divisor() = default;
+  explicit Divisor(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    mul = uint32_t((1ull << (31 + l)) / uint32_t(d) + 1);
+    shift = 31 + l;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const { return int((uint64_t(uint32_t(n)) * mul) >> shift); }
+#endif
+};
+
 // A rope as the kernels use it: pairs per axis, grid lengths and table offsets
 // (in (cos, sin) entries).
 struct RopeGeom {
@@ -16,6 +33,7 @@ struct RopeGeom {
   int npairs;   // pairs that turn
   int first;    // first grid token
   int ngrid;    // grid tokens
+  Divisor by[3];  // by len
 };
 
 struct RopeTableParams {
@@ -64,7 +82,8 @@ struct NormBwdParams {
   const int32_t* pos;
   RopeGeom g;
   int B, H, N;
-  int heads_per_unit;      // set by the launcher
+  int heads_per_unit;      // set by the launcher, with the divisors by its chunks and tiles
+  Divisor by_chunks, by_tiles;
   uint32_t* status;
 };
 // Upper bound of the blocks (rows of `partial`) a backward launch uses.
