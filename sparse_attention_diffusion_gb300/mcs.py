@@ -428,85 +428,111 @@ def rope_table(rope: mcs_rope, device="cuda", stream=None) -> torch.Tensor:
 
 
 def mcs_rope_table(rope, table, stream=None):
-    n = int(load().mcs_rope_table_size(ctypes.byref(rope)))
-    if n and (table.dtype != torch.float32 or table.numel() * 4 < n):
-        raise ValueError(f"table: expected {n // 4} fp32 elements, got {table.numel()} {table.dtype}")
-    _check("mcs_rope_table", load().mcs_rope_table(ctypes.byref(rope), _here(table), _stream(stream)))
+    _table(rope, table)
+    _on_device(table)
+    _check("mcs_rope_table", load().mcs_rope_table(rope, _address("table", table), _raw_stream(stream)))
 
 
-def _here(t):
-    """Pointer of a contiguous tensor on the current device (None passes through)."""
-    if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"libmcs launches on the current device, tensor is on {t.device}")
-    return _ptr(t)
+# These calls are short (a small layer's kernels take a few microseconds), so their checks
+# are plain comparisons and pointers go to ctypes as integers.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object (4 us)
 
 
-def _view(desc, name, t):
-    """Pointer and strides of a [B,H,N,d] view with contiguous d (None passes through)."""
+def _raw_stream(stream=None):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _on_device(*tensors):
+    """All of them (None allowed) on the device that the call launches on."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"libmcs takes device tensors on the current device, got one on {t.device}")
+
+
+def _address(name, t):
+    """Address of a contiguous tensor (None passes through)."""
     if t is None:
-        return None, None
-    shape = (desc.B, desc.H, desc.N, desc.d)
-    if tuple(t.shape) != shape or t.dtype != _io_dtype(desc):
-        raise ValueError(f"{name}: expected {shape} {_io_dtype(desc)}, got {tuple(t.shape)} {t.dtype}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: libmcs takes tensors on the current device, got {t.device}")
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libmcs takes contiguous tensors")
+    return t.data_ptr()
+
+
+def _exactly(name, t, shape, dtype):
+    """Address of a contiguous tensor of this shape and type (None passes through)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return _address(name, t)
+
+
+def _view(name, t, shape, dtype):
+    """Address and strides of a [B,H,N,d] view with contiguous d."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
     sb, sh, sn, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {sd}")
-    size = (desc.B, desc.H, desc.N)
-    return ctypes.c_void_p(t.data_ptr()), tuple(s if n > 1 else 0 for s, n in zip((sb, sh, sn), size))
+    B, H, N, _ = shape
+    return t.data_ptr(), (sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0)
 
 
-def _views(desc, **tensors):
-    """Pointers of views that must share one set of strides, and those strides."""
+def _views(named, shape, dtype):
+    """Addresses of views that must share one set of strides (None passes through), and those strides."""
     ptrs, common = [], None
-    for name, t in tensors.items():
-        p, st = _view(desc, name, t)
+    for name, t in named:
+        if t is None:
+            ptrs.append(None)
+            continue
+        p, st = _view(name, t, shape, dtype)
+        if common is not None and st != common:
+            raise ValueError(f"{name}: strides {st} differ from {common}; the views must share their strides")
         ptrs.append(p)
-        if st is not None:
-            if common is not None and st != common:
-                raise ValueError(f"{name}: strides {st} differ from {common}; the views must share their strides")
-            common = st
-    return ptrs, common
+        common = st
+    return ptrs, None if common is None else mcs_strides(*common)
 
 
-def _positions(desc, rope, table, pos):
-    """Host check of a rope's table and listed positions."""
-    n = int(load().mcs_rope_table_size(ctypes.byref(rope)))
+def _table(rope, table):
+    n = load().mcs_rope_table_size(rope)
     if n and (table.dtype != torch.float32 or table.numel() * 4 < n):
         raise ValueError(f"table: expected {n // 4} fp32 elements, got {table.numel()} {table.dtype}")
-    want = (desc.B, desc.N, rope.axes)
-    if pos is not None and (tuple(pos.shape) != want or pos.dtype != torch.int32):
-        raise ValueError(f"pos: expected {want} torch.int32, got {tuple(pos.shape)} {pos.dtype}")
 
 
-def _vector(name, t, n, dtype):
-    if t is not None and (tuple(t.shape) != (n,) or t.dtype != dtype):
-        raise ValueError(f"{name}: expected ({n},) {dtype}, got {tuple(t.shape)} {t.dtype}")
+def _rope_args(desc, rope, table, pos):
+    """Addresses of a rope's table and listed positions, checked."""
+    _table(rope, table)
+    return _address("table", table), _exactly("pos", pos, (desc.B, desc.N, rope.axes), torch.int32)
 
 
 def mcs_rope_apply(desc, rope, table, pos, x, out, inverse=False, stream=None):
     """out = R x (or R^T x): x, out are [B,H,N,d] views with contiguous d; out may be x."""
-    _positions(desc, rope, table, pos)
-    xp, xs = _view(desc, "x", x)
-    op, os_ = _view(desc, "out", out)
-    _check("mcs_rope_apply", load().mcs_rope_apply(ctypes.byref(desc), ctypes.byref(rope), _here(table), _here(pos),
-                                                   xp, mcs_strides(*xs), op, mcs_strides(*os_), int(bool(inverse)),
-                                                   _stream(stream)))
+    dt, shape = _io_dtype(desc), (desc.B, desc.H, desc.N, desc.d)
+    xp, xs = _view("x", x, shape, dt)
+    op, os_ = _view("out", out, shape, dt)
+    tp, pp = _rope_args(desc, rope, table, pos)
+    _on_device(table, pos, x, out)
+    _check("mcs_rope_apply", load().mcs_rope_apply(desc, rope, tp, pp, xp, mcs_strides(*xs), op, mcs_strides(*os_),
+                                                   1 if inverse else 0, _raw_stream(stream)))
 
 
 def mcs_qk_norm_rope(desc, rope, table, pos, q, k, v, wq, wk, eps, q_out, k_out, v_out, stream=None):
     """Per-head RMS norm of q and k, rotation, and the copy of q, k, v (views that share their strides, e.g. of a
     packed [B, N, 3, H, d] projection) into contiguous [B,H,N,d] tensors. Each of the three may be None."""
-    _positions(desc, rope, table, pos)
-    _expect(desc, q_out=q_out, k_out=k_out, v_out=v_out)
-    _vector("wq", wq, desc.d, _io_dtype(desc))
-    _vector("wk", wk, desc.d, _io_dtype(desc))
-    (qp, kp, vp), st = _views(desc, q=q, k=k, v=v)
-    _check("mcs_qk_norm_rope", load().mcs_qk_norm_rope(
-        ctypes.byref(desc), ctypes.byref(rope), _here(table), _here(pos), qp, kp, vp,
-        None if st is None else mcs_strides(*st), _here(wq), _here(wk), float(eps), _here(q_out), _here(k_out),
-        _here(v_out), _stream(stream)))
+    dt, shape = _io_dtype(desc), (desc.B, desc.H, desc.N, desc.d)
+    (qp, kp, vp), st = _views((("q", q), ("k", k), ("v", v)), shape, dt)
+    w = (desc.d,)
+    tp, pp = _rope_args(desc, rope, table, pos)
+    wqp, wkp = _exactly("wq", wq, w, dt), _exactly("wk", wk, w, dt)
+    qo, ko, vo = (_exactly(n, t, shape, dt) for n, t in (("q_out", q_out), ("k_out", k_out), ("v_out", v_out)))
+    _on_device(table, pos, q, k, v, wq, wk, q_out, k_out, v_out)
+    _check("mcs_qk_norm_rope", load().mcs_qk_norm_rope(desc, rope, tp, pp, qp, kp, vp, st, wqp, wkp, eps, qo, ko, vo,
+                                                       _raw_stream(stream)))
 
 
 def qk_norm_rope_bwd_workspace(desc, device="cuda") -> torch.Tensor:
@@ -520,18 +546,18 @@ def mcs_qk_norm_rope_bwd(desc, rope, table, pos, q, k, wq, wk, eps, dq_out, dk_o
                          stream=None):
     """Gradients of mcs_qk_norm_rope: dq, dk, dv are written as views that share the strides of q and k; dwq, dwk are
     fp32 [d] or None. Each group (q, dq_out, dq), (k, dk_out, dk), (dv_out, dv) may be None."""
-    _positions(desc, rope, table, pos)
-    _expect(desc, dq_out=dq_out, dk_out=dk_out, dv_out=dv_out)
-    _vector("wq", wq, desc.d, _io_dtype(desc))
-    _vector("wk", wk, desc.d, _io_dtype(desc))
-    _vector("dwq", dwq, desc.d, torch.float32)
-    _vector("dwk", dwk, desc.d, torch.float32)
-    (qp, kp, dqp, dkp, dvp), st = _views(desc, q=q, k=k, dq=dq, dk=dk, dv=dv)
+    dt, shape = _io_dtype(desc), (desc.B, desc.H, desc.N, desc.d)
+    (qp, kp, dqp, dkp, dvp), st = _views((("q", q), ("k", k), ("dq", dq), ("dk", dk), ("dv", dv)), shape, dt)
+    w, f32 = (desc.d,), torch.float32
+    tp, pp = _rope_args(desc, rope, table, pos)
+    wqp, wkp = _exactly("wq", wq, w, dt), _exactly("wk", wk, w, dt)
+    dwqp, dwkp = _exactly("dwq", dwq, w, f32), _exactly("dwk", dwk, w, f32)
+    qo, ko, vo = (_exactly(n, t, shape, dt) for n, t in (("dq_out", dq_out), ("dk_out", dk_out), ("dv_out", dv_out)))
+    wsp = _address("ws", ws)
+    _on_device(table, pos, q, k, wq, wk, dq_out, dk_out, dv_out, dq, dk, dv, dwq, dwk, ws)
     _check("mcs_qk_norm_rope_bwd", load().mcs_qk_norm_rope_bwd(
-        ctypes.byref(desc), ctypes.byref(rope), _here(table), _here(pos), qp, kp,
-        None if st is None else mcs_strides(*st), _here(wq), _here(wk), float(eps), _here(dq_out), _here(dk_out),
-        _here(dv_out), dqp, dkp, dvp, _here(dwq), _here(dwk), _here(ws), ws.numel() * ws.element_size(),
-        _stream(stream)))
+        desc, rope, tp, pp, qp, kp, st, wqp, wkp, eps, qo, ko, vo, dqp, dkp, dvp, dwqp, dwkp, wsp,
+        ws.numel() * ws.element_size(), _raw_stream(stream)))
 
 
 def linear_desc(B, N, in_features, out_features, dtype, act="none", heads=0) -> mcs_linear_desc:
@@ -546,14 +572,12 @@ def mcs_linear(desc, x, w, bias, gate, residual, y, stream=None):
     """y = residual + gate * act(x w^T + bias); x [B, N, in] or [B, heads, N, in / heads], w [out, in], bias [out],
     gate [B, out], residual and y [B, N, out] (bias, gate, residual may be None; y may be residual)."""
     B, N, I, O, h = desc.B, desc.N, desc.in_features, desc.out_features, desc.heads
-    dt = _io_dtype(desc)
-    xs = (B, N, I) if h == 0 else (B, h, N, I // h)
-    for name, t, shape in (("x", x, xs), ("w", w, (O, I)), ("bias", bias, (O,)), ("gate", gate, (B, O)),
-                           ("residual", residual, (B, N, O)), ("y", y, (B, N, O))):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != dt):
-            raise ValueError(f"{name}: expected {shape} {dt}, got {tuple(t.shape)} {t.dtype}")
-    _check("mcs_linear", load().mcs_linear(ctypes.byref(desc), _here(x), _here(w), _here(bias), _here(gate),
-                                           _here(residual), _here(y), _stream(stream)))
+    dt, rows = _io_dtype(desc), (B, N, O)
+    xp = _exactly("x", x, (B, h, N, I // h) if h > 0 else (B, N, I), dt)
+    wp, bp, gp = _exactly("w", w, (O, I), dt), _exactly("bias", bias, (O,), dt), _exactly("gate", gate, (B, O), dt)
+    rp, yp = _exactly("residual", residual, rows, dt), _exactly("y", y, rows, dt)
+    _on_device(x, w, bias, gate, residual, y)
+    _check("mcs_linear", load().mcs_linear(desc, xp, wp, bp, gp, rp, yp, _raw_stream(stream)))
 
 
 # ---------------------------------------------------------------- convenience: buffers for one layer
