@@ -6,6 +6,8 @@
 // comes after the first and after any tensor-memory allocation, so that a waiting
 // successor can never hold what a running kernel still needs.
 #pragma once
+#include <atomic>
+#include <cstdint>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -14,6 +16,22 @@ namespace mcs {
 
 __device__ __forceinline__ void grid_inputs_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device (bytes must
+// be the same in every call for one kernel; plans that differ share the kernel's
+// attribute between threads).
+template <auto kKern>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};  // one bit per device, of this kernel
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // cluster: CTAs of a cluster along x (0: the kernel's own attribute, or none).
 template <typename... Params, typename... Args>

@@ -272,6 +272,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
+template <int kAct>
+cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const LinearParams& p, const Tiling& t, int pairs,
+                       cudaStream_t s) {
+  const cudaError_t e = allow_smem<linear_pair_kernel<kAct>>(kSmemAlloc);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(linear_pair_kernel<kAct>, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, p, t);
+}
+
 cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t s) {
   Tiling t{};
   CUtensorMap mx, mw;
@@ -301,16 +309,11 @@ cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t
   ok = ok && make_tile_map(&mw, p.w, 1, p.O, p.K, t.bn / 2);
   if (!ok) return cudaErrorInvalidValue;
   const int pairs = t.total < num_sms / 2 ? t.total : num_sms / 2;
-  auto launch = [&](auto kern) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(kern, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, p, t);
-  };
   switch (p.act) {
-    case MCS_ACT_GELU_TANH: return launch(linear_pair_kernel<MCS_ACT_GELU_TANH>);
-    case MCS_ACT_GELU_ERF: return launch(linear_pair_kernel<MCS_ACT_GELU_ERF>);
-    case MCS_ACT_SILU: return launch(linear_pair_kernel<MCS_ACT_SILU>);
-    default: return launch(linear_pair_kernel<MCS_ACT_NONE>);
+    case MCS_ACT_GELU_TANH: return start_pair<MCS_ACT_GELU_TANH>(mx, mw, p, t, pairs, s);
+    case MCS_ACT_GELU_ERF: return start_pair<MCS_ACT_GELU_ERF>(mx, mw, p, t, pairs, s);
+    case MCS_ACT_SILU: return start_pair<MCS_ACT_SILU>(mx, mw, p, t, pairs, s);
+    default: return start_pair<MCS_ACT_NONE>(mx, mw, p, t, pairs, s);
   }
 }
 

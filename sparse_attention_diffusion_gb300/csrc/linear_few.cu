@@ -234,6 +234,14 @@ __global__ void __launch_bounds__(kThreads)
   if (a.splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
 }
 
+template <int kAct>
+cudaError_t start_few(const CUtensorMap& mx, const CUtensorMap& mw, const LinearParams& p, const FewArgs& a, dim3 grid,
+                      size_t smem, cudaStream_t s) {
+  const cudaError_t e = allow_smem<linear_few_kernel<kAct>>(226 * 1024);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(linear_few_kernel<kAct>, grid, kThreads, smem, s, unsigned(a.splits), mx, mw, p, a);
+}
+
 }  // namespace
 
 cudaError_t linear_few(const LinearParams& p, const FewPlan& plan, int num_sms, cudaStream_t s) {
@@ -270,17 +278,11 @@ cudaError_t linear_few(const LinearParams& p, const FewPlan& plan, int num_sms, 
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const size_t smem = size_t(a.stages) * stage + kBarBytes + 1024;
   const dim3 grid(unsigned(a.splits) * a.tiles * a.sections, (p.O + 127) / 128);
-  auto launch = [&](auto kern) {
-    // one value for every call: threads launching other plans at the same time share the attribute
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(kern, grid, kThreads, smem, s, unsigned(a.splits), mx, mw, p, a);
-  };
   switch (p.act) {
-    case MCS_ACT_GELU_TANH: return launch(linear_few_kernel<MCS_ACT_GELU_TANH>);
-    case MCS_ACT_GELU_ERF: return launch(linear_few_kernel<MCS_ACT_GELU_ERF>);
-    case MCS_ACT_SILU: return launch(linear_few_kernel<MCS_ACT_SILU>);
-    default: return launch(linear_few_kernel<MCS_ACT_NONE>);
+    case MCS_ACT_GELU_TANH: return start_few<MCS_ACT_GELU_TANH>(mx, mw, p, a, grid, smem, s);
+    case MCS_ACT_GELU_ERF: return start_few<MCS_ACT_GELU_ERF>(mx, mw, p, a, grid, smem, s);
+    case MCS_ACT_SILU: return start_few<MCS_ACT_SILU>(mx, mw, p, a, grid, smem, s);
+    default: return start_few<MCS_ACT_NONE>(mx, mw, p, a, grid, smem, s);
   }
 }
 
