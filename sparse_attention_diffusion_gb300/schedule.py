@@ -104,6 +104,43 @@ class MetaCacheLayer:
         return self.out
 
 
+class AttentionBlock:
+    """The projections around a MetaCacheLayer, from a block's hidden states x
+    [B, N, in] and back: packed q, k, v projection, per-head norms of q and k with
+    the rotary positions, attention (the layer's dense, anchor or reuse step), output
+    projection added to the hidden states through a gate.
+
+    w_qkv: [3 * H * d, in], rows ordered q heads, k heads, v heads; w_out: [in, H * d];
+    wq, wk: norm weights [d] or None; biases may be None. The block owns its buffers;
+    q, k, v are overwritten by every inputs() call. With run():
+        run(layer, sched, lambda: block.inputs(x), advance,
+            on_output=lambda t, kind, o: block.output(o, x, gate, x))"""
+
+    def __init__(self, layer: MetaCacheLayer, rope, w_qkv, b_qkv, wq, wk, w_out, b_out, eps=1e-6):
+        d = layer.desc
+        hd, dt, dev = d.H * d.d, layer.out.dtype, layer.out.device
+        self.layer, self.rope, self.eps = layer, rope, eps
+        self.w_qkv, self.b_qkv, self.wq, self.wk, self.w_out, self.b_out = w_qkv, b_qkv, wq, wk, w_out, b_out
+        self.table = mcs.rope_table(rope, device=dev)
+        self.proj_in = mcs.linear_desc(d.B, d.N, w_qkv.shape[1], 3 * hd, dt)
+        self.proj_out = mcs.linear_desc(d.B, d.N, hd, w_out.shape[0], dt, heads=d.H)
+        self.qkv = torch.empty((d.B, d.N, 3 * hd), dtype=dt, device=dev)
+        self.q, self.k, self.v = (torch.empty_like(layer.out) for _ in range(3))
+
+    def inputs(self, x):
+        """(q, k, v) [B, H, N, d] of the hidden states x."""
+        d = self.layer.desc
+        mcs.mcs_linear(self.proj_in, x, self.w_qkv, self.b_qkv, None, None, self.qkv)
+        q, k, v = self.qkv.view(d.B, d.N, 3, d.H, d.d).permute(2, 0, 3, 1, 4)
+        mcs.mcs_qk_norm_rope(d, self.rope, self.table, None, q, k, v, self.wq, self.wk, self.eps, self.q, self.k, self.v)
+        return self.q, self.k, self.v
+
+    def output(self, o, x, gate, y):
+        """y = x + gate * (o w_out^T + b_out) for an attention output o; y may be x."""
+        mcs.mcs_linear(self.proj_out, o, self.w_out, self.b_out, gate, x, y)
+        return y
+
+
 def run(layer: MetaCacheLayer, sched: Schedule, inputs, advance, on_output=None):
     """Run the schedule. `inputs()` returns the current (q, k, v); `advance()`
     drifts them to the next step. Returns the per-step records (CUDA-event ms)."""
