@@ -140,11 +140,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (++s == tl.stages) s = 0, phase ^= 1;
       }
     }
-    if (!ok && lane == 0) raise_status(st, kStatusTimeout);
-    // let the armed copies of both CTAs land before the pair can exit: the stages from s on carry the
-    // ring's previous phase, those before s the current one (a stage never used has nothing to wait for)
-    if (rank == 0 && lane == 0 && !ok)
-      for (int v = 0; v < tl.stages; ++v) mbar_drain(full + v, v < s ? phase : phase ^ 1);
+    if (!ok) {
+      if (lane == 0) raise_status(st, kStatusTimeout);
+      settle_copies();  // normally the MMAs have consumed every copy before the pair exits
+    }
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
@@ -180,6 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           mbar_drain(drain, 0);
         }
+        settle_copies();
       }
     }
     __syncwarp();

@@ -155,11 +155,12 @@ __global__ void __launch_bounds__(kThreads)
       __syncwarp();
       if (++s == a.stages) s = 0, phase ^= 1;
     }
-    if (!ok && lane == 0) {
-      *failed = 1;
-      raise_status(st, kStatusTimeout);
-      // let the armed copies land: stages from s on carry the ring's previous phase
-      for (int v = 0; v < a.stages; ++v) mbar_drain(full + v, v < s ? phase : phase ^ 1);
+    if (!ok) {
+      if (lane == 0) {
+        *failed = 1;
+        raise_status(st, kStatusTimeout);
+      }
+      settle_copies();  // normally the MMAs have consumed every copy before the CTA exits
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kThreads)
         __syncwarp();
         mbar_drain(drain, 0);
       }
+      settle_copies();
     }
     __syncwarp();
   } else {

@@ -74,12 +74,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
-// Wait for copies or MMAs already in flight on the way out of a failed kernel:
-// ignores the timeout flag (which is set by then) and has a limit of its own.
+// On the way out of a failed kernel: wait for MMAs already issued, whatever the
+// timeout flag (which is set by then) says, with a limit of its own.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(a, parity) && globaltimer_ns() - t0 < 20ull * 1000 * 1000) {
+  }
+}
+// The same for copies whose barrier the caller does not know: 1 ms, hundreds of
+// times what a copy takes.
+__device__ __forceinline__ void settle_copies() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000ull * 1000) {
   }
 }
 

@@ -431,12 +431,17 @@ template <typename T, int D, bool kHalf, bool kNorm>
 cudaError_t launch_rotate(RotateParams p, int num_sms, cudaStream_t s) {
   using R = Row<T, D>;
   const int tiles = (p.N + R::kTokens - 1) / R::kTokens;
-  // all heads of a token in one block when the tokens alone fill the GPU;
-  // otherwise the heads are split until about two blocks per SM are there
-  const long long rows = static_cast<long long>(tiles) * p.B;
-  long long chunks = (2ll * num_sms + rows - 1) / rows;
-  if (chunks > p.H) chunks = p.H;
-  p.heads_per_block = int((p.H + chunks - 1) / chunks);
+  // heads a block: the fewest rounds of blocks over the SMs (five fit on each), a block costing its
+  // groups of heads plus about half a group for the token's angles
+  const long long rows = static_cast<long long>(tiles) * p.B, slots = 5ll * num_sms;
+  const int groups = (p.H + kUnroll - 1) / kUnroll;
+  long long best = 0;
+  for (int c = 1; c <= groups; ++c) {
+    const int per = (groups + c - 1) / c;
+    const long long cost = (rows * ((groups + per - 1) / per) + slots - 1) / slots * (2 * per + 1);
+    if (best == 0 || cost < best) best = cost, p.heads_per_block = per * kUnroll;
+  }
+  if (p.heads_per_block > p.H) p.heads_per_block = p.H;
   const dim3 grid(tiles, (p.H + p.heads_per_block - 1) / p.heads_per_block, p.B);
   return launch_overlapped(rotate_kernel<T, D, kHalf, kNorm>, grid, kThreads, 0, s, 0, p);
 }
