@@ -15,9 +15,12 @@
 //                stages
 //   warp 1       MMA issuer (even CTA only, for both)
 //   warp 2       tensor-memory allocation
-//   warps 4-11   epilogue: 32 x 32 pieces of the accumulator through a swizzled
-//                shared-memory patch, so that bias, gate, residual and the store
-//                run along rows, 64 contiguous bytes a row
+//   warps 4-11   epilogue: 32 x 32 pieces of the accumulator, a row per lane; the
+//                residual arrives in a swizzled shared-memory patch by TMA one
+//                piece ahead, the result leaves through the same patch by TMA, so
+//                no lane touches rows of x's or y's stride (outputs whose row is
+//                no multiple of 16 bytes go through the patch in fp32 and leave by
+//                plain stores along the row)
 // The accumulator is double-buffered in tensor memory (2 x 256 columns), so a
 // tile's epilogue runs under the next tile's products. Tiles are walked in bands
 // of eight row tiles, column by column, which keeps the band's x rows and the
@@ -41,9 +44,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kHalfTile = 128 * 128;  // bytes of 128 rows x 64 columns
 constexpr int kRing = 6 * 2 * kHalfTile;  // six stages of the widest tile, more of narrower ones
 constexpr int kPatchOff = kRing;
-constexpr int kPatch = 32 * 32 * 4;
+constexpr int kPatch = 32 * 32 * 4;  // two bf16 pieces, or one in fp32
 constexpr int kBarOff = kPatchOff + kEpiWarps * kPatch;
-constexpr int kSmemAlloc = kBarOff + 256 + 1024;
+constexpr int kSmemAlloc = kBarOff + 512 + 1024;
 constexpr int kBand = 8;
 
 // How the rows of x are cut into tiles: sections of `rows` rows each (one
@@ -67,19 +70,85 @@ __device__ __forceinline__ Tile tile_at(const Tiling& t, int i) {
   return {rt / t.tiles, (rt % t.tiles) * 256, col * t.bn};
 }
 
-// Eight sums of a row of an epilogue patch (rows of 128 bytes, 16-byte pieces swizzled).
-__device__ __forceinline__ void patch_row(uint32_t patch, int row, int col, float (&v)[8]) {
+// 32 consecutive bf16 values (64 bytes) of global or shared memory as floats.
+__device__ __forceinline__ void global_row32(const __nv_bfloat16* src, float (&v)[32]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
-                 : "r"(patch + row * 128 + (((col / 4 + h) ^ (row & 7)) << 4))
+  for (int q = 0; q < 4; ++q) {
+    float t[8];
+    unpack8(reinterpret_cast<const uint4*>(src)[q], t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * q + i] = t[i];
+  }
+}
+__device__ __forceinline__ uint32_t piece_at(uint32_t patch, int row, int q) {
+  return patch + row * 64 + ((q ^ ((row >> 1) & 3)) << 4);
+}
+
+// A 32 x 32 piece of outputs whose rows are no multiple of 16 bytes: through the
+// patch in fp32, then along rows, one output a lane (two where the rows allow
+// 4-byte stores).
+template <int kAct>
+__device__ __forceinline__ void store_odd(const LinearParams& p, int rows, int sec, int n0, int o, uint32_t patch,
+                                          int lane, const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + ((q ^ (lane & 7)) << 4)),
+                 "r"(r[4 * q]), "r"(r[4 * q + 1]), "r"(r[4 * q + 2]), "r"(r[4 * q + 3])
                  : "memory");
+  __syncwarp();
+  auto sum = [&](int row, int c) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];"
+                 : "=f"(f)
+                 : "r"(patch + row * 128 + (((c >> 2) ^ (row & 7)) << 4) + (c & 3) * 4));
+    return f;
+  };
+  const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(p.bias);
+  const __nv_bfloat16* gate = static_cast<const __nv_bfloat16*>(p.gate);
+  const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(p.residual);
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
+  const int live = min(32, rows - n0), cols = min(32, p.O - o);
+  if (p.O % 2 == 0) {
+    const int c = (lane & 15) * 2;
+    if (c < cols) {  // cols is even
+      const float2 bs = bias ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(bias + o + c)) : make_float2(0, 0);
+#pragma unroll 4
+      for (int row = lane >> 4; row < live; row += 2) {
+        const int m = sec * rows + n0 + row;
+        const size_t at = size_t(m) * p.O + o + c;
+        float v[2] = {sum(row, c) + bs.x, sum(row, c + 1) + bs.y};
+        activate<kAct>(v);
+        if (gate) {
+          const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(gate + size_t(m / p.N) * p.O + o + c));
+          v[0] *= g.x, v[1] *= g.y;
+        }
+        if (res) {
+          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(res + at));
+          v[0] += f.x, v[1] += f.y;
+        }
+        *reinterpret_cast<uint32_t*>(y + at) = pack_bf16x2(v[0], v[1]);
+      }
+    }
+  } else if (lane < cols) {
+    const float bs = bias ? __bfloat162float(bias[o + lane]) : 0.f;
+#pragma unroll 4
+    for (int row = 0; row < live; ++row) {
+      const int m = sec * rows + n0 + row;
+      const size_t at = size_t(m) * p.O + o + lane;
+      float v[1] = {sum(row, lane) + bs};
+      activate<kAct>(v);
+      if (gate) v[0] *= __bfloat162float(gate[size_t(m / p.N) * p.O + o + lane]);
+      if (res) v[0] += __bfloat162float(res[at]);
+      y[at] = __float2bfloat16_rn(v[0]);
+    }
+  }
+  __syncwarp();
 }
 
 template <int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_r,
                        const LinearParams p, const Tiling tl) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -89,7 +158,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = empty + kMaxStages;                          // [2] each CTA: accumulator written
   uint64_t* acc_empty = acc_full + 2;                            // [2] even CTA: accumulator read by both CTAs
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* res_full = drain + 1;  // [epilogue warp][2] residual piece landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 2 * kEpiWarps);
   const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
   const int rank = blockIdx.x & 1;  // of the cluster {2, 1, 1}
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -98,14 +168,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 32) {
     tma_prefetch_map(&map_x);
     tma_prefetch_map(&map_w);
+    if (p.O % 8 == 0) tma_prefetch_map(&map_y);
+    if (p.O % 8 == 0 && p.residual) tma_prefetch_map(&map_r);
   }
   if (tid == 0) {
     for (int s = 0; s < tl.stages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
     for (int b = 0; b < 2; ++b) mbar_init(acc_full + b, 1), mbar_init(acc_empty + b, 2 * kEpiWarps);
     mbar_init(drain, 1);
+    for (int e = 0; e < 2 * kEpiWarps; ++e) mbar_init(res_full + e, 1);
     fence_mbar_init();
   }
-  __syncthreads();
   if (warp == 2) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
@@ -187,39 +259,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int e = warp - 4, quarter = e & 3, half = e >> 2;
     const uint32_t patch = sbase + kPatchOff + e * kPatch;
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
-    const int prow = lane >> 2, pcol = (lane & 3) * 8;  // this lane's row (of eight) and columns when reading back
-    const bool vec = p.O % 8 == 0;
+    const int nchunks = tl.bn / 32;
+    const bool vec = p.O % 8 == 0, add = vec && p.residual != nullptr;
+    const __nv_bfloat16 *bias = static_cast<const __nv_bfloat16*>(p.bias), *gate = static_cast<const __nv_bfloat16*>(p.gate);
+    uint64_t* rbar = res_full + 2 * e;
     bool ok = true;
-    int it = 0;
+    int it = 0, buf = 0;      // tile and patch buffer
+    uint32_t rphase = 0;      // bit b: parity of the next residual piece in buffer b
+    uint32_t awaited = 0;     // bit b: a residual piece is on its way to buffer b
+    // starts the copy of the residual piece (tile t, chunk cc) into buffer b, whose last store has to be read out
+    auto fetch = [&](const Tile& ti, int cc, int b) {
+      const int n0 = ti.row0 + rank * 128 + quarter * 32, o = ti.o0 + cc * 32;
+      if (n0 >= tl.rows || o >= p.O) return;
+      if (elect_one()) {
+        bulk_wait_read<0>();
+        mbar_arrive_expect_tx(rbar + b, kPatch / 2);
+        tma_load_3d(patch + b * (kPatch / 2), &map_r, o, n0, ti.sec, smem_u32(rbar + b));
+      }
+      __syncwarp();
+      awaited |= 1u << b;
+    };
+    if (add && pair < tl.total && half < nchunks) fetch(tile_at(tl, pair), half, 0);
     for (int t = pair; t < tl.total; t += pairs, ++it) {
       const int b = it & 1;
       const Tile ti = tile_at(tl, t);
-      ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st));
-      if (!ok) break;
-      tc_fence_after();
       const int n0 = ti.row0 + rank * 128 + quarter * 32;
-      const int m0 = ti.sec * tl.rows + n0;
-      const int nchunks = tl.bn / 32;
+      const int n = n0 + lane, m = ti.sec * tl.rows + n;  // this lane's row
+      const __nv_bfloat16* grow = gate ? gate + size_t(n < tl.rows ? m / p.N : 0) * p.O : nullptr;
       if (half >= nchunks) {  // nothing of this accumulator for this warp
-        tc_fence_before();
+        if (!(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
         if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
+        continue;
       }
       for (int cc = half; cc < nchunks; cc += 2) {
-        const int o = ti.o0 + cc * 32 + pcol;
-        const bool cols = vec && o < p.O, add = p.residual != nullptr;
-        const size_t at = size_t(m0 + prow) * p.O + o;  // this lane's first row; the others follow eight rows apart
-        float bias[8] = {};
-        uint4 res8[4] = {};
-        if (cols) {
-          if (p.bias) unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bias) + o), bias);
-          if (add) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (n0 + i * 8 + prow < tl.rows)
-                res8[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + at +
-                                                          size_t(8 * i) * p.O);
-          }
+        const int o = ti.o0 + cc * 32;
+        const bool live = n0 < tl.rows && o < p.O;  // the piece has outputs
+        if (add) {  // the next piece's residual, while this one is worked on
+          if (cc + 2 < nchunks) fetch(ti, cc + 2, buf ^ 1);
+          else if (t + pairs < tl.total) fetch(tile_at(tl, t + pairs), half, buf ^ 1);
         }
+        float v[32];
+        if (vec && live && bias) {
+          // the last piece of a row may end inside the bias: whole 16-byte words up to O, zeros after
+          if (o + 32 <= p.O) {
+            global_row32(bias + o, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = o + i < p.O ? __bfloat162float(bias[o + i]) : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        if (cc == half && !(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
+        tc_fence_after();
         uint32_t r[32];
         tmem_ld32(tmem + lane_off + b * 256 + cc * 32, r);
         if (cc + 2 >= nchunks) {  // last read of this accumulator by this warp
@@ -227,41 +320,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
         }
+        if (!vec) {
+          if (live) store_odd<kAct>(p, tl.rows, ti.sec, n0, o, patch, lane, r);
+          continue;
+        }
+        if (!live) {  // pieces take the two buffers in turn, each with its bulk group, an empty one here
+          if (elect_one()) bulk_commit();
+          __syncwarp();
+          buf ^= 1;
+          continue;
+        }
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + ((q ^ (lane & 7)) << 4)),
-                       "r"(r[4 * q]), "r"(r[4 * q + 1]), "r"(r[4 * q + 2]), "r"(r[4 * q + 3])
-                       : "memory");
-        __syncwarp();
-        if (vec) {
-          float v[4][8];  // all four row groups before the first store, so that their latencies overlap
+        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[i]);
+        activate<kAct>(v);
+        if (grow) {
+          float g[32];
+          if (o + 32 <= p.O) {
+            global_row32(grow + o, g);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) patch_row(patch, i * 8 + prow, pcol, v[i]);
+            for (int i = 0; i < 32; ++i) g[i] = o + i < p.O ? __bfloat162float(grow[o + i]) : 0.f;
+          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = i * 8 + prow;
-            if (cols && n0 + row < tl.rows) {
-              const __nv_bfloat16* gate = nullptr;
-              if (p.gate) gate = static_cast<const __nv_bfloat16*>(p.gate) + size_t((m0 + row) / p.N) * p.O + o;
-              finish_eight<kAct>(v[i], bias, gate, add, res8[i], static_cast<__nv_bfloat16*>(p.y) + at + size_t(8 * i) * p.O);
-            }
+          for (int i = 0; i < 32; ++i) v[i] *= g[i];
+        }
+        const uint32_t piece = patch + buf * (kPatch / 2);
+        if (add) {
+          if (!(ok = warp_all(mbar_wait(rbar + buf, (rphase >> buf) & 1, st)))) break;
+          rphase ^= 1u << buf;
+          awaited &= ~(1u << buf);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(piece_at(piece, lane, q)));
+            float t8[8];
+            unpack8(w, t8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * q + i] += t8[i];
           }
         } else {
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int row = i * 8 + prow;
-            float v[8];
-            patch_row(patch, row, pcol, v);
-            if (n0 + row < tl.rows) {
+          if (elect_one()) bulk_wait_read<1>();  // the store before the last one used this buffer
+          __syncwarp();
+        }
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (o + j < p.O) finish_one<kAct, __nv_bfloat16>(p, m0 + row, o + j, v[j]);
-            }
-          }
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece_at(piece, lane, q)), "r"(w[0]), "r"(w[1]),
+                       "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) {
+          tma_store_3d(&map_y, piece, o, n0, ti.sec);
+          bulk_commit();
         }
         __syncwarp();
+        buf ^= 1;
       }
+      if (!ok) break;
     }
+    if (!ok && awaited) settle_copies();
+    if (elect_one()) bulk_wait_all();
+    __syncwarp();
     if (!ok && lane == 0) raise_status(st, kStatusTimeout);
   }
   tc_fence_before();
@@ -273,16 +398,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int kAct>
-cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const LinearParams& p, const Tiling& t, int pairs,
+cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& my, const CUtensorMap& mr,
+                       const LinearParams& p, const Tiling& t, int pairs,
                        cudaStream_t s) {
   const cudaError_t e = allow_smem<linear_pair_kernel<kAct>>(kSmemAlloc);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(linear_pair_kernel<kAct>, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, p, t);
+  return launch_overlapped(linear_pair_kernel<kAct>, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, my, mr, p, t);
 }
 
 cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t s) {
   Tiling t{};
-  CUtensorMap mx, mw;
+  CUtensorMap mx, mw, my{}, mr{};
   bool ok;
   if (p.heads > 0) {
     const int d = p.K / p.heads;
@@ -307,13 +433,17 @@ cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t
   if (total > INT32_MAX - 1024) return cudaErrorInvalidValue;
   t.total = int(total);
   ok = ok && make_tile_map(&mw, p.w, 1, p.O, p.K, t.bn / 2);
+  if (p.O % 8 == 0) {  // otherwise the epilogue does not use them
+    ok = ok && make_patch_map(&my, p.y, t.sections, t.rows, p.O);
+    if (p.residual) ok = ok && make_patch_map(&mr, p.residual, t.sections, t.rows, p.O);
+  }
   if (!ok) return cudaErrorInvalidValue;
   const int pairs = t.total < num_sms / 2 ? t.total : num_sms / 2;
   switch (p.act) {
-    case MCS_ACT_GELU_TANH: return start_pair<MCS_ACT_GELU_TANH>(mx, mw, p, t, pairs, s);
-    case MCS_ACT_GELU_ERF: return start_pair<MCS_ACT_GELU_ERF>(mx, mw, p, t, pairs, s);
-    case MCS_ACT_SILU: return start_pair<MCS_ACT_SILU>(mx, mw, p, t, pairs, s);
-    default: return start_pair<MCS_ACT_NONE>(mx, mw, p, t, pairs, s);
+    case MCS_ACT_GELU_TANH: return start_pair<MCS_ACT_GELU_TANH>(mx, mw, my, mr, p, t, pairs, s);
+    case MCS_ACT_GELU_ERF: return start_pair<MCS_ACT_GELU_ERF>(mx, mw, my, mr, p, t, pairs, s);
+    case MCS_ACT_SILU: return start_pair<MCS_ACT_SILU>(mx, mw, my, mr, p, t, pairs, s);
+    default: return start_pair<MCS_ACT_NONE>(mx, mw, my, mr, p, t, pairs, s);
   }
 }
 

@@ -45,34 +45,6 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
 }
-// Eight consecutive bf16 outputs of one row from their sums: bias (0 where
-// absent), gate words and residual words where the pointers say so, stored at y.
-template <int kAct>
-__device__ __forceinline__ void finish_eight(float (&v)[8], const float (&bias)[8], const __nv_bfloat16* gate, bool add,
-                                             const uint4& res8, __nv_bfloat16* y) {
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] += bias[i];
-  activate<kAct>(v);
-  if (gate != nullptr) {
-    unpack8(*reinterpret_cast<const uint4*>(gate), t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= t[i];
-  }
-  if (add) {
-    unpack8(res8, t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Four consecutive bf16 outputs of one row from their sums; bias4 holds the bias
 // there (ignored where absent). Needs O % 4 == 0.
 __device__ __forceinline__ void unpack4(const uint2& w, float (&v)[4]) {
