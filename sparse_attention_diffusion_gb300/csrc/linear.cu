@@ -80,6 +80,8 @@ __device__ __forceinline__ void global_row32(const __nv_bfloat16* src, float (&v
     for (int i = 0; i < 8; ++i) v[8 * q + i] = t[i];
   }
 }
+// Address of a 16-byte piece of a patch row (rows of 64 bytes; with 128-byte rows and one
+// ring stage less for the room, the epilogue took the same time and the products longer).
 __device__ __forceinline__ uint32_t piece_at(uint32_t patch, int row, int q) {
   return patch + row * 64 + ((q ^ ((row >> 1) & 3)) << 4);
 }
@@ -452,8 +454,8 @@ cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t
 // Which kernel and tile a problem takes: the smallest estimated time, in SM
 // clocks, with constants from measured sweeps. A 64-column step of a tile costs
 // its MMAs (8,192 FLOP per clock and SM), its loads (62 bytes per clock and SM out
-// of L2) or a ring turn's latency (300), whichever is longest; tiles run in waves
-// over the SMs (or pairs); reading every operand once from HBM (23 bytes per clock
+// of L2) or a ring turn's latency (300), whichever is longest; a pair's tile is
+// never shorter than its epilogue; tiles run in waves over the SMs (or pairs); reading every operand once from HBM (23 bytes per clock
 // and SM) bounds everything; then come the start, the way out of the last tile (20
 // to 35 clocks a column or token) and the exchange between K slices.
 cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
@@ -474,7 +476,8 @@ cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
     last = bn;
     const long long tiles = row_tiles * ((p.O + bn - 1) / bn), slots = num_sms / 2;
     const double step = larger(300, larger(2.0 * bn, (16384 + 64.0 * bn) / 62));
-    const double cost = overlap(double((tiles + slots - 1) / slots) * nk * step, hbm) + 6200 + 28 * bn;
+    const double tile = larger(nk * step, 850 + 14.0 * bn);  // its products, or its way out when K is short
+    const double cost = overlap(double((tiles + slots - 1) / slots) * tile, hbm) + 6200 + 28 * bn;
     if (cost < best) best = cost, pair_bn = bn;
   }
   FewPlan few{};
