@@ -413,22 +413,33 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_bwd_kernel(con
   }
 }
 
-// dw[st][e] = sum over blocks of partial[block][st][e], in a fixed order.
+// dw[st][e] = sum over blocks of partial[block][st][e], in a fixed order: a block
+// takes 32 elements, a warp every 32nd row with eight rows in flight, then the
+// warps' sums in order.
 __global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float* partial, int nblk, int D, float* dwq,
                                                                float* dwk) {
-  __shared__ float red[1024];
-  const int st = blockIdx.x, e = threadIdx.x % D, part = threadIdx.x / D, parts = blockDim.x / D;
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, st = blockIdx.y, e = blockIdx.x * 32 + lane;
   float* dw = st == 0 ? dwq : dwk;
   grid_inputs_ready();
   grid_let_next_start();
   if (dw == nullptr) return;
+  const float* src = partial + st * D + e;
   float v = 0.f;
-  for (int i = part; i < nblk; i += parts) v += partial[(size_t(i) * 2 + st) * D + e];
-  red[threadIdx.x] = v;
+  for (int i = warp; i < nblk; i += 32 * 8) {
+    float f[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) f[u] = i + 32 * u < nblk ? src[size_t(i + 32 * u) * 2 * D] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += f[u];
+  }
+  red[warp][lane] = v;
   __syncthreads();
-  if (part == 0) {
-    for (int i = 1; i < parts; ++i) v += red[i * D + e];
-    dw[e] = v;
+  if (warp == 0) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += red[i][lane];
+    dw[e] = t;
   }
 }
 
@@ -476,7 +487,7 @@ cudaError_t launch_bwd(NormBwdParams p, int num_sms, cudaStream_t s) {
   p.by_tiles = Divisor((p.N + R::kTokens - 1) / R::kTokens);
   const cudaError_t e = launch_overlapped(norm_bwd_kernel<T, D, kHalf>, dim3(unsigned(blocks)), kThreads, 0, s, 0, p);
   if (e != cudaSuccess || (p.dw[0] == nullptr && p.dw[1] == nullptr)) return e;
-  return launch_overlapped(norm_bwd_reduce_kernel, dim3(2), 1024, 0, s, 0, p.partial, int(blocks), D, p.dw[0], p.dw[1]);
+  return launch_overlapped(norm_bwd_reduce_kernel, dim3(D / 32, 2), 1024, 0, s, 0, p.partial, int(blocks), D, p.dw[0], p.dw[1]);
 }
 
 template <typename T, int D>
