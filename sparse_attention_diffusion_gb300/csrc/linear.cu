@@ -41,10 +41,10 @@ namespace {
 constexpr int kMaxStages = 9;
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr int kHalfTile = 128 * 128;  // bytes of 128 rows x 64 columns
+constexpr int kHalfTile = 128 * 128;      // bytes of 128 rows x 64 columns
 constexpr int kRing = 6 * 2 * kHalfTile;  // six stages of the widest tile, more of narrower ones
 constexpr int kPatchOff = kRing;
-constexpr int kPatch = 32 * 32 * 4;  // two bf16 pieces, or one in fp32
+constexpr int kPatch = 32 * 32 * 4;       // two bf16 pieces, or one in fp32
 constexpr int kBarOff = kPatchOff + kEpiWarps * kPatch;
 constexpr int kSmemAlloc = kBarOff + 512 + 1024;
 constexpr int kBand = 8;
@@ -70,7 +70,7 @@ __device__ __forceinline__ Tile tile_at(const Tiling& t, int i) {
   return {rt / t.tiles, (rt % t.tiles) * 256, col * t.bn};
 }
 
-// 32 consecutive bf16 values (64 bytes) of global or shared memory as floats.
+// 32 consecutive bf16 values (64 bytes, 16-byte aligned) as floats.
 __device__ __forceinline__ void global_row32(const __nv_bfloat16* src, float (&v)[32]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -156,11 +156,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // even CTA: both CTAs' copies of a stage landed
-  uint64_t* empty = full + kMaxStages;                              // each CTA: the MMAs of a stage are done
-  uint64_t* acc_full = empty + kMaxStages;                          // [2] each CTA: accumulator written
+  uint64_t* empty = full + kMaxStages;                           // each CTA: the MMAs of a stage are done
+  uint64_t* acc_full = empty + kMaxStages;                       // [2] each CTA: accumulator written
   uint64_t* acc_empty = acc_full + 2;                            // [2] even CTA: accumulator read by both CTAs
   uint64_t* drain = acc_empty + 2;
-  uint64_t* res_full = drain + 1;  // [epilogue warp][2] residual piece landed
+  uint64_t* res_full = drain + 1;                                // [epilogue warp][2] residual piece landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 2 * kEpiWarps);
   const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
   const int rank = blockIdx.x & 1;  // of the cluster {2, 1, 1}
@@ -401,8 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 template <int kAct>
 cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& my, const CUtensorMap& mr,
-                       const LinearParams& p, const Tiling& t, int pairs,
-                       cudaStream_t s) {
+                       const LinearParams& p, const Tiling& t, int pairs, cudaStream_t s) {
   const cudaError_t e = allow_smem<linear_pair_kernel<kAct>>(kSmemAlloc);
   if (e != cudaSuccess) return e;
   return launch_overlapped(linear_pair_kernel<kAct>, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, my, mr, p, t);
@@ -455,9 +454,10 @@ cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t
 // clocks, with constants from measured sweeps. A 64-column step of a tile costs
 // its MMAs (8,192 FLOP per clock and SM), its loads (62 bytes per clock and SM out
 // of L2) or a ring turn's latency (300), whichever is longest; a pair's tile is
-// never shorter than its epilogue; tiles run in waves over the SMs (or pairs); reading every operand once from HBM (23 bytes per clock
-// and SM) bounds everything; then come the start, the way out of the last tile (20
-// to 35 clocks a column or token) and the exchange between K slices.
+// never shorter than its epilogue; tiles run in waves over the SMs (or pairs);
+// reading every operand once from HBM (23 bytes per clock and SM) bounds
+// everything; then come the start, the way out of the last tile (20 to 35 clocks a
+// column or token) and the exchange between K slices.
 cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
   const int nk = (p.K + 63) / 64;
   const long long rows = p.heads > 0 ? p.N : p.M, sections = p.heads > 0 ? p.B : 1;
