@@ -238,7 +238,7 @@ mcs_status mcs_linear(const mcs_linear_desc* desc, const void* x, const void* w,
   p.heads = desc->heads;
   p.act = desc->act;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return from_cuda(bf16 ? mcs::linear_tc(p, sms, s) : mcs::linear_simt(p, sms, s));
+  return from_cuda(bf16 ? mcs::linear_tc(p, sms, s) : mcs::linear_f32(p, sms, s));
 }
 
 }  // extern "C"

@@ -20,6 +20,8 @@ struct LinearParams {
   uint32_t* status;
 };
 cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s);
-cudaError_t linear_simt(const LinearParams& p, int num_sms, cudaStream_t s);
+// fp32: rows by the CUDA cores (up to eight) or the tensor cores in bf16 parts.
+cudaError_t linear_f32(const LinearParams& p, int num_sms, cudaStream_t s);
+cudaError_t linear_split(const LinearParams& p, int num_sms, cudaStream_t s);
 
 }  // namespace mcs

@@ -76,4 +76,31 @@ __device__ __forceinline__ void finish_four(const LinearParams& p, int m, int o,
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// Four consecutive fp32 outputs of one row from their sums (any alignment).
+template <int kAct>
+__device__ __forceinline__ void finish_row4(const LinearParams& p, int m, int o, float (&v)[4]) {
+  if (p.O % 4 != 0 || o + 4 > p.O) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (o + i < p.O) finish_one<kAct, float>(p, m, o + i, v[i]);
+    return;
+  }
+  auto at4 = [](const void* q, size_t i) { return *reinterpret_cast<const float4*>(static_cast<const float*>(q) + i); };
+  const size_t at = size_t(m) * p.O + o;
+  if (p.bias) {
+    const float4 t = at4(p.bias, o);
+    v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
+  }
+  activate<kAct>(v);
+  if (p.gate) {
+    const float4 t = at4(p.gate, size_t(m / p.N) * p.O + o);
+    v[0] *= t.x, v[1] *= t.y, v[2] *= t.z, v[3] *= t.w;
+  }
+  if (p.residual) {
+    const float4 t = at4(p.residual, at);
+    v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
+  }
+  *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
 }  // namespace mcs

@@ -1,0 +1,359 @@
+// fp32 matrix product with epilogue on the bf16 tensor cores, with fp32's accuracy.
+//
+// Every fp32 number is the exact sum of three bf16 parts, h + m + l, each the next
+// eight bits of its significand (cut off, not rounded: two integer operations and an
+// exact subtraction a part). Of the nine products of parts the six largest are
+// summed; what is left out is below 2^-21 of |x w|, 2^-24 on average. The tensor
+// core adds into its fp32 accumulator by truncation (measured on this GPU: two
+// bits below the sum's last one are kept), which over a long K would shrink the
+// sum by 2^-24 a step or more. So an accumulator takes 32 columns of K only, small
+// products first, and the epilogue's threads add it to fp32 sums in registers,
+// rounding to nearest.
+//
+// One CTA per 128 x 128 tile, 576 threads:
+//   warp 0        TMA producer: fp32 tiles of 32 columns, two stages
+//   warp 1        tensor-memory allocation and MMA issue: 12 MMAs a stage
+//   warps 2-9     cut the fp32 tiles into parts, in the layout the MMA reads: rows of
+//                 128 bytes hold h and m of the 32 columns, a second tile l
+//   warps 10-17   sums: two threads a row, 64 columns each, tensor memory double-buffered
+// Few tiles are cut along K over the CTAs of a cluster, which join their sums through
+// distributed shared memory, ranks in order, so that equal calls give equal bits.
+// An infinite element makes its outputs NaN (its lower parts are infinity less infinity).
+#include "attn_tc.h"
+#include "common.cuh"
+#include "launch.cuh"
+#include "linear.h"
+#include "linear_epi.cuh"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+#include "tma.cuh"
+
+namespace mcs {
+namespace {
+
+constexpr int kThreads = 576, kWarps = kThreads / 32;
+constexpr int kCutWarps = 8, kSumWarps = 8;
+constexpr int kBK = 32;
+constexpr int kTile = 128 * 128;            // bytes of a 128-row tile of 128-byte rows
+constexpr int kRaw = 2 * kTile;             // fp32 stage: x, w
+constexpr int kParts = 4 * kTile;           // bf16 stage: x h|m, x l, w h|m, w l
+constexpr int kPartsOff = 2 * kRaw;
+constexpr int kBarOff = kPartsOff + 2 * kParts;
+constexpr int kSmemAlloc = kBarOff + 256 + 1024;
+constexpr int kSumLd = 132;                 // floats a row of the final sums takes in shared memory
+static_assert(128 * kSumLd * 4 <= kBarOff, "the sums fit over the stages");
+
+struct SplitArgs {
+  int rows, tiles;            // rows of a section of x (as in the bf16 kernels), its row tiles
+  int col_mask, head_shift;
+  int splits;
+};
+
+// Cuts eight fp32 numbers into their parts: 16 bytes of h, m and l.
+__device__ __forceinline__ void cut8(const float4& a, const float4& b, uint4& h, uint4& m, uint4& l) {
+  const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t hw[4], mw[4], lw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t p[2], q[2], r[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float v = x[2 * i + j];
+      p[j] = __float_as_uint(v);
+      const float v1 = v - __uint_as_float(p[j] & 0xffff0000u);
+      q[j] = __float_as_uint(v1);
+      r[j] = __float_as_uint(v1 - __uint_as_float(q[j] & 0xffff0000u));
+    }
+    hw[i] = __byte_perm(p[0], p[1], 0x7632);
+    mw[i] = __byte_perm(q[0], q[1], 0x7632);
+    lw[i] = __byte_perm(r[0], r[1], 0x7632);
+  }
+  h = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+  m = make_uint4(mw[0], mw[1], mw[2], mw[3]);
+  l = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+}
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts4(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <int kAct>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_split_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                        const LinearParams p, const SplitArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // each [2]
+  uint64_t* raw_empty = raw_full + 2;
+  uint64_t* parts_full = raw_empty + 2;
+  uint64_t* parts_empty = parts_full + 2;
+  uint64_t* acc_full = parts_empty + 2;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* failed = tmem_slot + 1;  // a wait of this CTA ran out
+  const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+  const int rt = blockIdx.x / a.splits, rank = blockIdx.x % a.splits;  // of the cluster {splits, 1, 1}
+  const int sec = rt / a.tiles, row0 = (rt % a.tiles) * 128, o0 = blockIdx.y * 128;
+  const int nk = (p.K + kBK - 1) / kBK;
+  const int k_beg = int(static_cast<long long>(nk) * rank / a.splits);
+  const int steps = int(static_cast<long long>(nk) * (rank + 1) / a.splits) - k_beg;
+  uint32_t* st = p.status;
+  if (tid == 64) {
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_w);
+  }
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(raw_full + b, 1);
+      mbar_init(raw_empty + b, kCutWarps);
+      mbar_init(parts_full + b, kCutWarps);
+      mbar_init(parts_empty + b, 1);
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, kSumWarps);
+    }
+    mbar_init(drain, 1);
+    *reinterpret_cast<volatile uint32_t*>(failed) = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = warp_uniform(*tmem_slot);
+  grid_inputs_ready();
+  grid_let_next_start();
+
+  bool ok = true;
+  float2 sum[32];  // sum warps: this thread's 64 columns
+  if (warp == 0) {
+    const int z0 = sec * p.heads;
+    for (int i = 0; i < steps; ++i) {
+      const int s = i & 1;
+      if (!(ok = warp_all(mbar_wait(raw_empty + s, ((i >> 1) & 1) ^ 1, st)))) break;
+      const int k = (k_beg + i) * kBK;
+      const uint32_t dst = sbase + s * kRaw;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(raw_full + s, kRaw);
+        tma_load_3d(dst, &map_x, k & a.col_mask, row0, z0 + (k >> a.head_shift), smem_u32(raw_full + s));
+        tma_load_3d(dst + kTile, &map_w, k, o0, 0, smem_u32(raw_full + s));
+      }
+      __syncwarp();
+    }
+    if (!ok) settle_copies();  // normally the cutting warps have read every copy before the CTA exits
+  } else if (warp == 1) {
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, 128, 0, 0);
+    bool issued = false;
+    for (int i = 0; i < steps; ++i) {
+      const int s = i & 1;
+      const uint32_t phase = (i >> 1) & 1;
+      ok = warp_all(mbar_wait(parts_full + s, phase, st)) && warp_all(mbar_wait(acc_empty + s, phase ^ 1, st));
+      if (!ok) break;
+      tc_fence_after();
+      issued = true;
+      const uint32_t base = sbase + kPartsOff + s * kParts;
+      const uint32_t xhm = desc_lo_kmajor(base), xl = desc_lo_kmajor(base + kTile);
+      const uint32_t whm = desc_lo_kmajor(base + 2 * kTile), wl = desc_lo_kmajor(base + 3 * kTile);
+      if (elect_one()) {
+        const uint32_t d = tmem + s * 128;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)  // m m
+          tc_mma_ss_lo(d, xhm + kstep_kmajor(2 + ks), whm + kstep_kmajor(2 + ks), kIdesc, ks > 0 ? 1u : 0u);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)  // h l
+          tc_mma_ss_lo(d, xhm + kstep_kmajor(ks), wl + kstep_kmajor(ks), kIdesc, 1u);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)  // l h
+          tc_mma_ss_lo(d, xl + kstep_kmajor(ks), whm + kstep_kmajor(ks), kIdesc, 1u);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)  // h m
+          tc_mma_ss_lo(d, xhm + kstep_kmajor(ks), whm + kstep_kmajor(2 + ks), kIdesc, 1u);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)  // m h
+          tc_mma_ss_lo(d, xhm + kstep_kmajor(2 + ks), whm + kstep_kmajor(ks), kIdesc, 1u);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)  // h h
+          tc_mma_ss_lo(d, xhm + kstep_kmajor(ks), whm + kstep_kmajor(ks), kIdesc, 1u);
+        tc_commit(parts_empty + s);
+        tc_commit(acc_full + s);
+      }
+      __syncwarp();
+    }
+    if (!ok && issued) {
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      mbar_drain(drain, 0);
+    }
+  } else if (warp < 2 + kCutWarps) {
+    // a unit is eight numbers of a row: 16 bytes of each part; a warp takes 32 rows and two of the
+    // four units of a row, of x and of w
+    const int c = warp - 2, row = (c & 3) * 32 + lane, j0 = (c >> 2) * 2;
+    for (int i = 0; i < steps; ++i) {
+      const int s = i & 1;
+      const uint32_t phase = (i >> 1) & 1;
+      ok = warp_all(mbar_wait(raw_full + s, phase, st)) && warp_all(mbar_wait(parts_empty + s, phase ^ 1, st));
+      if (!ok) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {  // x, w
+        const uint32_t src = sbase + s * kRaw + t * kTile + row * 128;
+        const uint32_t dst = sbase + kPartsOff + s * kParts + t * 2 * kTile + row * 128;
+#pragma unroll
+        for (int j = j0; j < j0 + 2; ++j) {
+          uint4 h, m, l;
+          cut8(lds4(src + (((2 * j) ^ (row & 7)) << 4)), lds4(src + (((2 * j + 1) ^ (row & 7)) << 4)), h, m, l);
+          sts4(dst + ((j ^ (row & 7)) << 4), h);
+          sts4(dst + (((4 + j) ^ (row & 7)) << 4), m);
+          sts4(dst + kTile + ((j ^ (row & 7)) << 4), l);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(parts_full + s);
+        mbar_arrive(raw_empty + s);
+      }
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2 - kCutWarps) >> 2;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[i] = make_float2(0.f, 0.f);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i & 1;
+      if (!(ok = warp_all(mbar_wait(acc_full + s, (i >> 1) & 1, st)))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tmem + (uint32_t(quarter * 32) << 16) + s * 128 + half * 64 + c * 32, r);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          float2& v = sum[c * 16 + q];
+          const uint64_t t =
+              f2_add(f2_pack(v.x, v.y), f2_pack(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1])));
+          f2_unpack(t, v.x, v.y);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + s);
+    }
+  }
+  if (!ok && lane == 0) {
+    *reinterpret_cast<volatile uint32_t*>(failed) = 1;
+    raise_status(st, kStatusTimeout);
+  }
+  // all MMAs are done once the sum warps are (the last accumulator's commit covers them): the stages are free
+  __syncthreads();
+  if (warp >= 2 + kCutWarps) {
+    const int quarter = warp & 3, half = (warp - 2 - kCutWarps) >> 2;
+    const uint32_t at = sbase + ((quarter * 32 + lane) * kSumLd + half * 64) * 4;
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      sts4(at + q * 16, make_uint4(__float_as_uint(sum[2 * q].x), __float_as_uint(sum[2 * q].y),
+                                   __float_as_uint(sum[2 * q + 1].x), __float_as_uint(sum[2 * q + 1].y)));
+  }
+  tc_fence_before();
+  if (a.splits > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+  // sums with a failed CTA's share are not written anywhere
+  ok = true;
+  for (int r = 0; r < a.splits; ++r) {
+    uint32_t f;
+    if (a.splits == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(f) : "r"(smem_u32(failed)) : "memory");
+    else asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(f) : "r"(cluster_map(smem_u32(failed), r)) : "memory");
+    ok = ok && f == 0;
+  }
+  const int live = min(128, a.rows - row0);
+#pragma unroll 1
+  for (int r = rank + a.splits * warp; ok && r < live; r += a.splits * kWarps) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t at = sbase + (r * kSumLd + lane * 4) * 4;
+    if (a.splits == 1) {
+      const float4 f = lds4(at);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+      float f[4][4];
+      for (int c0 = 0; c0 < a.splits; c0 += 4) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f[c][0] = f[c][1] = f[c][2] = f[c][3] = 0.f;
+          if (c0 + c < a.splits)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(f[c][0]), "=f"(f[c][1]), "=f"(f[c][2]), "=f"(f[c][3])
+                         : "r"(cluster_map(at, c0 + c)));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] += f[c][i];
+      }
+    }
+    finish_row4<kAct>(p, sec * a.rows + row0 + r, o0 + lane * 4, v);
+  }
+  if (a.splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
+}
+
+template <int kAct>
+cudaError_t start(const CUtensorMap& mx, const CUtensorMap& mw, const LinearParams& p, const SplitArgs& a, dim3 grid,
+                  cudaStream_t s) {
+  const cudaError_t e = allow_smem<linear_split_kernel<kAct>>(kSmemAlloc);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(linear_split_kernel<kAct>, grid, kThreads, kSmemAlloc, s, unsigned(a.splits), mx, mw, p, a);
+}
+
+}  // namespace
+
+cudaError_t linear_split(const LinearParams& p, int num_sms, cudaStream_t s) {
+  SplitArgs a{};
+  CUtensorMap mx, mw;
+  bool ok;
+  int sections = 1;
+  if (p.heads > 0) {
+    const int d = p.K / p.heads;
+    a.head_shift = d == 64 ? 6 : 7;
+    a.col_mask = d - 1;
+    a.rows = p.N;
+    sections = p.B;
+    ok = make_tile_map_f32(&mx, p.x, uint64_t(p.B) * p.heads, p.N, d, 128);
+  } else {
+    a.head_shift = 31;
+    a.col_mask = INT32_MAX;
+    a.rows = p.M;
+    ok = make_tile_map_f32(&mx, p.x, 1, p.M, p.K, 128);
+  }
+  if (!(ok && make_tile_map_f32(&mw, p.w, 1, p.O, p.K, 128))) return cudaErrorInvalidValue;
+  a.tiles = (a.rows + 127) / 128;
+  // K slices: the shortest estimate of waves x (steps of about 900 clocks + way in and out)
+  const int nk = (p.K + kBK - 1) / kBK;
+  const long long tiles = static_cast<long long>(a.tiles) * sections * ((p.O + 127) / 128);
+  long long best = 0;
+  for (int splits = 1; splits <= 8 && splits <= nk; splits *= 2) {
+    const int slots = splits <= 2 ? num_sms : int(0.85 * num_sms) / splits * splits;
+    const long long cost = (tiles * splits + slots - 1) / slots *
+                           (static_cast<long long>((nk + splits - 1) / splits) * 900 + 6000 + (splits > 1 ? 3000 : 0));
+    if (best == 0 || cost < best) best = cost, a.splits = splits;
+  }
+  const long long gx = static_cast<long long>(a.splits) * a.tiles * sections;
+  if (gx > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid(unsigned(gx), (p.O + 127) / 128);
+  switch (p.act) {
+    case MCS_ACT_GELU_TANH: return start<MCS_ACT_GELU_TANH>(mx, mw, p, a, grid, s);
+    case MCS_ACT_GELU_ERF: return start<MCS_ACT_GELU_ERF>(mx, mw, p, a, grid, s);
+    case MCS_ACT_SILU: return start<MCS_ACT_SILU>(mx, mw, p, a, grid, s);
+    default: return start<MCS_ACT_NONE>(mx, mw, p, a, grid, s);
+  }
+}
+
+}  // namespace mcs

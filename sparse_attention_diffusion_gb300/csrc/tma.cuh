@@ -51,6 +51,19 @@ inline bool make_tile_map(CUtensorMap* m, const void* base, uint64_t BH, uint64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same over fp32 [BH, N, d]: box = 32 columns x box_rows rows x 1 head.
+inline bool make_tile_map_f32(CUtensorMap* m, const void* base, uint64_t BH, uint64_t N, int d, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(d), N, BH};
+  const cuuint64_t strides[2] = {cuuint64_t(d) * 4, cuuint64_t(d) * 4 * N};
+  const cuuint32_t box[3] = {32, cuuint32_t(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Tiled map over bf16 [BH, N, d] for epilogue patches: box = 32 columns x 32 rows x
 // 1 head, 64-byte swizzle (16-byte piece c of row r sits at piece c ^ (r / 2 % 4)).
 // Reads beyond the tensor give zeros, writes beyond it are dropped.
