@@ -11,11 +11,16 @@
 // rounding to nearest.
 //
 // One CTA per 128 x 128 tile, 576 threads:
-//   warp 0        TMA producer: fp32 tiles of 32 columns, two stages
-//   warp 1        tensor-memory allocation and MMA issue: 12 MMAs a stage
-//   warps 2-9     cut the fp32 tiles into parts, in the layout the MMA reads: rows of
-//                 128 bytes hold h and m of the 32 columns, a second tile l
-//   warps 10-17   sums: two threads a row, 64 columns each, tensor memory double-buffered
+//   warp 0        TMA producer: fp32 tiles of 32 columns, four stages
+//   warp 1        tensor-memory allocation and MMA issue: 12 MMAs a step
+//   warps 2-9     cut the fp32 tiles into parts, in the layout the MMA reads: those of x
+//                 go to tensor memory (the MMA's A operand), those of w to shared memory,
+//                 rows of 128 bytes with h and m of the 32 columns and a second tile for l
+//   warps 10-17   sums: two threads a row, 64 columns each
+// Accumulators and parts are double-buffered. Shared memory's bandwidth bounds a step:
+// 32 KB in, 32 KB read, 24 KB of parts written and 48 KB read by the MMAs, 1,088 clocks
+// at 128 bytes each, against 768 of MMAs (with the parts of x in shared memory too,
+// 1,664 clocks; 4,096 x 5,120 x 5,120 took 1.22 ms).
 // Few tiles are cut along K over the CTAs of a cluster, which join their sums through
 // distributed shared memory, ranks in order, so that equal calls give equal bits.
 // An infinite element makes its outputs NaN (its lower parts are infinity less infinity).
@@ -35,11 +40,13 @@ constexpr int kThreads = 576, kWarps = kThreads / 32;
 constexpr int kCutWarps = 8, kSumWarps = 8;
 constexpr int kBK = 32;
 constexpr int kTile = 128 * 128;            // bytes of a 128-row tile of 128-byte rows
+constexpr int kRawStages = 4;
 constexpr int kRaw = 2 * kTile;             // fp32 stage: x, w
-constexpr int kParts = 4 * kTile;           // bf16 stage: x h|m, x l, w h|m, w l
-constexpr int kPartsOff = 2 * kRaw;
+constexpr int kParts = 2 * kTile;           // bf16 stage: w h|m, w l
+constexpr int kPartsOff = kRawStages * kRaw;
 constexpr int kBarOff = kPartsOff + 2 * kParts;
 constexpr int kSmemAlloc = kBarOff + 256 + 1024;
+constexpr uint32_t kColX = 256;             // tensor memory: accumulators [0, 256), parts of x [256, 384)
 constexpr int kSumLd = 132;                 // floats a row of the final sums takes in shared memory
 static_assert(128 * kSumLd * 4 <= kBarOff, "the sums fit over the stages");
 
@@ -88,9 +95,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // each [2]
-  uint64_t* raw_empty = raw_full + 2;
-  uint64_t* parts_full = raw_empty + 2;
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + kBarOff);  // [kRawStages], like raw_empty; the others [2]
+  uint64_t* raw_empty = raw_full + kRawStages;
+  uint64_t* parts_full = raw_empty + kRawStages;
   uint64_t* parts_empty = parts_full + 2;
   uint64_t* acc_full = parts_empty + 2;
   uint64_t* acc_empty = acc_full + 2;
@@ -109,9 +116,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&map_w);
   }
   if (tid == 0) {
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kRawStages; ++b) {
       mbar_init(raw_full + b, 1);
       mbar_init(raw_empty + b, kCutWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
       mbar_init(parts_full + b, kCutWarps);
       mbar_init(parts_empty + b, 1);
       mbar_init(acc_full + b, 1);
@@ -122,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 256);
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -137,8 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     const int z0 = sec * p.heads;
     for (int i = 0; i < steps; ++i) {
-      const int s = i & 1;
-      if (!(ok = warp_all(mbar_wait(raw_empty + s, ((i >> 1) & 1) ^ 1, st)))) break;
+      const int s = i % kRawStages;
+      if (!(ok = warp_all(mbar_wait(raw_empty + s, ((i / kRawStages) & 1) ^ 1, st)))) break;
       const int k = (k_beg + i) * kBK;
       const uint32_t dst = sbase + s * kRaw;
       if (elect_one()) {
@@ -159,29 +168,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       issued = true;
-      const uint32_t base = sbase + kPartsOff + s * kParts;
-      const uint32_t xhm = desc_lo_kmajor(base), xl = desc_lo_kmajor(base + kTile);
-      const uint32_t whm = desc_lo_kmajor(base + 2 * kTile), wl = desc_lo_kmajor(base + 3 * kTile);
+      const uint32_t whm = desc_lo_kmajor(sbase + kPartsOff + s * kParts), wl = desc_lo_kmajor(sbase + kPartsOff + s * kParts + kTile);
+      const uint32_t xh = tmem + kColX + s * 64, xm = xh + 16, xl = xh + 32;
       if (elect_one()) {
         const uint32_t d = tmem + s * 128;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)  // m m
-          tc_mma_ss_lo(d, xhm + kstep_kmajor(2 + ks), whm + kstep_kmajor(2 + ks), kIdesc, ks > 0 ? 1u : 0u);
+          tc_mma_ts_lo(d, xm + ks * 8, whm + kstep_kmajor(2 + ks), kIdesc, ks > 0 ? 1u : 0u);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)  // h l
-          tc_mma_ss_lo(d, xhm + kstep_kmajor(ks), wl + kstep_kmajor(ks), kIdesc, 1u);
+        for (int ks = 0; ks < 2; ++ks) tc_mma_ts_lo(d, xh + ks * 8, wl + kstep_kmajor(ks), kIdesc, 1u);       // h l
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)  // l h
-          tc_mma_ss_lo(d, xl + kstep_kmajor(ks), whm + kstep_kmajor(ks), kIdesc, 1u);
+        for (int ks = 0; ks < 2; ++ks) tc_mma_ts_lo(d, xl + ks * 8, whm + kstep_kmajor(ks), kIdesc, 1u);      // l h
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)  // h m
-          tc_mma_ss_lo(d, xhm + kstep_kmajor(ks), whm + kstep_kmajor(2 + ks), kIdesc, 1u);
+        for (int ks = 0; ks < 2; ++ks) tc_mma_ts_lo(d, xh + ks * 8, whm + kstep_kmajor(2 + ks), kIdesc, 1u);  // h m
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)  // m h
-          tc_mma_ss_lo(d, xhm + kstep_kmajor(2 + ks), whm + kstep_kmajor(ks), kIdesc, 1u);
+        for (int ks = 0; ks < 2; ++ks) tc_mma_ts_lo(d, xm + ks * 8, whm + kstep_kmajor(ks), kIdesc, 1u);      // m h
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)  // h h
-          tc_mma_ss_lo(d, xhm + kstep_kmajor(ks), whm + kstep_kmajor(ks), kIdesc, 1u);
+        for (int ks = 0; ks < 2; ++ks) tc_mma_ts_lo(d, xh + ks * 8, whm + kstep_kmajor(ks), kIdesc, 1u);      // h h
         tc_commit(parts_empty + s);
         tc_commit(acc_full + s);
       }
@@ -193,32 +196,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_drain(drain, 0);
     }
   } else if (warp < 2 + kCutWarps) {
-    // a unit is eight numbers of a row: 16 bytes of each part; a warp takes 32 rows and two of the
-    // four units of a row, of x and of w
-    const int c = warp - 2, row = (c & 3) * 32 + lane, j0 = (c >> 2) * 2;
+    // a unit is eight numbers of a row: 16 bytes of each part; a warp takes the 32 rows of its tensor-memory
+    // lanes and two of the four units of a row, of x and of w
+    const int quarter = warp & 3, row = quarter * 32 + lane, j0 = ((warp - 2) >> 2) * 2;
     for (int i = 0; i < steps; ++i) {
-      const int s = i & 1;
-      const uint32_t phase = (i >> 1) & 1;
-      ok = warp_all(mbar_wait(raw_full + s, phase, st)) && warp_all(mbar_wait(parts_empty + s, phase ^ 1, st));
+      const int s = i & 1, rs = i % kRawStages;
+      ok = warp_all(mbar_wait(raw_full + rs, (i / kRawStages) & 1, st)) &&
+           warp_all(mbar_wait(parts_empty + s, ((i >> 1) & 1) ^ 1, st));
       if (!ok) break;
+      tc_fence_after();
+      const uint32_t src = sbase + rs * kRaw + row * 128;
+      uint4 h[2], m[2], l[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {  // x, w
-        const uint32_t src = sbase + s * kRaw + t * kTile + row * 128;
-        const uint32_t dst = sbase + kPartsOff + s * kParts + t * 2 * kTile + row * 128;
-#pragma unroll
-        for (int j = j0; j < j0 + 2; ++j) {
-          uint4 h, m, l;
-          cut8(lds4(src + (((2 * j) ^ (row & 7)) << 4)), lds4(src + (((2 * j + 1) ^ (row & 7)) << 4)), h, m, l);
-          sts4(dst + ((j ^ (row & 7)) << 4), h);
-          sts4(dst + (((4 + j) ^ (row & 7)) << 4), m);
-          sts4(dst + kTile + ((j ^ (row & 7)) << 4), l);
-        }
+      for (int u = 0; u < 2; ++u) {
+        const int j = j0 + u;
+        cut8(lds4(src + (((2 * j) ^ (row & 7)) << 4)), lds4(src + (((2 * j + 1) ^ (row & 7)) << 4)), h[u], m[u], l[u]);
       }
+      const uint32_t xt = tmem + (uint32_t(quarter * 32) << 16) + kColX + s * 64 + j0 * 4;
+      tmem_st8_nowait(xt, h[0], h[1]);
+      tmem_st8_nowait(xt + 16, m[0], m[1]);
+      tmem_st8_nowait(xt + 32, l[0], l[1]);
+      const uint32_t dst = sbase + kPartsOff + s * kParts + row * 128;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int j = j0 + u;
+        uint4 wh, wm, wl;
+        cut8(lds4(src + kTile + (((2 * j) ^ (row & 7)) << 4)), lds4(src + kTile + (((2 * j + 1) ^ (row & 7)) << 4)), wh, wm, wl);
+        sts4(dst + ((j ^ (row & 7)) << 4), wh);
+        sts4(dst + (((4 + j) ^ (row & 7)) << 4), wm);
+        sts4(dst + kTile + ((j ^ (row & 7)) << 4), wl);
+      }
+      tmem_wait_st();
+      tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(parts_full + s);
-        mbar_arrive(raw_empty + s);
+        mbar_arrive(raw_empty + rs);
       }
     }
   } else {
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
   // sums with a failed CTA's share are not written anywhere
   ok = true;
