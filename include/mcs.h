@@ -293,7 +293,8 @@ mcs_status mcs_rope_table(const mcs_rope *rope, float *table, mcs_stream stream)
  * strides xs, os (NULL: contiguous); out may be x with equal strides. One pass,
  * fp32 arithmetic, one rounding. Errors: MCS_ERR_INVALID_ARG for a bad pointer,
  * stride or grid (the grid must fit in N), MCS_ERR_UNSUPPORTED for a rope
- * outside the set above. desc->C, scale and pddp_iters have no effect here. */
+ * outside the set above. desc->C (which must be valid), scale and pddp_iters have no
+ * effect here. */
 mcs_status mcs_rope_apply(const mcs_desc *desc, const mcs_rope *rope, const float *table, const int32_t *pos,
                           const void *x, const mcs_strides *xs, void *out, const mcs_strides *os, int inverse,
                           mcs_stream stream);
@@ -319,7 +320,9 @@ mcs_status mcs_qk_norm_rope(const mcs_desc *desc, const mcs_rope *rope, const fl
  * Sums are fp32 in a fixed order: equal calls give equal bits. Tokens with a
  * position out of range are left unwritten, flagged, and add nothing to dwq, dwk.
  * ws: at least mcs_qk_norm_rope_bwd_workspace_size(desc) bytes (0 for an invalid
- * description); calls that may run at the same time need one each. */
+ * description); calls that may run at the same time need one each. Rows whose sum of
+ * squares overflows fp32 (elements beyond 1e18) count as infinitely long here and in
+ * mcs_qk_norm_rope: their normalised values are 0. */
 size_t mcs_qk_norm_rope_bwd_workspace_size(const mcs_desc *desc);
 mcs_status mcs_qk_norm_rope_bwd(const mcs_desc *desc, const mcs_rope *rope, const float *table, const int32_t *pos,
                                 const void *q, const void *k, const mcs_strides *in, const void *wq, const void *wk,
@@ -337,8 +340,12 @@ mcs_status mcs_qk_norm_rope_bwd(const mcs_desc *desc, const mcs_rope *rope, cons
  * mcs_act; MCS_ACT_GELU_TANH is z / (1 + exp(-2 sqrt(2/pi) (z + 0.044715 z^3))),
  * MCS_ACT_GELU_ERF z/2 (1 + erf(z / sqrt 2)), MCS_ACT_SILU z / (1 + exp(-z)).
  * Supported: in a multiple of 8 (BF16) or 4 (F32), out any; in, out <= 2^20,
- * B * N < 2^31 - 256, else MCS_ERR_UNSUPPORTED. BF16 runs on the tensor cores,
- * F32 in fp32 SIMT arithmetic. No workspace. Equal calls give equal bits. */
+ * B * N < 2^31 - 256, else MCS_ERR_UNSUPPORTED. BF16 runs on the tensor cores.
+ * F32 with up to eight rows (B * N) runs in fp32 on the CUDA cores, with more on the
+ * tensor cores, every number as the exact sum of three bf16 parts: a sum's error
+ * stays below (19 * 2^-23 + (in / 32 + 1) * 2^-24) * sum |x w|, infinite elements
+ * give NaN, and parts below fp32's normal range may count as 0. No workspace. Equal
+ * calls give equal bits. */
 typedef enum { MCS_ACT_NONE = 0, MCS_ACT_GELU_TANH = 1, MCS_ACT_GELU_ERF = 2, MCS_ACT_SILU = 3 } mcs_act;
 typedef struct {
   int B, N;

@@ -3,9 +3,9 @@
 // Every fp32 number is the exact sum of three bf16 parts, h + m + l, each the next
 // eight bits of its significand (cut off, not rounded: two integer operations and an
 // exact subtraction a part). Of the nine products of parts the six largest are
-// summed; what is left out is below 2^-21 of |x w|, 2^-24 on average. The tensor
-// core adds into its fp32 accumulator by truncation (measured on this GPU: two
-// bits below the sum's last one are kept), which over a long K would shrink the
+// summed; what is left out is below 2^-20 of |x w|, about 2^-24 on average. The
+// tensor core adds into its fp32 accumulator by truncation (measured on this GPU:
+// two bits below the sum's last one are kept), which over a long K would shrink the
 // sum by 2^-24 a step or more. So an accumulator takes 32 columns of K only, small
 // products first, and the epilogue's threads add it to fp32 sums in registers,
 // rounding to nearest.
@@ -24,6 +24,11 @@
 // Few tiles are cut along K over the CTAs of a cluster, which join their sums through
 // distributed shared memory, ranks in order, so that equal calls give equal bits.
 // An infinite element makes its outputs NaN (its lower parts are infinity less infinity).
+//
+// Measured: 4,096 x 5,120 -> 5,120 outputs 0.88 ms (243 TFLOP/s; 1,170 clocks a step;
+// the CUDA cores' 128 x 128 tiles of packed FMAs took 3.89 ms), 1,024 x 1,536 -> 1,536 33
+// us, 300 x 3,200 -> 320 15 us in eight slices; relative error of the result 1.0e-7 to
+// 1.9e-7 over K = 32 .. 5,120 (fp32 FMAs in order: 0.8e-7 to 7e-7).
 #include "attn_tc.h"
 #include "common.cuh"
 #include "launch.cuh"
@@ -168,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       issued = true;
-      const uint32_t whm = desc_lo_kmajor(sbase + kPartsOff + s * kParts), wl = desc_lo_kmajor(sbase + kPartsOff + s * kParts + kTile);
+      const uint32_t base = sbase + kPartsOff + s * kParts;
+      const uint32_t whm = desc_lo_kmajor(base), wl = desc_lo_kmajor(base + kTile);
       const uint32_t xh = tmem + kColX + s * 64, xm = xh + 16, xl = xh + 32;
       if (elect_one()) {
         const uint32_t d = tmem + s * 128;
@@ -349,14 +355,14 @@ cudaError_t linear_split(const LinearParams& p, int num_sms, cudaStream_t s) {
   }
   if (!(ok && make_tile_map_f32(&mw, p.w, 1, p.O, p.K, 128))) return cudaErrorInvalidValue;
   a.tiles = (a.rows + 127) / 128;
-  // K slices: the shortest estimate of waves x (steps of about 900 clocks + way in and out)
+  // K slices: the shortest estimate of waves x (steps of about 1,150 clocks + way in and out)
   const int nk = (p.K + kBK - 1) / kBK;
   const long long tiles = static_cast<long long>(a.tiles) * sections * ((p.O + 127) / 128);
   long long best = 0;
   for (int splits = 1; splits <= 8 && splits <= nk; splits *= 2) {
     const int slots = splits <= 2 ? num_sms : int(0.85 * num_sms) / splits * splits;
     const long long cost = (tiles * splits + slots - 1) / slots *
-                           (static_cast<long long>((nk + splits - 1) / splits) * 900 + 6000 + (splits > 1 ? 3000 : 0));
+                           (static_cast<long long>((nk + splits - 1) / splits) * 1150 + 6000 + (splits > 1 ? 3000 : 0));
     if (best == 0 || cost < best) best = cost, a.splits = splits;
   }
   const long long gx = static_cast<long long>(a.splits) * a.tiles * sections;
