@@ -105,11 +105,6 @@ __device__ __forceinline__ T warp_uniform(T v) {
 }
 
 // ---------------------------------------------------------------- clusters
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 // All threads of all CTAs of the cluster; shared-memory writes before it are
 // visible to the other CTAs after it.
 __device__ __forceinline__ void cluster_sync() {
