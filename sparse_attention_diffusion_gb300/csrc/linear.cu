@@ -25,6 +25,13 @@
 // tile's epilogue runs under the next tile's products. Tiles are walked in bands
 // of eight row tiles, column by column, which keeps the band's x rows and the
 // current columns of w in L2.
+//
+// Measured: 32,768 x 1,536 -> 4,608 outputs 237 us alone (1,954 TFLOP/s, tensor pipe
+// 93 % active) and 276 us back to back under the power cap (1,680); 75,600 x 5,120 ->
+// 5,120 from heads with gated residual 2.34 ms (1,696). A k step of 256 columns needs
+// 64 bytes per clock and SM of operands, about what an SM takes in (62 measured), so
+// the tensor pipe and the operand port run out together; tiles of 128 x 128 on single
+// CTAs (twice the bytes per FLOP), without epilogue overlap, took 2,423 us and 10.9 ms.
 #include "attn_tc.h"
 #include "common.cuh"
 #include "linear.h"
