@@ -17,8 +17,8 @@
 //
 // Measured against the copy bandwidth of 6,783 GB/s (bf16, d = 128): rotation of 40 heads x
 // 75,600 tokens 224 us (1.02 of it), norm + rotation + repacking of its q, k, v 680 us
-// (1.01), of 12 heads x 32,768 tokens 93 us (0.96); gradient of the latter 139 us (0.85)
-// and of the former 0.93 ms (0.98).
+// (1.01), of 12 heads x 32,768 tokens 93 us (0.96); gradient of the latter 134 us (0.89)
+// and of the former 0.93 ms (0.99).
 #include "rope.h"
 
 #include "common.cuh"
