@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_bwd_kernel(con
               s0 += __shfl_xor_sync(0xffffffffu, s0, o);
               d0 += __shfl_xor_sync(0xffffffffu, d0, o);
             }
-            const float rstd = rsqrtf(s0 * (1.f / D) + p.eps), k = -rstd * rstd * rstd * d0 * (1.f / D);
+            const float rstd = rsqrtf(s0 * (1.f / D) + p.eps);
+            const float k = -(rstd * d0 * (1.f / D)) * rstd * rstd;  // in this order no power of rstd leaves the range
             const uint64_t r2 = f2_pack(rstd, rstd), k2 = f2_pack(k, k);
 #pragma unroll
             for (int j = 0; j < N2; ++j) {
