@@ -256,7 +256,7 @@ mcs_status mcs_residual_apply(const mcs_desc *desc, const void *o_sparse, const 
  * elements (i, i + R / 2) for MCS_ROPE_HALF. Elements from R on do not turn.
  * dims: even, at least 2, R <= d (R == d for MCS_ROPE_HALF); len: positions per
  * axis, each at least 1; unused axes (index >= axes) are ignored. start and
- * scale may be fractional. Angles are computed in 64 bits.
+ * scale may be fractional. Angles are computed in 64 bits and have to be finite.
  * Positions of tokens, with pos == NULL: tokens first .. first + len[0] * len[1]
  * * len[2] - 1 are the grid in (t, y, x) order, the last axis fastest, and the
  * other tokens (a text prefix or suffix) do not turn. With pos: int32 [B, N,

@@ -28,6 +28,9 @@ mcs_status check_rope(const mcs_rope* r, mcs::RopeGeom* g, long long* entries) {
     if (r->dims[a] < 2 || r->dims[a] % 2 != 0 || r->dims[a] > 128) return MCS_ERR_UNSUPPORTED;
     if (r->len[a] < 1) return MCS_ERR_INVALID_ARG;
     if (!std::isfinite(r->start[a]) || !std::isfinite(r->scale[a])) return MCS_ERR_INVALID_ARG;
+    // the largest angle: theta^(-2 j / dims) lies between 1 and 1 / theta
+    const double f = r->theta < 1.0 ? 1.0 / r->theta : 1.0;
+    if (!std::isfinite((std::fabs(r->start[a]) + r->len[a]) * std::fabs(r->scale[a]) * f)) return MCS_ERR_INVALID_ARG;
     g->pairs[a] = r->dims[a] / 2;
     g->len[a] = r->len[a];
     g->by[a] = mcs::Divisor(r->len[a]);

@@ -186,3 +186,10 @@ def test_binding_refuses_host_and_misshapen_tensors():
         mcs.mcs_linear(ld, x, w, None, torch.empty(1, 96, dtype=torch.bfloat16), None, y)
     with pytest.raises(ValueError, match="device tensors"):
         mcs.mcs_linear(ld, x, w, None, None, None, y)
+
+
+@pytest.mark.parametrize("kw", [dict(start=(1e308, 0, 0), scale=(100.0, 1, 1)), dict(theta=1e-307, start=(1e10, 0, 0))])
+def test_infinite_angles(lib, kw):
+    r = rope(**kw)
+    assert lib.mcs_rope_table_size(ctypes.byref(r)) == 0
+    assert lib.mcs_rope_table(ctypes.byref(r), A, None) == INVALID
