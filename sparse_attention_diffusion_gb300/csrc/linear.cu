@@ -34,6 +34,7 @@
 // CTAs (twice the bytes per FLOP), without epilogue overlap, took 2,423 us and 10.9 ms.
 #include "attn_tc.h"
 #include "common.cuh"
+#include "divisor.h"
 #include "linear.h"
 #include "linear_epi.cuh"
 #include "launch.cuh"
@@ -65,24 +66,25 @@ struct Tiling {
   int bn, cols;
   int stages, stage_bytes;
   int total;
+  Divisor by_band, by_tail, by_tiles, by_batch;  // by kBand * cols, the last band's rows, tiles, rows of a batch
 };
 struct Tile {
   int sec, row0, o0;
 };
 __device__ __forceinline__ Tile tile_at(const Tiling& t, int i) {
-  const int nrt = t.tiles * t.sections;
-  const int band = i / (kBand * t.cols), rem = i - band * kBand * t.cols;
-  const int rows = min(kBand, nrt - band * kBand);
-  const int col = rem / rows, rt = band * kBand + rem % rows;
-  return {rt / t.tiles, (rt % t.tiles) * 256, col * t.bn};
+  const int band = t.by_band.div(i), rem = i - band * kBand * t.cols;
+  const int rows = min(kBand, t.tiles * t.sections - band * kBand);
+  const int col = rows == kBand ? rem / kBand : t.by_tail.div(rem);
+  const int rt = band * kBand + rem - col * rows, sec = t.by_tiles.div(rt);
+  return {sec, (rt - sec * t.tiles) * 256, col * t.bn};
 }
 
-// 32 consecutive bf16 values (64 bytes, 16-byte aligned) as floats.
-__device__ __forceinline__ void global_row32(const __nv_bfloat16* src, float (&v)[32]) {
+// Values o .. o + 31 of a bf16 row of `len`, a multiple of 8 (16-byte aligned at o), as floats; 0 past its end.
+__device__ __forceinline__ void row32(const __nv_bfloat16* row, int o, int len, float (&v)[32]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    float t[8];
-    unpack8(reinterpret_cast<const uint4*>(src)[q], t);
+    float t[8] = {};
+    if (o + 8 * q < len) unpack8(*reinterpret_cast<const uint4*>(row + o + 8 * q), t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[8 * q + i] = t[i];
   }
@@ -294,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Tile ti = tile_at(tl, t);
       const int n0 = ti.row0 + rank * 128 + quarter * 32;
       const int n = n0 + lane, m = ti.sec * tl.rows + n;  // this lane's row
-      const __nv_bfloat16* grow = gate ? gate + size_t(n < tl.rows ? m / p.N : 0) * p.O : nullptr;
+      const __nv_bfloat16* grow = gate ? gate + size_t(n < tl.rows ? tl.by_batch.div(m) : 0) * p.O : nullptr;
       if (half >= nchunks) {  // nothing of this accumulator for this warp
         if (!(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
         if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
@@ -308,18 +310,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else if (t + pairs < tl.total) fetch(tile_at(tl, t + pairs), half, buf ^ 1);
         }
         float v[32];
-        if (vec && live && bias) {
-          // the last piece of a row may end inside the bias: whole 16-byte words up to O, zeros after
-          if (o + 32 <= p.O) {
-            global_row32(bias + o, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = o + i < p.O ? __bfloat162float(bias[o + i]) : 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
+        const bool biased = vec && live && bias != nullptr;
+        if (biased) row32(bias, o, p.O, v);
         if (cc == half && !(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
         tc_fence_after();
         uint32_t r[32];
@@ -340,16 +332,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           continue;
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[i]);
+        for (int i = 0; i < 32; ++i) v[i] = biased ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
         activate<kAct>(v);
         if (grow) {
           float g[32];
-          if (o + 32 <= p.O) {
-            global_row32(grow + o, g);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) g[i] = o + i < p.O ? __bfloat162float(grow[o + i]) : 0.f;
-          }
+          row32(grow, o, p.O, g);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= g[i];
         }
@@ -440,6 +427,11 @@ cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t
   const long long total = static_cast<long long>(t.tiles) * t.sections * t.cols;
   if (total > INT32_MAX - 1024) return cudaErrorInvalidValue;
   t.total = int(total);
+  const int tail = t.tiles * t.sections % kBand;
+  t.by_band = Divisor(kBand * t.cols);
+  t.by_tail = Divisor(tail > 0 ? tail : kBand);
+  t.by_tiles = Divisor(t.tiles);
+  t.by_batch = Divisor(p.N);
   ok = ok && make_tile_map(&mw, p.w, 1, p.O, p.K, t.bn / 2);
   if (p.O % 8 == 0) {  // otherwise the epilogue does not use them
     ok = ok && make_patch_map(&my, p.y, t.sections, t.rows, p.O);
