@@ -340,7 +340,8 @@ mcs_status mcs_qk_norm_rope_bwd(const mcs_desc *desc, const mcs_rope *rope, cons
  * mcs_act; MCS_ACT_GELU_TANH is z / (1 + exp(-2 sqrt(2/pi) (z + 0.044715 z^3))),
  * MCS_ACT_GELU_ERF z/2 (1 + erf(z / sqrt 2)), MCS_ACT_SILU z / (1 + exp(-z)).
  * Supported: in a multiple of 8 (BF16) or 4 (F32), out any; in, out <= 2^20,
- * B * N < 2^31 - 256, else MCS_ERR_UNSUPPORTED. BF16 runs on the tensor cores.
+ * B * N < 2^31 - 256, else MCS_ERR_UNSUPPORTED. BF16 runs on the tensor cores: a sum's
+ * error stays below (504 * 2^-23 + (in / 1024 + 9) * 2^-24) * sum |x w|.
  * F32 with up to eight rows (B * N) runs in fp32 on the CUDA cores, with more on the
  * tensor cores, every number as the exact sum of three bf16 parts: a sum's error
  * stays below (19 * 2^-23 + (in / 32 + 1) * 2^-24) * sum |x w|, infinite elements

@@ -22,7 +22,8 @@
 //                no multiple of 16 bytes go through the patch in fp32 and leave by
 //                plain stores along the row)
 // The accumulator is double-buffered in tensor memory (2 x 256 columns), so a
-// tile's epilogue runs under the next tile's products. Tiles are walked in bands
+// tile's epilogue runs under the next tile's products. A long row takes several
+// accumulators (linear.h), which the epilogue's warps sum in registers meanwhile. Tiles are walked in bands
 // of eight row tiles, column by column, which keeps the band's x rows and the
 // current columns of w in L2.
 //
@@ -79,15 +80,39 @@ __device__ __forceinline__ Tile tile_at(const Tiling& t, int i) {
   return {sec, (rt - sec * t.tiles) * 256, col * t.bn};
 }
 
-// Values o .. o + 31 of a bf16 row of `len`, a multiple of 8 (16-byte aligned at o), as floats; 0 past its end.
-__device__ __forceinline__ void row32(const __nv_bfloat16* row, int o, int len, float (&v)[32]) {
+// Values o .. o + 31 of a bf16 row of `len`, a multiple of 8 (16-byte aligned at o); 0 past its end.
+struct Words32 {
+  uint4 w[4];
+};
+__device__ __forceinline__ Words32 row32(const __nv_bfloat16* row, int o, int len) {
+  Words32 r;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float t[8] = {};
-    if (o + 8 * q < len) unpack8(*reinterpret_cast<const uint4*>(row + o + 8 * q), t);
+  for (int q = 0; q < 4; ++q) r.w[q] = o + 8 * q < len ? *reinterpret_cast<const uint4*>(row + o + 8 * q) : uint4{};
+  return r;
+}
+// Adds 32 columns of tensor memory to fp32 sums, 16 at a time where 32 more registers would be spilled.
+template <int kCols>
+__device__ __forceinline__ void add_tmem32(uint32_t at, float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[8 * q + i] = t[i];
+  for (int h = 0; h < 32; h += kCols) {
+    uint32_t r[kCols];
+    if constexpr (kCols == 16) tmem_ld16(at + h, r);
+    else tmem_ld32(at, r);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[h + i] += __uint_as_float(r[i]);
   }
+}
+__device__ __forceinline__ void get_tmem32(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld32(at, r);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void put_tmem32(uint32_t at, const float (&v)[32]) {  // complete after tmem_wait_st
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  tmem_st32_nowait(at, r);
 }
 // Address of a 16-byte piece of a patch row (rows of 64 bytes; with 128-byte rows and one
 // ring stage less for the room, the epilogue took the same time and the products longer).
@@ -100,11 +125,11 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t patch, int row, int q) {
 // 4-byte stores).
 template <int kAct>
 __device__ __forceinline__ void store_odd(const LinearParams& p, int rows, int sec, int n0, int o, uint32_t patch,
-                                          int lane, const uint32_t (&r)[32]) {
+                                          int lane, const float (&r)[32]) {
 #pragma unroll
   for (int q = 0; q < 8; ++q)
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + ((q ^ (lane & 7)) << 4)),
-                 "r"(r[4 * q]), "r"(r[4 * q + 1]), "r"(r[4 * q + 2]), "r"(r[4 * q + 3])
+                 "f"(r[4 * q]), "f"(r[4 * q + 1]), "f"(r[4 * q + 2]), "f"(r[4 * q + 3])
                  : "memory");
   __syncwarp();
   auto sum = [&](int row, int c) {
@@ -156,7 +181,9 @@ __device__ __forceinline__ void store_odd(const LinearParams& p, int rows, int s
   __syncwarp();
 }
 
-template <int kAct>
+// kPieces: 0 for rows of one accumulator; otherwise the pieces of 32 columns that a warp sums in registers, 3 or 4
+// (tiles of up to 192 and 256 columns).
+template <int kAct, int kPieces>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_r,
@@ -171,6 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* drain = acc_empty + 2;
   uint64_t* res_full = drain + 1;                                // [epilogue warp][2] residual piece landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 2 * kEpiWarps);
+  constexpr bool kLong = kPieces > 0;
   const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
   const int rank = blockIdx.x & 1;  // of the cluster {2, 1, 1}
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -232,12 +260,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       const uint32_t idesc = idesc_bf16_f32(256, 0, 0, 0) | (uint32_t(tl.bn >> 3) << 17);
       bool ok = true, issued = false;
-      int s = 0, it = 0;
+      int s = 0, it = 0, b = 0;  // ring stage, accumulators begun, the current one's buffer
       uint32_t phase = 0;
-      for (int t = pair; t < tl.total && ok; t += pairs, ++it) {
-        const int b = it & 1;
-        if (!(ok = warp_all(mbar_wait(acc_empty + b, ((it >> 1) & 1) ^ 1, st)))) break;
+      for (int t = pair; t < tl.total && ok; t += pairs) {
         for (int i = 0; i < nk; ++i) {
+          const int step = kLong ? i % kAccSteps : i;
+          if (step == 0) {
+            b = it & 1;
+            if (!(ok = warp_all(mbar_wait(acc_empty + b, ((it++ >> 1) & 1) ^ 1, st)))) break;
+          }
           if (!(ok = warp_all(mbar_wait(full + s, phase, st)))) break;
           tc_fence_after();
           issued = true;
@@ -247,9 +278,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               tc_mma_ss_lo_pair(tmem + b * 256, a + kstep_kmajor(ks), w + kstep_kmajor(ks), idesc,
-                                (i > 0 || ks > 0) ? 1u : 0u);
+                                (step > 0 || ks > 0) ? 1u : 0u);
             tc_commit_pair(empty + s);
-            if (i == nk - 1) tc_commit_pair(acc_full + b);
+            if ((kLong && step == kAccSteps - 1) || i == nk - 1) tc_commit_pair(acc_full + b);
           }
           __syncwarp();
           if (++s == tl.stages) s = 0, phase ^= 1;
@@ -292,16 +323,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     if (add && pair < tl.total && half < nchunks) fetch(tile_at(tl, pair), half, 0);
     for (int t = pair; t < tl.total; t += pairs, ++it) {
+      if constexpr (kLong) {
+        // the accumulators of the row are summed in registers; the sums take the last one's place in tensor memory
+        // and leave from there as those of a short row do
+        float sum[kPieces][32];
+        for (int i = 0;; i += kAccSteps, ++it) {
+          const int b = it & 1;
+          const bool last = i + kAccSteps >= nk;
+          if (!(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c) {
+            if (half + 2 * c >= nchunks) continue;
+            const uint32_t at = tmem + lane_off + b * 256 + (half + 2 * c) * 32;
+            if (i == 0) get_tmem32(at, sum[c]);
+            else add_tmem32<kPieces == 4 ? 16 : 32>(at, sum[c]);
+            if (last) put_tmem32(at, sum[c]);
+          }
+          if (last) {
+            tmem_wait_st();
+            break;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
+        }
+        if (!ok) break;
+      }
       const int b = it & 1;
+      if (half >= nchunks) {  // nothing of this accumulator for this warp
+        if (!kLong && !(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
+        if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
+        continue;
+      }
       const Tile ti = tile_at(tl, t);
       const int n0 = ti.row0 + rank * 128 + quarter * 32;
       const int n = n0 + lane, m = ti.sec * tl.rows + n;  // this lane's row
       const __nv_bfloat16* grow = gate ? gate + size_t(n < tl.rows ? tl.by_batch.div(m) : 0) * p.O : nullptr;
-      if (half >= nchunks) {  // nothing of this accumulator for this warp
-        if (!(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
-        if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
-        continue;
-      }
+#pragma unroll 1
       for (int cc = half; cc < nchunks; cc += 2) {
         const int o = ti.o0 + cc * 32;
         const bool live = n0 < tl.rows && o < p.O;  // the piece has outputs
@@ -309,20 +368,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (cc + 2 < nchunks) fetch(ti, cc + 2, buf ^ 1);
           else if (t + pairs < tl.total) fetch(tile_at(tl, t + pairs), half, buf ^ 1);
         }
-        float v[32];
         const bool biased = vec && live && bias != nullptr;
-        if (biased) row32(bias, o, p.O, v);
-        if (cc == half && !(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
+        Words32 bw;
+        if (biased) bw = row32(bias, o, p.O);
+        if (!kLong && cc == half && !(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
         tc_fence_after();
-        uint32_t r[32];
-        tmem_ld32(tmem + lane_off + b * 256 + cc * 32, r);
+        float v[32];
+        get_tmem32(tmem + lane_off + b * 256 + cc * 32, v);
         if (cc + 2 >= nchunks) {  // last read of this accumulator by this warp
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
         }
         if (!vec) {
-          if (live) store_odd<kAct>(p, tl.rows, ti.sec, n0, o, patch, lane, r);
+          if (live) store_odd<kAct>(p, tl.rows, ti.sec, n0, o, patch, lane, v);
           continue;
         }
         if (!live) {  // pieces take the two buffers in turn, each with its bulk group, an empty one here
@@ -331,14 +390,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           buf ^= 1;
           continue;
         }
+        if (biased) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = biased ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+          for (int q = 0; q < 4; ++q) {
+            float t8[8];
+            unpack8(bw.w[q], t8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * q + i] += t8[i];
+          }
+        }
         activate<kAct>(v);
         if (grow) {
-          float g[32];
-          row32(grow, o, p.O, g);
+          const Words32 gw = row32(grow, o, p.O);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= g[i];
+          for (int q = 0; q < 4; ++q) {
+            float t8[8];
+            unpack8(gw.w[q], t8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * q + i] *= t8[i];
+          }
         }
         const uint32_t piece = patch + buf * (kPatch / 2);
         if (add) {
@@ -396,9 +466,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int kAct>
 cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& my, const CUtensorMap& mr,
                        const LinearParams& p, const Tiling& t, int pairs, cudaStream_t s) {
-  const cudaError_t e = allow_smem<linear_pair_kernel<kAct>>(kSmemAlloc);
-  if (e != cudaSuccess) return e;
-  return launch_overlapped(linear_pair_kernel<kAct>, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, my, mr, p, t);
+  auto start = [&](auto kern, cudaError_t e) {
+    return e != cudaSuccess ? e : launch_overlapped(kern, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, my, mr, p, t);
+  };
+  if (p.K <= 64 * kOneAccSteps) return start(linear_pair_kernel<kAct, 0>, allow_smem<linear_pair_kernel<kAct, 0>>(kSmemAlloc));
+  return t.bn <= 192 ? start(linear_pair_kernel<kAct, 3>, allow_smem<linear_pair_kernel<kAct, 3>>(kSmemAlloc))
+                     : start(linear_pair_kernel<kAct, 4>, allow_smem<linear_pair_kernel<kAct, 4>>(kSmemAlloc));
 }
 
 cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t s) {
@@ -489,13 +562,15 @@ cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
     const long long tiles = otiles * sections * ((rows + bn - 1) / bn);
     const double step = larger(300, larger(2.0 * bn, (16384 + 128.0 * bn) / 62));
     for (int splits = 1; splits <= 8 && splits <= nk; ++splits) {
+      const int steps = (nk + splits - 1) / splits;
+      if (!few_fits(bn, steps)) continue;
       const int slots = few_slots(splits, num_sms);
       if (splits > 4 && tiles * splits > 64) break;  // clusters of more than four start late on a busy GPU
       // each CTA's way out is exposed once a wave, unless two CTAs share an SM
       const double waves = double((tiles * splits + slots - 1) / slots);
       const double out = splits > 1 ? 3500 + 20 * bn : 35 * bn;
-      const double cost = overlap(waves * ((nk + splits - 1) / splits) * step, hbm) + 6000 +
-                          out * (few_two_per_sm(bn) ? 1.0 : waves);
+      const double cost = overlap(waves * steps * step, hbm) + 6000 +
+                          out * (few_two_per_sm(bn, steps) ? 1.0 : waves);
       if (cost < best) {
         best = cost;
         few.bn = bn;

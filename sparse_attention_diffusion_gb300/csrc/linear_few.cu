@@ -3,11 +3,12 @@
 // do not fill the GPU. The operands are exchanged, so that the 128 lanes of the
 // tensor core take 128 rows of w (outputs) and the rows of x (tokens, 16 to 256
 // of them) are the MMA's N; K is cut into S slices, one per CTA of a cluster.
-// Each CTA streams its slice of w through a ring of TMA stages into an fp32
-// accumulator [128 outputs x tokens] in tensor memory and leaves it in its shared
-// memory; after a cluster barrier every CTA sums a share of the tokens over the S
-// partial accumulators (distributed shared memory, ranks in order, so that equal
-// calls give equal bits) and applies the epilogue. No workspace, one launch.
+// Each CTA streams its slice of w through a ring of TMA stages into fp32
+// accumulators [128 outputs x tokens] in tensor memory (one for up to 1,536 columns,
+// linear.h) and leaves their sum in its shared memory; after a cluster barrier every
+// CTA adds a share of the tokens over the S partial sums (distributed shared memory,
+// ranks in order, so that equal calls give equal bits) and applies the epilogue. No
+// workspace, one launch.
 // Measured: 2 rows x 5,120 -> 30,720 outputs (315 MB of w) 48 us = 0.96 of the copy
 // bandwidth; back to back, 1 x 5,120 -> 5,120 13 us with three slices (18 with one),
 // 64 x 1,536 -> 1,536 6.3 us, 200 x 5,120 -> 1,000 10 us with four slices (19 with one).
@@ -35,6 +36,7 @@ struct FewArgs {
   int rows, tiles, sections;  // rows of a section of x, its token tiles
   int col_mask, head_shift;   // column k of x is column k & col_mask of head k >> head_shift (token-major: one head)
   int bn, stages, splits;
+  int accs, acc_cols;         // accumulators of the longest slice, their columns in tensor memory
   uint32_t tmem_cols;
 };
 
@@ -98,8 +100,9 @@ __device__ __forceinline__ void final_sums(const LinearParams& p, const FewArgs&
   }
 }
 
-template <int kAct>
-__global__ void __launch_bounds__(kThreads)
+// kTurns: two accumulators take turns and their sums are kept in registers; otherwise all stay until the end.
+template <int kAct, bool kTurns>
+__global__ void __launch_bounds__(kThreads, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                       const LinearParams p, const FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -108,8 +111,9 @@ __global__ void __launch_bounds__(kThreads)
   const int stage_bytes = kWTile + a.bn * 128;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.stages * stage_bytes);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* done = empty + kMaxStages;
-  uint64_t* drain = done + 1;
+  uint64_t* acc_full = empty + kMaxStages;  // [2] accumulator written (the first: all of them, if they stay)
+  uint64_t* acc_empty = acc_full + 2;       // [2] accumulator read
+  uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* failed = tmem_slot + 1;  // a wait of this CTA ran out
   const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
@@ -118,6 +122,8 @@ __global__ void __launch_bounds__(kThreads)
   const int nk = (p.K + 63) / 64;
   const int k_beg = int(static_cast<long long>(nk) * rank / a.splits);
   const int k_end = int(static_cast<long long>(nk) * (rank + 1) / a.splits);
+  const int per_acc = a.accs > 1 ? kAccSteps : kOneAccSteps;  // k steps; a.accs: of the longest slice
+  const int accs = (k_end - k_beg + per_acc - 1) / per_acc;
   uint32_t* st = p.status;
   if (tid == 64) {
     tma_prefetch_map(&map_w);
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
-    mbar_init(done, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(acc_full + b, 1), mbar_init(acc_empty + b, 4);
     mbar_init(drain, 1);
     *failed = 0;
     fence_mbar_init();
@@ -171,7 +177,10 @@ __global__ void __launch_bounds__(kThreads)
     bool issued = false;
     int s = 0;
     uint32_t phase = 0;
+    int step = 0, c = 0;  // k steps in the accumulator c
     for (int i = k_beg; i < k_end; ++i) {
+      const int b = kTurns ? c & 1 : c;
+      if (kTurns && step == 0 && !(ok = warp_all(mbar_wait(acc_empty + b, ((c >> 1) & 1) ^ 1, st)))) break;
       if (!(ok = warp_all(mbar_wait(full + s, phase, st)))) break;
       tc_fence_after();
       issued = true;
@@ -180,12 +189,14 @@ __global__ void __launch_bounds__(kThreads)
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          tc_mma_ss_lo(tmem, w + kstep_kmajor(ks), x + kstep_kmajor(ks), idesc, (i > k_beg || ks > 0) ? 1u : 0u);
+          tc_mma_ss_lo(tmem + b * a.acc_cols, w + kstep_kmajor(ks), x + kstep_kmajor(ks), idesc,
+                       (step > 0 || ks > 0) ? 1u : 0u);
         tc_commit(empty + s);
-        if (i == k_end - 1) tc_commit(done);
+        if (i == k_end - 1 || (kTurns && step == per_acc - 1)) tc_commit(acc_full + (kTurns ? b : 0));
       }
       __syncwarp();
       if (++s == a.stages) s = 0, phase ^= 1;
+      if (++step == per_acc) step = 0, ++c;
     }
     if (!ok) {
       if (lane == 0) {
@@ -201,20 +212,59 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
   } else {
-    // every MMA has read its stages when `done` completes, so the ring is free
-    ok = warp_all(mbar_wait(done, 0, st));
-    tc_fence_after();
-    if (ok) {
-      const int quarter = warp & 3;
-      float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
-      for (int c = 0; c < a.bn; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(tmem + (uint32_t(quarter * 32) << 16) + c, r);
+    const int quarter = warp & 3;
+    const uint32_t acc = tmem + (uint32_t(quarter * 32) << 16);
+    float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+    auto add = [](uint32_t (&v)[32], const uint32_t (&r)[32]) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < a.bn) part[(c + i) * 128] = __uint_as_float(r[i]);
+      for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(r[i]));
+    };
+    // every MMA has read its stages once the last accumulator is complete, so the ring is free then
+    auto leave = [&](const uint32_t (&v)[32], int c) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c + i < a.bn) part[(c + i) * 128] = __uint_as_float(v[i]);
+    };
+    if constexpr (kTurns) {
+      uint32_t sum[4][32];  // this output's sums of 32 tokens each
+      for (int n = 0; n < accs; ++n) {
+        const int b = n & 1;
+        if (!(ok = warp_all(mbar_wait(acc_full + b, (n >> 1) & 1, st)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c * 32 >= a.bn) continue;
+          if (n == 0) {
+            tmem_ld32(acc + c * 32, sum[c]);
+          } else {
+            uint32_t r[32];
+            tmem_ld32(acc + b * a.acc_cols + c * 32, r);
+            add(sum[c], r);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + b);
       }
-    } else if (lane == 0) {
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c * 32 < a.bn) leave(sum[c], c * 32);
+      }
+    } else if ((ok = warp_all(mbar_wait(acc_full, 0, st)))) {
+      tc_fence_after();
+      for (int c = 0; c < a.bn; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(acc + c, v);
+        for (int n = 1; n < accs; ++n) {
+          uint32_t r[32];
+          tmem_ld32(acc + n * a.acc_cols + c, r);
+          add(v, r);
+        }
+        leave(v, c);
+      }
+    }
+    if (!ok && lane == 0) {
       *failed = 1;
       raise_status(st, kStatusTimeout);
     }
@@ -239,12 +289,22 @@ __global__ void __launch_bounds__(kThreads)
   if (a.splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
 }
 
-template <int kAct>
+template <int kAct, bool kTurns>
 cudaError_t start_few(const CUtensorMap& mx, const CUtensorMap& mw, const LinearParams& p, const FewArgs& a, dim3 grid,
                       size_t smem, cudaStream_t s) {
-  const cudaError_t e = allow_smem<linear_few_kernel<kAct>>(226 * 1024);
+  const cudaError_t e = allow_smem<linear_few_kernel<kAct, kTurns>>(226 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(linear_few_kernel<kAct>, grid, kThreads, smem, s, unsigned(a.splits), mx, mw, p, a);
+  return launch_overlapped(linear_few_kernel<kAct, kTurns>, grid, kThreads, smem, s, unsigned(a.splits), mx, mw, p, a);
+}
+template <bool kTurns>
+cudaError_t start_few(const CUtensorMap& mx, const CUtensorMap& mw, const LinearParams& p, const FewArgs& a, dim3 grid,
+                      size_t smem, cudaStream_t s) {
+  switch (p.act) {
+    case MCS_ACT_GELU_TANH: return start_few<MCS_ACT_GELU_TANH, kTurns>(mx, mw, p, a, grid, smem, s);
+    case MCS_ACT_GELU_ERF: return start_few<MCS_ACT_GELU_ERF, kTurns>(mx, mw, p, a, grid, smem, s);
+    case MCS_ACT_SILU: return start_few<MCS_ACT_SILU, kTurns>(mx, mw, p, a, grid, smem, s);
+    default: return start_few<MCS_ACT_NONE, kTurns>(mx, mw, p, a, grid, smem, s);
+  }
 }
 
 }  // namespace
@@ -272,23 +332,21 @@ cudaError_t linear_few(const LinearParams& p, const FewPlan& plan, int num_sms, 
   a.bn = plan.bn;
   a.splits = plan.splits;
   a.tiles = (a.rows + a.bn - 1) / a.bn;
+  const int steps = ((p.K + 63) / 64 + a.splits - 1) / a.splits;
+  a.accs = acc_count(steps);
+  a.acc_cols = few_acc_cols(a.bn);
   a.tmem_cols = 32;
-  while (int(a.tmem_cols) < a.bn) a.tmem_cols *= 2;
+  while (int(a.tmem_cols) < few_accs(a.bn, steps) * a.acc_cols) a.tmem_cols *= 2;
   // the ring takes an SM's shared memory when every CTA has an SM to itself, half of it otherwise; it ends
   // up holding the partial accumulator
   const int stage = kWTile + a.bn * 128;
   const long long ctas = static_cast<long long>(a.splits) * a.tiles * a.sections * ((p.O + 127) / 128);
-  const bool half = ctas > few_slots(a.splits, num_sms) && few_two_per_sm(a.bn);
+  const bool half = ctas > few_slots(a.splits, num_sms) && few_two_per_sm(a.bn, steps);
   a.stages = (half ? kFewHalfSm : 226 * 1024 - kBarBytes - 1024) / stage;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const size_t smem = size_t(a.stages) * stage + kBarBytes + 1024;
   const dim3 grid(unsigned(a.splits) * a.tiles * a.sections, (p.O + 127) / 128);
-  switch (p.act) {
-    case MCS_ACT_GELU_TANH: return start_few<MCS_ACT_GELU_TANH>(mx, mw, p, a, grid, smem, s);
-    case MCS_ACT_GELU_ERF: return start_few<MCS_ACT_GELU_ERF>(mx, mw, p, a, grid, smem, s);
-    case MCS_ACT_SILU: return start_few<MCS_ACT_SILU>(mx, mw, p, a, grid, smem, s);
-    default: return start_few<MCS_ACT_NONE>(mx, mw, p, a, grid, smem, s);
-  }
+  return few_turns(a.bn, steps) ? start_few<true>(mx, mw, p, a, grid, smem, s) : start_few<false>(mx, mw, p, a, grid, smem, s);
 }
 
 }  // namespace mcs

@@ -15,12 +15,21 @@ struct FewPlan {
 inline int few_slots(int splits, int num_sms) {
   return splits <= 2 ? num_sms : int(0.85 * num_sms) / splits * splits;
 }
-// Half of an SM's shared memory holds three stages (16 KB of w and bn x 128 bytes of x
-// each) and the bn x 512 bytes of the partial accumulator.
+// Tensor memory: an accumulator's columns, and how many accumulators a slice of `steps` k steps holds at once. All
+// of them stay until the end where they fit in half of the tensor memory; otherwise, up to 128 tokens, two take turns
+// and their sums are kept in registers.
+inline int few_acc_cols(int bn) { return (bn + 31) / 32 * 32; }
+inline bool few_turns(int bn, int steps) {
+  return bn <= 128 && acc_count(steps) * few_acc_cols(bn) > 256;
+}
+inline int few_accs(int bn, int steps) { return few_turns(bn, steps) ? 2 : acc_count(steps); }
+inline bool few_fits(int bn, int steps) { return few_accs(bn, steps) * few_acc_cols(bn) <= 512; }
+// Half of an SM's shared memory holds three stages (16 KB of w and bn x 128 bytes of x each) and the bn x 512
+// bytes of the partial accumulator, and half of its tensor memory the accumulators.
 constexpr int kFewHalfSm = 112 * 1024 - 1280;
-inline bool few_two_per_sm(int bn) {
+inline bool few_two_per_sm(int bn, int steps) {
   const int stage = 16384 + bn * 128;
-  return kFewHalfSm / stage >= 3 && kFewHalfSm / stage * stage >= bn * 512;
+  return kFewHalfSm / stage >= 3 && kFewHalfSm / stage * stage >= bn * 512 && few_accs(bn, steps) * few_acc_cols(bn) <= 256;
 }
 cudaError_t linear_few(const LinearParams& p, const FewPlan& plan, int num_sms, cudaStream_t s);
 
