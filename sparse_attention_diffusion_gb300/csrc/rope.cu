@@ -281,14 +281,17 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) 
 // over the block's rows through shared memory, and goes to partial[block];
 // norm_bwd_reduce_kernel adds the blocks in order.
 //
-// With g = R^T dy and t = g * x, the sums over the row are ss = sum x^2 and
-// dot = sum w t, taken together; then dw += rstd t and
-// dx = rstd (g w) - (rstd^3 dot / d) x. Instructions bound this (two row sums and
-// the conversions beside 48 bytes a lane), so pairs of pairs go through packed
-// fp32 operations.
-// Heads in flight per lane, at three blocks an SM (480p layer, 12 heads of 128: two
-// heads 165 us, three 149, four 144; as halves, whose rows are two loads, three 150,
-// four 179; four blocks of two heads 168, two blocks of four 158).
+// With g = R^T dy and xhat = rstd x: dw += g xhat and dx = rstd (g w - xhat mean(g w xhat)).
+// The row is scaled by rstd before anything is multiplied with it, so that no factor leaves
+// fp32's range for rows of any length: one whose squares overflow has rstd = 0 and gives 0.
+// (Both row sums taken together over the unscaled row give infinities and NaN for long rows and
+// lose the projection where dot rstd^2 underflows.) Instructions bound this (two row sums and
+// the conversions beside 48 bytes a lane), so pairs of pairs go through packed fp32 operations.
+// Heads in flight per lane, at three blocks an SM; and whether the lengths of all of them are
+// summed before the first gradient (480p layer, 12 heads of 128, bf16: four heads 138 us, with all
+// lengths first 172; as halves, whose rows are two loads, two heads 156, three 177 and four 175,
+// three with all lengths first 145, four 173; fp32, 2 x 6 heads of 128 x 16,687 tokens: 152, all
+// lengths first 149).
 template <bool kHalf>
 constexpr int kBwdUnroll = kHalf ? 3 : 4;
 constexpr int kBwdBlocksPerSm = 3;
@@ -297,6 +300,7 @@ template <typename T, int D, bool kHalf>
 __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_bwd_kernel(const NormBwdParams p) {
   using R = Row<T, D>;
   constexpr int NP = R::NP, U = kBwdUnroll<kHalf>;
+  constexpr bool kTogether = kHalf || sizeof(T) == 4;
   __shared__ float red[R::kTokens][D];
   const int lane = threadIdx.x % R::L, row = threadIdx.x / R::L;
   const int tiles = (p.N + R::kTokens - 1) / R::kTokens;
@@ -352,39 +356,50 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_bwd_kernel(con
             if (st < 2) rx[i] = load_raw<T, D, kHalf>(px + (h0 + i) * p.in.h, lane);
           }
         }
+        auto squares = [&](const Raw& r) {
+          uint64_t x[N2], y[N2], ss = f2_pack(0.f, 0.f);
+          unpack2<T, kHalf, N2>(r, x, y);
+#pragma unroll
+          for (int j = 0; j < N2; ++j) ss = f2_fma(y[j], y[j], f2_fma(x[j], x[j], ss));
+          float s0, s1;
+          f2_unpack(ss, s0, s1);
+          return s0 + s1;
+        };
+        [[maybe_unused]] float lengths[U];
+        if constexpr (kTogether) {
+          if (st < 2) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) lengths[i] = squares(rx[i]);
+#pragma unroll
+            for (int i = 0; i < U; ++i) lengths[i] = row_sum<R::L>(lengths[i]);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           if (st < 2) {
-            uint64_t x[N2], y[N2], ga[N2], gb[N2];
+            const float rstd = rsqrtf((kTogether ? lengths[i] : row_sum<R::L>(squares(rx[i]))) * (1.f / D) + p.eps);
+            uint64_t x[N2], y[N2], ga[N2], gb[N2], dot = f2_pack(0.f, 0.f);
             unpack2<T, kHalf, N2>(rx[i], x, y);
             unpack2<T, kHalf, N2>(ry[i], ga, gb);
-            uint64_t ss = f2_pack(0.f, 0.f), dot = ss, ta[N2], tb[N2];
+            const uint64_t r2 = f2_pack(rstd, rstd);
 #pragma unroll
             for (int j = 0; j < N2; ++j) {
-              ss = f2_fma(y[j], y[j], f2_fma(x[j], x[j], ss));
+              x[j] = f2_mul(x[j], r2), y[j] = f2_mul(y[j], r2);
               const uint64_t g = ga[j];
               ga[j] = f2_fma(gb[j], s2[j], f2_mul(g, c2[j]));
               gb[j] = f2_fma(g, n2[j], f2_mul(gb[j], c2[j]));
-              ta[j] = f2_mul(ga[j], x[j]), tb[j] = f2_mul(gb[j], y[j]);
-              dot = f2_fma(wb[j], tb[j], f2_fma(wa[j], ta[j], dot));
+              da[j] = f2_fma(ga[j], x[j], da[j]), db[j] = f2_fma(gb[j], y[j], db[j]);
+              ga[j] = f2_mul(ga[j], wa[j]), gb[j] = f2_mul(gb[j], wb[j]);
+              dot = f2_fma(gb[j], y[j], f2_fma(ga[j], x[j], dot));
             }
-            float s0, s1, d0, d1;
-            f2_unpack(ss, s0, s1);
-            f2_unpack(dot, d0, d1);
-            s0 += s1, d0 += d1;
-#pragma unroll
-            for (int o = R::L / 2; o > 0; o >>= 1) {
-              s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-              d0 += __shfl_xor_sync(0xffffffffu, d0, o);
-            }
-            const float rstd = rsqrtf(s0 * (1.f / D) + p.eps);
-            const float k = -(rstd * d0 * (1.f / D)) * rstd * rstd;  // in this order no power of rstd leaves the range
-            const uint64_t r2 = f2_pack(rstd, rstd), k2 = f2_pack(k, k);
+            float s0, s1;
+            f2_unpack(dot, s0, s1);
+            const float m = -row_sum<R::L>(s0 + s1) * (1.f / D);
+            const uint64_t m2 = f2_pack(m, m);
 #pragma unroll
             for (int j = 0; j < N2; ++j) {
-              da[j] = f2_fma(r2, ta[j], da[j]), db[j] = f2_fma(r2, tb[j], db[j]);
-              ga[j] = f2_fma(r2, f2_mul(ga[j], wa[j]), f2_mul(k2, x[j]));
-              gb[j] = f2_fma(r2, f2_mul(gb[j], wb[j]), f2_mul(k2, y[j]));
+              ga[j] = f2_mul(r2, f2_fma(m2, x[j], ga[j]));
+              gb[j] = f2_mul(r2, f2_fma(m2, y[j], gb[j]));
             }
             ry[i] = pack2<T, kHalf, N2>(ga, gb);
           }
