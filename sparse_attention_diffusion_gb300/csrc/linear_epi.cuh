@@ -9,18 +9,30 @@
 
 namespace mcs {
 
-// The gates of SiLU and of the tanh form of GELU are logistic functions, z /
-// (1 + exp(-t)): no cancellation for negative z, and exp overflowing to
-// infinity gives the right limit 0. GELU's erf form uses erfc for the same reason.
-__device__ __forceinline__ float logistic_gate(float z, float t) { return __fdividef(z, 1.f + __expf(-t)); }
-template <int kAct, int n>
+// The gates of SiLU and of the tanh form of GELU are logistic functions, z / (1 + exp(-t)), taken
+// as z exp(t) / (1 + exp(t)) for negative t: no cancellation, no overflow, and a denominator
+// between 1 and 2, which the fast division needs. GELU's erf form uses erfc for the same reason.
+// bf16 outputs take the fast exponential (2 + 1.2 |t| ulp, below 2^-16 wherever the result is in
+// bf16's normal range) and division. fp32 outputs take expf (2 ulp), of t / 2 and squared, so that
+// it stays in the normal range as long as the result does, and the division to nearest.
+template <bool kF32>
+__device__ __forceinline__ float logistic_gate(float z, float t) {
+  if constexpr (kF32) {
+    const float h = expf(-0.5f * fabsf(t));
+    return (t < 0.f ? z * h * h : z) / (1.f + h * h);
+  } else {
+    const float e = __expf(-fabsf(t));
+    return __fdividef(t < 0.f ? z * e : z, 1.f + e);
+  }
+}
+template <int kAct, bool kF32 = false, int n>
 __device__ __forceinline__ void activate(float (&v)[n]) {
 #pragma unroll
   for (int i = 0; i < n; ++i) {
     if constexpr (kAct == MCS_ACT_GELU_TANH)  // sqrt(8 / pi) = 1.5957691216
-      v[i] = logistic_gate(v[i], 1.5957691216f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+      v[i] = logistic_gate<kF32>(v[i], 1.5957691216f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
     else if constexpr (kAct == MCS_ACT_SILU)
-      v[i] = logistic_gate(v[i], v[i]);
+      v[i] = logistic_gate<kF32>(v[i], v[i]);
     else if constexpr (kAct == MCS_ACT_GELU_ERF)
       v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678f);
   }
@@ -31,7 +43,7 @@ template <int kAct, typename T>
 __device__ __forceinline__ void finish_one(const LinearParams& p, int m, int o, float acc) {
   if (p.bias) acc += to_f32(static_cast<const T*>(p.bias)[o]);
   float v[1] = {acc};
-  activate<kAct>(v);
+  activate<kAct, sizeof(T) == 4>(v);
   acc = v[0];
   if (p.gate) acc *= to_f32(static_cast<const T*>(p.gate)[size_t(m / p.N) * p.O + o]);
   const size_t at = size_t(m) * p.O + o;
@@ -91,7 +103,7 @@ __device__ __forceinline__ void finish_row4(const LinearParams& p, int m, int o,
     const float4 t = at4(p.bias, o);
     v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
   }
-  activate<kAct>(v);
+  activate<kAct, true>(v);
   if (p.gate) {
     const float4 t = at4(p.gate, size_t(m / p.N) * p.O + o);
     v[0] *= t.x, v[1] *= t.y, v[2] *= t.z, v[3] *= t.w;
