@@ -23,7 +23,7 @@
 // 1,664 clocks; 4,096 x 5,120 x 5,120 took 1.22 ms).
 // Few tiles are cut along K over the CTAs of a cluster, which join their sums through
 // distributed shared memory, ranks in order, so that equal calls give equal bits.
-// An infinite element makes its outputs NaN (its lower parts are infinity less infinity).
+// Outputs that come out infinite or NaN are summed again on the CUDA cores.
 //
 // Measured: 4,096 x 5,120 -> 5,120 outputs 0.88 ms (243 TFLOP/s; 1,170 clocks a step;
 // the CUDA cores' 128 x 128 tiles of packed FMAs took 3.89 ms), 1,024 x 1,536 -> 1,536 33
@@ -93,10 +93,68 @@ __device__ __forceinline__ void sts4(uint32_t at, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// A row's four sums of a lane, joined over the K slices (ranks in order).
+__device__ __forceinline__ void joined_sums(const SplitArgs& a, uint32_t sbase, int r, int lane, float (&v)[4]) {
+  const uint32_t at = sbase + (r * kSumLd + lane * 4) * 4;
+  v[0] = v[1] = v[2] = v[3] = 0.f;
+  if (a.splits == 1) {
+    const float4 f = lds4(at);
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+  } else {
+    float f[4][4];
+    for (int c0 = 0; c0 < a.splits; c0 += 4) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f[c][0] = f[c][1] = f[c][2] = f[c][3] = 0.f;
+        if (c0 + c < a.splits)
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(f[c][0]), "=f"(f[c][1]), "=f"(f[c][2]), "=f"(f[c][3])
+                       : "r"(cluster_map(at, c0 + c)));
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += f[c][i];
+    }
+  }
+}
+
+// Not finite if one of the four is not (or if they are very large).
+__device__ __forceinline__ float sum4(const float (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); }
+
+// The outputs whose sum over the parts is not finite, summed again in fp32 on the CUDA cores: an infinite element
+// has no parts (infinity less infinity); here it gives what its products and their sum are. A function of its own,
+// with the parameters left in constant memory, so that the ordinary way out keeps its registers (20,000 x 200 ->
+// 1,000 86 -> 88 us with it, 92 inline; 4,096 x 5,120 -> 5,120 874 -> 880 us).
+template <int kAct>
+__device__ __noinline__ void finish_not_finite(const LinearParams& p, const SplitArgs& a, uint32_t sbase, int sec, int row0,
+                                               int live, int o0, int rank, int warp, int lane) {
+  const int d = p.heads > 0 ? p.K / p.heads : p.K, o = o0 + lane * 4;
+  const size_t head = size_t(a.rows) * d;
+  const float* w = static_cast<const float*>(p.w);
+  for (int r = rank + a.splits * warp; r < live; r += a.splits * kWarps) {
+    float v[4];
+    joined_sums(a, sbase, r, lane, v);
+    const float* x = static_cast<const float*>(p.x) + size_t(sec) * (p.heads > 0 ? p.heads : 1) * head + size_t(row0 + r) * d;
+    if (isfinite(sum4(v))) continue;
+    for (int i = 0; i < 4; ++i) {
+      if (isfinite(v[i]) || o + i >= p.O) continue;
+      float t = 0.f;
+      for (int k = 0; k < p.K && !isnan(t); k += 4) {  // NaN stays
+        const float4 f = *reinterpret_cast<const float4*>(x + (k >> a.head_shift) * head + (k & a.col_mask));
+        const float4 g = *reinterpret_cast<const float4*>(w + size_t(o + i) * p.K + k);
+        t = fmaf(f.w, g.w, fmaf(f.z, g.z, fmaf(f.y, g.y, fmaf(f.x, g.x, t))));
+      }
+      v[i] = t;
+    }
+    finish_row4<kAct>(p, sec * a.rows + row0 + r, o, v);
+  }
+}
+
 template <int kAct>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                        const LinearParams p, const SplitArgs a) {
+                        const __grid_constant__ LinearParams p, const __grid_constant__ SplitArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -295,33 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     else asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(f) : "r"(cluster_map(smem_u32(failed), r)) : "memory");
     ok = ok && f == 0;
   }
-  const int live = min(128, a.rows - row0);
+  const int live = min(128, a.rows - row0), o = o0 + lane * 4;
+  bool again = false;
 #pragma unroll 1
   for (int r = rank + a.splits * warp; ok && r < live; r += a.splits * kWarps) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t at = sbase + (r * kSumLd + lane * 4) * 4;
-    if (a.splits == 1) {
-      const float4 f = lds4(at);
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-    } else {
-      float f[4][4];
-      for (int c0 = 0; c0 < a.splits; c0 += 4) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          f[c][0] = f[c][1] = f[c][2] = f[c][3] = 0.f;
-          if (c0 + c < a.splits)
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(f[c][0]), "=f"(f[c][1]), "=f"(f[c][2]), "=f"(f[c][3])
-                         : "r"(cluster_map(at, c0 + c)));
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += f[c][i];
-      }
-    }
-    finish_row4<kAct>(p, sec * a.rows + row0 + r, o0 + lane * 4, v);
+    float v[4];
+    joined_sums(a, sbase, r, lane, v);
+    if (isfinite(sum4(v))) finish_row4<kAct>(p, sec * a.rows + row0 + r, o, v);
+    else again = true;
   }
+  if (__any_sync(0xffffffffu, again)) finish_not_finite<kAct>(p, a, sbase, sec, row0, live, o0, rank, warp, lane);
   if (a.splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
 }
 
