@@ -1,14 +1,15 @@
 // fp32 matrix product with epilogue on the bf16 tensor cores, with fp32's accuracy.
 //
-// Every fp32 number is the exact sum of three bf16 parts, h + m + l, each the next
-// eight bits of its significand (cut off, not rounded: two integer operations and an
-// exact subtraction a part). Of the nine products of parts the six largest are
-// summed; what is left out is below 2^-20 of |x w|, about 2^-24 on average. The
-// tensor core adds into its fp32 accumulator by truncation (measured on this GPU:
-// two bits below the sum's last one are kept), which over a long K would shrink the
-// sum by 2^-24 a step or more. So an accumulator takes 32 columns of K only, small
-// products first, and the epilogue's threads add it to fp32 sums in registers,
-// rounding to nearest.
+// Every fp32 number is the exact sum of three bf16 parts, h + m + l: it is rounded to
+// bf16, then twice what is left (exact subtractions; two numbers a conversion), which takes
+// as many instructions as cutting the bits off. Of the nine products of parts the six
+// largest are summed; |m| < 2^-8 |x| and |l| <= 2^-17 |x| leave at most 1.01 * 2^-24 |x w|
+// out, of either sign (parts cut off left out up to 2^-20, always towards 0). A number
+// keeps bits down to 2^-133 only, bf16's last. The tensor core adds into its fp32
+// accumulator by truncation (measured on this GPU: two bits below the sum's last one
+// are kept), which over a long K would shrink the sum by 2^-24 a step or more. So an
+// accumulator takes 32 columns of K only, small products first, and the epilogue's
+// threads add it to fp32 sums in registers, rounding to nearest.
 //
 // One CTA per 128 x 128 tile, 576 threads:
 //   warp 0        TMA producer: fp32 tiles of 32 columns, four stages
@@ -25,7 +26,7 @@
 // distributed shared memory, ranks in order, so that equal calls give equal bits.
 // Outputs that come out infinite or NaN are summed again on the CUDA cores.
 //
-// Measured: 4,096 x 5,120 -> 5,120 outputs 0.88 ms (243 TFLOP/s; 1,170 clocks a step;
+// Measured: 4,096 x 5,120 -> 5,120 outputs 0.85 ms (252 TFLOP/s; 1,140 clocks a step;
 // the CUDA cores' 128 x 128 tiles of packed FMAs took 3.89 ms), 1,024 x 1,536 -> 1,536 33
 // us, 300 x 3,200 -> 320 15 us in eight slices; relative error of the result 1.0e-7 to
 // 1.9e-7 over K = 32 .. 5,120 (fp32 FMAs in order: 0.8e-7 to 7e-7).
@@ -67,18 +68,12 @@ __device__ __forceinline__ void cut8(const float4& a, const float4& b, uint4& h,
   uint32_t hw[4], mw[4], lw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t p[2], q[2], r[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float v = x[2 * i + j];
-      p[j] = __float_as_uint(v);
-      const float v1 = v - __uint_as_float(p[j] & 0xffff0000u);
-      q[j] = __float_as_uint(v1);
-      r[j] = __float_as_uint(v1 - __uint_as_float(q[j] & 0xffff0000u));
-    }
-    hw[i] = __byte_perm(p[0], p[1], 0x7632);
-    mw[i] = __byte_perm(q[0], q[1], 0x7632);
-    lw[i] = __byte_perm(r[0], r[1], 0x7632);
+    float u = x[2 * i], v = x[2 * i + 1];
+    hw[i] = pack_bf16x2(u, v);
+    u -= __uint_as_float(hw[i] << 16), v -= __uint_as_float(hw[i] & 0xffff0000u);
+    mw[i] = pack_bf16x2(u, v);
+    u -= __uint_as_float(mw[i] << 16), v -= __uint_as_float(mw[i] & 0xffff0000u);
+    lw[i] = pack_bf16x2(u, v);
   }
   h = make_uint4(hw[0], hw[1], hw[2], hw[3]);
   m = make_uint4(mw[0], mw[1], mw[2], mw[3]);
@@ -123,9 +118,10 @@ __device__ __forceinline__ void joined_sums(const SplitArgs& a, uint32_t sbase, 
 __device__ __forceinline__ float sum4(const float (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); }
 
 // The outputs whose sum over the parts is not finite, summed again in fp32 on the CUDA cores: an infinite element
-// has no parts (infinity less infinity); here it gives what its products and their sum are. A function of its own,
-// with the parameters left in constant memory, so that the ordinary way out keeps its registers (20,000 x 200 ->
-// 1,000 86 -> 88 us with it, 92 inline; 4,096 x 5,120 -> 5,120 874 -> 880 us).
+// has no parts (infinity less infinity), nor has one that bf16 rounds to infinity (3.39e38 and more); here they
+// give what their products and sums are. A function of its own, with the parameters left in constant memory, so
+// that the ordinary way out keeps its registers (20,000 x 200 -> 1,000 86 -> 88 us with it, 92 inline; 4,096 x
+// 5,120 -> 5,120 874 -> 880 us).
 template <int kAct>
 __device__ __noinline__ void finish_not_finite(const LinearParams& p, const SplitArgs& a, uint32_t sbase, int sec, int row0,
                                                int live, int o0, int rank, int warp, int lane) {
