@@ -304,8 +304,9 @@ mcs_status mcs_rope_apply(const mcs_desc *desc, const mcs_rope *rope, const floa
  * over the d elements of each token and head, k likewise, and v copied, all
  * rounded once. q, k, v: views with the strides `in` (NULL: contiguous), e.g. the
  * packed output of a projection; q_out, k_out, v_out: contiguous [B,H,N,d], what
- * mcs_dense_attn and the others take. Each of the three may be absent (input and
- * output both NULL), not all. wq, wk: [d] in the I/O dtype, or NULL for 1.
+ * mcs_dense_attn and the others take. An output may take its own input's place if
+ * that is contiguous; other overlaps are MCS_ERR_INVALID_ARG, as below. Each of the
+ * three may be absent (input and output both NULL), not all. wq, wk: [d] in the I/O dtype, or NULL for 1.
  * eps: finite, > 0. */
 mcs_status mcs_qk_norm_rope(const mcs_desc *desc, const mcs_rope *rope, const float *table, const int32_t *pos,
                             const void *q, const void *k, const void *v, const mcs_strides *in, const void *wq,
@@ -336,7 +337,8 @@ mcs_status mcs_qk_norm_rope_bwd(const mcs_desc *desc, const mcs_rope *rope, cons
  * [B, heads, N, in / heads] (in / heads 64 or 128), so that an output projection
  * needs no transposed copy. w: [out, in]. bias: [out] or NULL. gate: [B, out],
  * one row per batch, or NULL for 1. residual: [B, N, out] or NULL for 0. y:
- * [B, N, out]; y may be residual. All in the I/O dtype, 16-byte aligned. act:
+ * [B, N, out]; y may be residual, and overlaps nothing else (MCS_ERR_INVALID_ARG).
+ * All in the I/O dtype, 16-byte aligned. act:
  * mcs_act; MCS_ACT_GELU_TANH is z / (1 + exp(-2 sqrt(2/pi) (z + 0.044715 z^3))),
  * MCS_ACT_GELU_ERF z/2 (1 + erf(z / sqrt 2)), MCS_ACT_SILU z / (1 + exp(-z)).
  * Supported: in a multiple of 8 (BF16) or 4 (F32), out any; in, out <= 2^20,

@@ -88,6 +88,25 @@ bool view(const mcs_desc* desc, const mcs_strides* s, bool written, mcs::ViewStr
   return true;
 }
 
+// Byte ranges, for the refusal of outputs that alias inputs. A null pointer is no range.
+struct Range {
+  const char* at;
+  long long bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  return a.at != nullptr && b.at != nullptr && a.at < b.at + b.bytes && b.at < a.at + a.bytes;
+}
+Range range(const void* p, long long bytes) { return {static_cast<const char*>(p), bytes}; }
+// From a view's first element to its last.
+Range range(const mcs_desc* d, const void* p, const mcs::ViewStrides& v) {
+  const long long n = (d->B - 1) * v.b + (d->H - 1) * v.h + (d->N - 1) * v.n + d->d;
+  return {static_cast<const char*>(p), n * (d->dtype == MCS_BF16 ? 2 : 4)};
+}
+bool contiguous(const mcs_desc* d, const mcs::ViewStrides& v) {
+  return (d->B == 1 || v.b == static_cast<long long>(d->H) * d->N * d->d) &&
+         (d->H == 1 || v.h == static_cast<long long>(d->N) * d->d) && (d->N == 1 || v.n == d->d);
+}
+
 }  // namespace
 
 extern "C" {
@@ -150,6 +169,14 @@ mcs_status mcs_qk_norm_rope(const mcs_desc* desc, const mcs_rope* rope, const fl
   if (!aligned16_or_null(wq) || !aligned16_or_null(wk)) return MCS_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || eps <= 0.f) return MCS_ERR_INVALID_ARG;
   if (!view(desc, in, false, &p.in) || !view(desc, nullptr, true, &p.out)) return MCS_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {  // an output may only be its own input, row by row
+    const Range out = range(desc, dst[i], p.out);
+    for (int j = 0; j < 3; ++j) {
+      if (j < i && overlap(out, range(desc, dst[j], p.out))) return MCS_ERR_INVALID_ARG;
+      if (i == j && src[j] == dst[i] && contiguous(desc, p.in)) continue;
+      if (overlap(out, range(desc, src[j], p.in))) return MCS_ERR_INVALID_ARG;
+    }
+  }
   int sms = 0;
   if ((st = mcs::current_device(&p.status, &sms)) != MCS_OK) return st;
   p.w[0] = wq;
@@ -198,6 +225,17 @@ mcs_status mcs_qk_norm_rope_bwd(const mcs_desc* desc, const mcs_rope* rope, cons
   if (!std::isfinite(eps) || eps <= 0.f) return MCS_ERR_INVALID_ARG;
   if (!view(desc, in, true, &p.in)) return MCS_ERR_INVALID_ARG;
   if (!aligned16(ws) || ws_bytes < mcs_qk_norm_rope_bwd_workspace_size(desc)) return MCS_ERR_WORKSPACE;
+  mcs::ViewStrides block;
+  view(desc, nullptr, true, &block);
+  if (dwq != nullptr && dwq == dwk) return MCS_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {  // a gradient may only take the place of its own stream's tensors, row by row
+    if (dx[i] == nullptr) continue;
+    for (int j = 0; j < 3; ++j) {
+      if (i != j && (dx[i] == dx[j] || (j < 2 && dx[i] == x[j]))) return MCS_ERR_INVALID_ARG;
+      if (i == j && dx[i] == dy[j] && contiguous(desc, p.in)) continue;
+      if (overlap(range(desc, dx[i], p.in), range(desc, dy[j], block))) return MCS_ERR_INVALID_ARG;
+    }
+  }
   int sms = 0;
   if ((st = mcs::current_device(&p.status, &sms)) != MCS_OK) return st;
   p.partial = static_cast<float*>(ws);
@@ -223,6 +261,12 @@ mcs_status mcs_linear(const mcs_linear_desc* desc, const void* x, const void* w,
   if (static_cast<long long>(desc->B) * (desc->heads > 0 ? desc->heads : 1) >= (1ll << 31)) return MCS_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(w) || !aligned16(y)) return MCS_ERR_INVALID_ARG;
   if (!aligned16_or_null(bias) || !aligned16_or_null(gate) || !aligned16_or_null(residual)) return MCS_ERR_INVALID_ARG;
+  const long long es = bf16 ? 2 : 4, out = desc->out;
+  const Range written = range(y, rows * out * es);
+  if (overlap(written, range(x, rows * desc->in * es)) || overlap(written, range(w, out * desc->in * es)) ||
+      overlap(written, range(bias, out * es)) || overlap(written, range(gate, desc->B * out * es)))
+    return MCS_ERR_INVALID_ARG;
+  if (residual != y && overlap(written, range(residual, rows * out * es))) return MCS_ERR_INVALID_ARG;
   mcs::LinearParams p{};
   int sms = 0;
   const mcs_status st = mcs::current_device(&p.status, &sms);

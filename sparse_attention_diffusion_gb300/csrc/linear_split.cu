@@ -28,8 +28,8 @@
 //
 // Measured: 4,096 x 5,120 -> 5,120 outputs 0.85 ms (252 TFLOP/s; 1,140 clocks a step;
 // the CUDA cores' 128 x 128 tiles of packed FMAs took 3.89 ms), 1,024 x 1,536 -> 1,536 33
-// us, 300 x 3,200 -> 320 15 us in eight slices; relative error of the result 1.0e-7 to
-// 1.9e-7 over K = 32 .. 5,120 (fp32 FMAs in order: 0.8e-7 to 7e-7).
+// us, 300 x 3,200 -> 320 15 us in eight slices; relative error of the result 0.5e-7 to
+// 1.4e-7 over K = 4 .. 5,120 (fp32 FMAs in order: 0.4e-7 to 13e-7).
 #include "attn_tc.h"
 #include "common.cuh"
 #include "launch.cuh"
