@@ -361,6 +361,20 @@ typedef struct {
 mcs_status mcs_linear(const mcs_linear_desc *desc, const void *x, const void *w, const void *bias, const void *gate,
                       const void *residual, void *y, mcs_stream stream);
 
+/* Diagnostic (no counterpart in the method): what mcs_linear runs a description as on
+ * a GPU of num_sms SMs (8 .. 1,024), so that a test can say which kernel it covers.
+ * tile: columns (pairs) or rows of x (few) of a tile; slices: K slices of a cluster;
+ * accumulators: how many a slice takes one after another. Host-only; launches
+ * nothing. */
+typedef enum {
+  MCS_LINEAR_PAIRS = 0,     /* bf16, CTA pairs on 256-row tiles */
+  MCS_LINEAR_FEW = 1,       /* bf16, few rows: w on the tensor core's lanes */
+  MCS_LINEAR_F32_ROWS = 2,  /* fp32 on the CUDA cores */
+  MCS_LINEAR_F32_PARTS = 3  /* fp32 in bf16 parts */
+} mcs_linear_kernel;
+typedef struct { int kernel, tile, slices, accumulators; } mcs_linear_choice;
+mcs_status mcs_linear_plan(const mcs_linear_desc *desc, int with_residual, int num_sms, mcs_linear_choice *choice);
+
 /* Synchronises `stream`, then reports (and clears) the device-side flags raised
  * since the last call: MCS_ERR_DEVICE_BOUNDS, MCS_ERR_DEVICE_TIMEOUT, or a
  * sticky CUDA error as MCS_ERR_CUDA. MCS_OK if none. */

@@ -88,6 +88,28 @@ bool view(const mcs_desc* desc, const mcs_strides* s, bool written, mcs::ViewStr
   return true;
 }
 
+// The checks of a product's description; fills its sizes.
+mcs_status check_linear(const mcs_linear_desc* desc, mcs::LinearParams* p) {
+  if (desc == nullptr) return MCS_ERR_INVALID_ARG;
+  if (desc->B < 1 || desc->N < 1 || desc->in < 1 || desc->out < 1 || desc->heads < 0) return MCS_ERR_INVALID_ARG;
+  if (desc->dtype != MCS_F32 && desc->dtype != MCS_BF16) return MCS_ERR_UNSUPPORTED;
+  if (desc->act < MCS_ACT_NONE || desc->act > MCS_ACT_SILU) return MCS_ERR_UNSUPPORTED;
+  const bool bf16 = desc->dtype == MCS_BF16;
+  const long long rows = static_cast<long long>(desc->B) * desc->N;
+  if (desc->in > (1 << 20) || desc->out > (1 << 20) || rows >= (1ll << 31) - 256) return MCS_ERR_UNSUPPORTED;
+  if (desc->in % (bf16 ? 8 : 4) != 0) return MCS_ERR_UNSUPPORTED;
+  if (desc->heads > 0 && desc->in != 64ll * desc->heads && desc->in != 128ll * desc->heads) return MCS_ERR_UNSUPPORTED;
+  if (static_cast<long long>(desc->B) * (desc->heads > 0 ? desc->heads : 1) >= (1ll << 31)) return MCS_ERR_UNSUPPORTED;
+  p->B = desc->B;
+  p->N = desc->N;
+  p->M = int(rows);
+  p->K = desc->in;
+  p->O = desc->out;
+  p->heads = desc->heads;
+  p->act = desc->act;
+  return MCS_OK;
+}
+
 // Byte ranges, for the refusal of outputs that alias inputs. A null pointer is no range.
 struct Range {
   const char* at;
@@ -249,43 +271,39 @@ mcs_status mcs_qk_norm_rope_bwd(const mcs_desc* desc, const mcs_rope* rope, cons
 
 mcs_status mcs_linear(const mcs_linear_desc* desc, const void* x, const void* w, const void* bias, const void* gate,
                       const void* residual, void* y, mcs_stream stream) {
-  if (desc == nullptr) return MCS_ERR_INVALID_ARG;
-  if (desc->B < 1 || desc->N < 1 || desc->in < 1 || desc->out < 1 || desc->heads < 0) return MCS_ERR_INVALID_ARG;
-  if (desc->dtype != MCS_F32 && desc->dtype != MCS_BF16) return MCS_ERR_UNSUPPORTED;
-  if (desc->act < MCS_ACT_NONE || desc->act > MCS_ACT_SILU) return MCS_ERR_UNSUPPORTED;
-  const bool bf16 = desc->dtype == MCS_BF16;
-  const long long rows = static_cast<long long>(desc->B) * desc->N;
-  if (desc->in > (1 << 20) || desc->out > (1 << 20) || rows >= (1ll << 31) - 256) return MCS_ERR_UNSUPPORTED;
-  if (desc->in % (bf16 ? 8 : 4) != 0) return MCS_ERR_UNSUPPORTED;
-  if (desc->heads > 0 && desc->in != 64ll * desc->heads && desc->in != 128ll * desc->heads) return MCS_ERR_UNSUPPORTED;
-  if (static_cast<long long>(desc->B) * (desc->heads > 0 ? desc->heads : 1) >= (1ll << 31)) return MCS_ERR_UNSUPPORTED;
+  mcs::LinearParams p{};
+  mcs_status st = check_linear(desc, &p);
+  if (st != MCS_OK) return st;
   if (!aligned16(x) || !aligned16(w) || !aligned16(y)) return MCS_ERR_INVALID_ARG;
   if (!aligned16_or_null(bias) || !aligned16_or_null(gate) || !aligned16_or_null(residual)) return MCS_ERR_INVALID_ARG;
-  const long long es = bf16 ? 2 : 4, out = desc->out;
+  const bool bf16 = desc->dtype == MCS_BF16;
+  const long long es = bf16 ? 2 : 4, out = desc->out, rows = p.M;
   const Range written = range(y, rows * out * es);
   if (overlap(written, range(x, rows * desc->in * es)) || overlap(written, range(w, out * desc->in * es)) ||
       overlap(written, range(bias, out * es)) || overlap(written, range(gate, desc->B * out * es)))
     return MCS_ERR_INVALID_ARG;
   if (residual != y && overlap(written, range(residual, rows * out * es))) return MCS_ERR_INVALID_ARG;
-  mcs::LinearParams p{};
   int sms = 0;
-  const mcs_status st = mcs::current_device(&p.status, &sms);
-  if (st != MCS_OK) return st;
+  if ((st = mcs::current_device(&p.status, &sms)) != MCS_OK) return st;
   p.x = x;
   p.w = w;
   p.bias = bias;
   p.gate = gate;
   p.residual = residual;
   p.y = y;
-  p.B = desc->B;
-  p.N = desc->N;
-  p.M = int(rows);
-  p.K = desc->in;
-  p.O = desc->out;
-  p.heads = desc->heads;
-  p.act = desc->act;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return from_cuda(bf16 ? mcs::linear_tc(p, sms, s) : mcs::linear_f32(p, sms, s));
+}
+
+mcs_status mcs_linear_plan(const mcs_linear_desc* desc, int with_residual, int num_sms, mcs_linear_choice* choice) {
+  mcs::LinearParams p{};
+  const mcs_status st = check_linear(desc, &p);
+  if (st != MCS_OK) return st;
+  if (num_sms < 8 || num_sms > 1024 || choice == nullptr) return MCS_ERR_INVALID_ARG;
+  p.residual = with_residual ? choice : nullptr;  // only whether there is one
+  const mcs::LinearPlan plan = desc->dtype == MCS_BF16 ? mcs::plan_linear_tc(p, num_sms) : mcs::plan_linear_f32(p, num_sms);
+  *choice = {plan.kernel, plan.tile, plan.slices, plan.accumulators};
+  return MCS_OK;
 }
 
 }  // extern "C"

@@ -530,7 +530,7 @@ cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t
 // reading every operand once from HBM (23 bytes per clock and SM) bounds
 // everything; then come the start, the way out of the last tile (20 to 35 clocks a
 // column or token) and the exchange between K slices.
-cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
+LinearPlan plan_linear_tc(const LinearParams& p, int num_sms) {
   const int nk = (p.K + 63) / 64;
   const long long rows = p.heads > 0 ? p.N : p.M, sections = p.heads > 0 ? p.B : 1;
   const double hbm = 2.0 * (double(p.M) * p.K + double(p.O) * p.K + double(p.M) * p.O * (p.residual ? 2 : 1)) /
@@ -578,7 +578,14 @@ cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
       }
     }
   }
-  return few.bn > 0 ? linear_few(p, few, num_sms, s) : launch_pair(p, pair_bn, num_sms, s);
+  if (few.bn > 0) return {MCS_LINEAR_FEW, few.bn, few.splits, acc_count((nk + few.splits - 1) / few.splits)};
+  return {MCS_LINEAR_PAIRS, pair_bn, 1, acc_count(nk)};
+}
+
+cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
+  const LinearPlan plan = plan_linear_tc(p, num_sms);
+  return plan.kernel == MCS_LINEAR_FEW ? linear_few(p, {plan.tile, plan.slices}, num_sms, s)
+                                       : launch_pair(p, plan.tile, num_sms, s);
 }
 
 }  // namespace mcs

@@ -32,9 +32,16 @@ struct LinearParams {
   int act;               // mcs_act
   uint32_t* status;
 };
+// What a product runs as: the kernel (mcs_linear_kernel), columns (pairs) or rows of x (few) of a tile, K slices,
+// and accumulators a slice takes one after another.
+struct LinearPlan {
+  int kernel, tile, slices, accumulators;
+};
+LinearPlan plan_linear_tc(const LinearParams& p, int num_sms);
+LinearPlan plan_linear_f32(const LinearParams& p, int num_sms);
 cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s);
 // fp32: rows by the CUDA cores (up to eight) or the tensor cores in bf16 parts.
 cudaError_t linear_f32(const LinearParams& p, int num_sms, cudaStream_t s);
-cudaError_t linear_split(const LinearParams& p, int num_sms, cudaStream_t s);
+cudaError_t linear_split(const LinearParams& p, int splits, cudaStream_t s);
 
 }  // namespace mcs

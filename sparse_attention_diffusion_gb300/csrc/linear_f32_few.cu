@@ -96,8 +96,26 @@ cudaError_t launch(const LinearParams& p, cudaStream_t s) {
 
 }  // namespace
 
+LinearPlan plan_linear_f32(const LinearParams& p, int num_sms) {
+  if (p.M <= 8) return {MCS_LINEAR_F32_ROWS, p.M <= 2 ? 2 : 4, 1, 1};
+  // K slices of 128 x 128 tiles: the shortest estimate of waves x (steps of 32 columns of about 1,150 clocks + way in and out)
+  const int nk = (p.K + 31) / 32;
+  const long long row_tiles = p.heads > 0 ? static_cast<long long>((p.N + 127) / 128) * p.B : (p.M + 127) / 128;
+  const long long tiles = row_tiles * ((p.O + 127) / 128);
+  long long best = 0;
+  int slices = 1;
+  for (int splits = 1; splits <= 8 && splits <= nk; splits *= 2) {
+    const int slots = splits <= 2 ? num_sms : int(0.85 * num_sms) / splits * splits;
+    const long long cost = (tiles * splits + slots - 1) / slots *
+                           (static_cast<long long>((nk + splits - 1) / splits) * 1150 + 6000 + (splits > 1 ? 3000 : 0));
+    if (best == 0 || cost < best) best = cost, slices = splits;
+  }
+  return {MCS_LINEAR_F32_PARTS, 128, slices, (nk + slices - 1) / slices};
+}
+
 cudaError_t linear_f32(const LinearParams& p, int num_sms, cudaStream_t s) {
-  if (p.M > 8) return linear_split(p, num_sms, s);
+  const LinearPlan plan = plan_linear_f32(p, num_sms);
+  if (plan.kernel == MCS_LINEAR_F32_PARTS) return linear_split(p, plan.slices, s);
   switch (p.act) {
     case MCS_ACT_GELU_TANH: return launch<MCS_ACT_GELU_TANH>(p, s);
     case MCS_ACT_GELU_ERF: return launch<MCS_ACT_GELU_ERF>(p, s);

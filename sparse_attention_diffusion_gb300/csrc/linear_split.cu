@@ -372,7 +372,7 @@ cudaError_t start(const CUtensorMap& mx, const CUtensorMap& mw, const LinearPara
 
 }  // namespace
 
-cudaError_t linear_split(const LinearParams& p, int num_sms, cudaStream_t s) {
+cudaError_t linear_split(const LinearParams& p, int splits, cudaStream_t s) {
   SplitArgs a{};
   CUtensorMap mx, mw;
   bool ok;
@@ -392,16 +392,7 @@ cudaError_t linear_split(const LinearParams& p, int num_sms, cudaStream_t s) {
   }
   if (!(ok && make_tile_map_f32(&mw, p.w, 1, p.O, p.K, 128))) return cudaErrorInvalidValue;
   a.tiles = (a.rows + 127) / 128;
-  // K slices: the shortest estimate of waves x (steps of about 1,150 clocks + way in and out)
-  const int nk = (p.K + kBK - 1) / kBK;
-  const long long tiles = static_cast<long long>(a.tiles) * sections * ((p.O + 127) / 128);
-  long long best = 0;
-  for (int splits = 1; splits <= 8 && splits <= nk; splits *= 2) {
-    const int slots = splits <= 2 ? num_sms : int(0.85 * num_sms) / splits * splits;
-    const long long cost = (tiles * splits + slots - 1) / slots *
-                           (static_cast<long long>((nk + splits - 1) / splits) * 1150 + 6000 + (splits > 1 ? 3000 : 0));
-    if (best == 0 || cost < best) best = cost, a.splits = splits;
-  }
+  a.splits = splits;
   const long long gx = static_cast<long long>(a.splits) * a.tiles * sections;
   if (gx > INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid(unsigned(gx), (p.O + 127) / 128);

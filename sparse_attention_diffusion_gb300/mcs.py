@@ -28,7 +28,7 @@ EXPORTS = ("mcs_workspace_size", "mcs_group_pddp", "mcs_dense_attn", "mcs_anchor
            "mcs_cache_ring_acquire", "mcs_cache_ring_release", "mcs_cache_ring_destroy",
            "mcs_selftest_wait_timeout", "mcs_pddp_dirs_size", "mcs_group_pddp_warm", "mcs_selftest_ex2_rate",
            "mcs_rope_table_size", "mcs_rope_table", "mcs_rope_apply", "mcs_qk_norm_rope",
-           "mcs_qk_norm_rope_bwd_workspace_size", "mcs_qk_norm_rope_bwd", "mcs_linear")
+           "mcs_qk_norm_rope_bwd_workspace_size", "mcs_qk_norm_rope_bwd", "mcs_linear", "mcs_linear_plan")
 
 
 class McsError(RuntimeError):
@@ -57,6 +57,10 @@ class mcs_linear_desc(ctypes.Structure):
     # "in" and "out" of the C struct are in_features and out_features here
     _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("in_features", ctypes.c_int),
                 ("out_features", ctypes.c_int), ("heads", ctypes.c_int), ("dtype", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+class mcs_linear_choice(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int), ("tile", ctypes.c_int), ("slices", ctypes.c_int), ("accumulators", ctypes.c_int)]
 
 
 ROPE_STYLES = {"interleaved": 0, "half": 1}
@@ -116,6 +120,7 @@ def load(build_if_missing: bool = False):
         "mcs_qk_norm_rope_bwd_workspace_size": (Z, [D]),
         "mcs_qk_norm_rope_bwd": (I, [D, R, P, P, P, P, V, P, P, F, P, P, P, P, P, P, P, P, P, Z, S]),
         "mcs_linear": (I, [ctypes.POINTER(mcs_linear_desc), P, P, P, P, P, P, S]),
+        "mcs_linear_plan": (I, [ctypes.POINTER(mcs_linear_desc), I, I, ctypes.POINTER(mcs_linear_choice)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -578,6 +583,16 @@ def mcs_linear(desc, x, w, bias, gate, residual, y, stream=None):
     rp, yp = _exactly("residual", residual, rows, dt), _exactly("y", y, rows, dt)
     _on_device(x, w, bias, gate, residual, y)
     _check("mcs_linear", load().mcs_linear(desc, xp, wp, bp, gp, rp, yp, _raw_stream(stream)))
+
+
+LINEAR_KERNELS = ("pairs", "few", "f32_rows", "f32_parts")
+
+
+def mcs_linear_plan(desc, residual=False, num_sms=152):
+    """(kernel, tile, K slices, accumulators a slice) that mcs_linear takes for a description; host only."""
+    c = mcs_linear_choice()
+    _check("mcs_linear_plan", load().mcs_linear_plan(desc, 1 if residual else 0, int(num_sms), ctypes.byref(c)))
+    return LINEAR_KERNELS[c.kernel], c.tile, c.slices, c.accumulators
 
 
 # ---------------------------------------------------------------- convenience: buffers for one layer
