@@ -21,8 +21,10 @@ __device__ uint32_t g_status_word;  // OR of mcs::kStatus* bits raised by kernel
 std::atomic<uint64_t> g_launches{0};
 
 constexpr int kMaxDevices = 64;
-uint32_t* g_status_ptr[kMaxDevices] = {};
-int g_num_sms[kMaxDevices] = {};
+// Set once per device, by whichever thread comes first: the pointer after the SM count, so that a thread that sees
+// the one sees the other.
+std::atomic<uint32_t*> g_status_ptr[kMaxDevices] = {};
+std::atomic<int> g_num_sms[kMaxDevices] = {};
 
 // Rows of pass-2 scores kept in the workspace at once (each row is N fp32).
 constexpr long long kSelectRows = 4096;
@@ -64,16 +66,25 @@ bool aligned16_or_null(const void* p) { return p == nullptr || aligned16(p); }
 mcs_status device_state(uint32_t** status, int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MCS_ERR_CUDA;
-  if (g_status_ptr[dev] == nullptr) {
+  // Tensor maps are encoded by the driver, which wants a current context; in a thread that has made no call yet
+  // there is none, and cudaGetDevice does not make one.
+  thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return MCS_ERR_CUDA;
+    bound = dev;
+  }
+  uint32_t* ptr = g_status_ptr[dev].load(std::memory_order_acquire);
+  if (ptr == nullptr) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return MCS_ERR_CUDA;
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MCS_ERR_CUDA;
-    g_num_sms[dev] = n;
-    g_status_ptr[dev] = static_cast<uint32_t*>(p);
+    ptr = static_cast<uint32_t*>(p);
+    g_num_sms[dev].store(n, std::memory_order_relaxed);
+    g_status_ptr[dev].store(ptr, std::memory_order_release);
   }
-  *status = g_status_ptr[dev];
-  if (sms) *sms = g_num_sms[dev];
+  *status = ptr;
+  if (sms) *sms = g_num_sms[dev].load(std::memory_order_relaxed);
   return MCS_OK;
 }
 
