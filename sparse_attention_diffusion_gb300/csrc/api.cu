@@ -63,22 +63,24 @@ mcs_status check_desc(const mcs_desc* desc, Dims* o) {
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned16_or_null(const void* p) { return p == nullptr || aligned16(p); }
 
+using mcs::from_cuda;
+
 mcs_status device_state(uint32_t** status, int* sms) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MCS_ERR_CUDA;
+  if (from_cuda(cudaGetDevice(&dev)) != MCS_OK || dev < 0 || dev >= kMaxDevices) return MCS_ERR_CUDA;
   // Tensor maps are encoded by the driver, which wants a current context; in a thread that has made no call yet
   // there is none, and cudaGetDevice does not make one.
   thread_local int bound = -1;
   if (bound != dev) {
-    if (cudaSetDevice(dev) != cudaSuccess) return MCS_ERR_CUDA;
+    if (from_cuda(cudaSetDevice(dev)) != MCS_OK) return MCS_ERR_CUDA;
     bound = dev;
   }
   uint32_t* ptr = g_status_ptr[dev].load(std::memory_order_acquire);
   if (ptr == nullptr) {
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return MCS_ERR_CUDA;
+    if (from_cuda(cudaGetSymbolAddress(&p, g_status_word)) != MCS_OK) return MCS_ERR_CUDA;
     int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MCS_ERR_CUDA;
+    if (from_cuda(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != MCS_OK) return MCS_ERR_CUDA;
     ptr = static_cast<uint32_t*>(p);
     g_num_sms[dev].store(n, std::memory_order_relaxed);
     g_status_ptr[dev].store(ptr, std::memory_order_release);
@@ -87,8 +89,6 @@ mcs_status device_state(uint32_t** status, int* sms) {
   if (sms) *sms = g_num_sms[dev].load(std::memory_order_relaxed);
   return MCS_OK;
 }
-
-mcs_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MCS_OK : MCS_ERR_CUDA; }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -234,7 +234,7 @@ mcs_status anchor_select_rows(const mcs_desc* desc, const void* q, const void* k
       p.status = status;
       e = simt_colsum(p, nrows, s);
     }
-    if (e != cudaSuccess) return MCS_ERR_CUDA;
+    if (e != cudaSuccess) return from_cuda(e);
     TopkParams t{};
     t.scores = scores;
     t.perm = perm;
@@ -247,7 +247,7 @@ mcs_status anchor_select_rows(const mcs_desc* desc, const void* q, const void* k
     t.K = K;
     t.row0 = static_cast<int>(r0);
     t.status = status;
-    if ((e = topk_rows(t, nrows, s)) != cudaSuccess) return MCS_ERR_CUDA;
+    if ((e = topk_rows(t, nrows, s)) != cudaSuccess) return from_cuda(e);
   }
   return MCS_OK;
 }
@@ -256,6 +256,13 @@ void note_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n), std::
 mcs_status validate_desc(const mcs_desc* desc) {
   Dims dm;
   return check_desc(desc, &dm);
+}
+// MCS_ERR_CUDA for a failed runtime call, whose error is taken off the thread: left there, the next launch would
+// report it as its own.
+mcs_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return MCS_OK;
+  (void)cudaGetLastError();
+  return MCS_ERR_CUDA;
 }
 mcs_status current_device(uint32_t** status, int* sms) { return device_state(status, sms); }
 uint32_t* status_word_for_current_device() {
@@ -521,15 +528,14 @@ mcs_status mcs_residual_apply(const mcs_desc* desc, const void* o_sparse, const 
 }
 
 mcs_status mcs_check_status(mcs_stream stream) {
-  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MCS_ERR_CUDA;
+  mcs_status st = from_cuda(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
   uint32_t* status = nullptr;
-  mcs_status st = device_state(&status, nullptr);
-  if (st != MCS_OK) return st;
+  if (st != MCS_OK || (st = device_state(&status, nullptr)) != MCS_OK) return st;
   uint32_t v = 0;
-  if (cudaMemcpy(&v, status, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MCS_ERR_CUDA;
+  if ((st = from_cuda(cudaMemcpy(&v, status, sizeof(v), cudaMemcpyDeviceToHost))) != MCS_OK) return st;
   if (v != 0) {
     const uint32_t zero = 0;
-    if (cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return MCS_ERR_CUDA;
+    if ((st = from_cuda(cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice))) != MCS_OK) return st;
   }
   if (v & mcs::kStatusTimeout) return MCS_ERR_DEVICE_TIMEOUT;
   if (v & mcs::kStatusBounds) return MCS_ERR_DEVICE_BOUNDS;

@@ -19,6 +19,8 @@ mcs_status anchor_select_rows(const mcs_desc* desc, const void* q, const void* k
 
 // The checks every entry point makes of its mcs_desc (api.cu).
 mcs_status validate_desc(const mcs_desc* desc);
+// MCS_OK, or MCS_ERR_CUDA with the thread's last error cleared.
+mcs_status from_cuda(cudaError_t e);
 // Status word and SM count of the current device.
 mcs_status current_device(uint32_t** status, int* sms);
 

@@ -14,7 +14,7 @@ namespace {
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned16_or_null(const void* p) { return p == nullptr || aligned16(p); }
-mcs_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MCS_OK : MCS_ERR_CUDA; }
+using mcs::from_cuda;
 
 // Checks a rope by itself and fills the kernels' geometry; entries: table pairs.
 mcs_status check_rope(const mcs_rope* r, mcs::RopeGeom* g, long long* entries) {

@@ -54,8 +54,8 @@ cudaError_t launch_overlapped(void (*kern)(Params...), dim3 grid, int threads, s
   }
   cfg.attrs = attr;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, Params(args)...);
-  note_launches(1);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  if (e == cudaSuccess) note_launches(1);
+  return e;
 }
 
 }  // namespace mcs
