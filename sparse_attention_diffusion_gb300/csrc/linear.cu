@@ -23,7 +23,10 @@
 //                plain stores along the row)
 // The accumulator is double-buffered in tensor memory (2 x 256 columns), so a
 // tile's epilogue runs under the next tile's products. A long row takes several
-// accumulators (linear.h), which the epilogue's warps sum in registers meanwhile. Tiles are walked in bands
+// accumulators (linear.h), which the epilogue's warps sum in registers meanwhile: 128 of
+// them a thread, for which the other warps hand registers over (without that some are
+// spilled, and reloads from local memory beside the copies held the next tile up: 75,600 x
+// 5,120 -> 5,120 with gated residual 2.50 ms instead of 2.33). Tiles are walked in bands
 // of eight row tiles, column by column, which keeps the band's x rows and the
 // current columns of w in L2.
 //
@@ -50,6 +53,10 @@ namespace {
 constexpr int kMaxStages = 9;
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
+// Registers a thread of the long-row kernels: all warps start with kLaunchRegs; the control warps' go to the
+// epilogue's, which hold 128 sums.
+constexpr int kLaunchRegs = 168, kControlRegs = 56, kEpiRegs = 224;
+static_assert(128 * kControlRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * kLaunchRegs, "an increase would wait forever");
 constexpr int kHalfTile = 128 * 128;      // bytes of 128 rows x 64 columns
 constexpr int kRing = 6 * 2 * kHalfTile;  // six stages of the widest tile, more of narrower ones
 constexpr int kPatchOff = kRing;
@@ -90,17 +97,12 @@ __device__ __forceinline__ Words32 row32(const __nv_bfloat16* row, int o, int le
   for (int q = 0; q < 4; ++q) r.w[q] = o + 8 * q < len ? *reinterpret_cast<const uint4*>(row + o + 8 * q) : uint4{};
   return r;
 }
-// Adds 32 columns of tensor memory to fp32 sums, 16 at a time where 32 more registers would be spilled.
-template <int kCols>
+// Adds 32 columns of tensor memory to fp32 sums.
 __device__ __forceinline__ void add_tmem32(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld32(at, r);
 #pragma unroll
-  for (int h = 0; h < 32; h += kCols) {
-    uint32_t r[kCols];
-    if constexpr (kCols == 16) tmem_ld16(at + h, r);
-    else tmem_ld32(at, r);
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) v[h + i] += __uint_as_float(r[i]);
-  }
+  for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void get_tmem32(uint32_t at, float (&v)[32]) {
   uint32_t r[32];
@@ -182,8 +184,11 @@ __device__ __forceinline__ void store_odd(const LinearParams& p, int rows, int s
 }
 
 // kPieces: 0 for rows of one accumulator; otherwise the pieces of 32 columns that a warp sums in registers, 3 or 4
-// (tiles of up to 192 and 256 columns).
-template <int kAct, int kPieces>
+// (tiles of up to 192 and 256 columns). kBack: how long rows leave. With one tile a pair the sums go back to tensor
+// memory, which keeps the way out's code short (452 x 4,096 -> 5,120 18.8 us against 19.9); with more tiles that
+// would keep the next tile's second accumulator waiting (75,600 x 5,120 -> 5,120 with gated residual 2.42 ms against
+// 2.33).
+template <int kAct, int kPieces, bool kBack>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_r,
@@ -228,59 +233,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   grid_inputs_ready();
   grid_let_next_start();
 
-  if (warp == 0) {
-    const int bn2 = tl.bn / 2;
-    const uint32_t bytes = uint32_t(2 * (kHalfTile + bn2 * 128));
-    bool ok = true;
-    int s = 0;
-    uint32_t phase = 0;
-    for (int t = pair; t < tl.total && ok; t += pairs) {
-      const Tile ti = tile_at(tl, t);
-      const int xrow = ti.row0 + rank * 128, wrow = ti.o0 + rank * bn2, z0 = ti.sec * p.heads;
-      for (int i = 0; i < nk; ++i) {
-        if (!(ok = warp_all(mbar_wait(empty + s, phase ^ 1, st)))) break;
-        const int k = i * 64;
-        const uint32_t bar = cluster_map(smem_u32(full + s), 0);
-        const uint32_t dst = sbase + s * tl.stage_bytes;
-        if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
-          tma_load_3d_pair(dst, &map_x, k & tl.col_mask, xrow, z0 + (k >> tl.head_shift), bar);
-          tma_load_3d_pair(dst + kHalfTile, &map_w, k, wrow, 0, bar);
-        }
-        __syncwarp();
-        if (++s == tl.stages) s = 0, phase ^= 1;
-      }
-    }
-    if (!ok) {
-      if (lane == 0) raise_status(st, kStatusTimeout);
-      settle_copies();  // normally the MMAs have consumed every copy before the pair exits
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0) {
-      const uint32_t idesc = idesc_bf16_f32(256, 0, 0, 0) | (uint32_t(tl.bn >> 3) << 17);
-      bool ok = true, issued = false;
-      int s = 0, it = 0, b = 0;  // ring stage, accumulators begun, the current one's buffer
+  if (warp < 4) {
+    if constexpr (kLong) registers_down<kControlRegs>();
+    if (warp == 0) {
+      const int bn2 = tl.bn / 2;
+      const uint32_t bytes = uint32_t(2 * (kHalfTile + bn2 * 128));
+      bool ok = true;
+      int s = 0;
       uint32_t phase = 0;
       for (int t = pair; t < tl.total && ok; t += pairs) {
+        const Tile ti = tile_at(tl, t);
+        const int xrow = ti.row0 + rank * 128, wrow = ti.o0 + rank * bn2, z0 = ti.sec * p.heads;
         for (int i = 0; i < nk; ++i) {
-          const int step = kLong ? i % kAccSteps : i;
-          if (step == 0) {
-            b = it & 1;
-            if (!(ok = warp_all(mbar_wait(acc_empty + b, ((it++ >> 1) & 1) ^ 1, st)))) break;
-          }
-          if (!(ok = warp_all(mbar_wait(full + s, phase, st)))) break;
-          tc_fence_after();
-          issued = true;
-          const uint32_t a = desc_lo_kmajor(sbase + s * tl.stage_bytes);
-          const uint32_t w = desc_lo_kmajor(sbase + s * tl.stage_bytes + kHalfTile);
+          if (!(ok = warp_all(mbar_wait(empty + s, phase ^ 1, st)))) break;
+          const int k = i * 64;
+          const uint32_t bar = cluster_map(smem_u32(full + s), 0);
+          const uint32_t dst = sbase + s * tl.stage_bytes;
           if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              tc_mma_ss_lo_pair(tmem + b * 256, a + kstep_kmajor(ks), w + kstep_kmajor(ks), idesc,
-                                (step > 0 || ks > 0) ? 1u : 0u);
-            tc_commit_pair(empty + s);
-            if ((kLong && step == kAccSteps - 1) || i == nk - 1) tc_commit_pair(acc_full + b);
+            if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+            tma_load_3d_pair(dst, &map_x, k & tl.col_mask, xrow, z0 + (k >> tl.head_shift), bar);
+            tma_load_3d_pair(dst + kHalfTile, &map_w, k, wrow, 0, bar);
           }
           __syncwarp();
           if (++s == tl.stages) s = 0, phase ^= 1;
@@ -288,16 +260,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         if (lane == 0) raise_status(st, kStatusTimeout);
-        if (issued) {
-          if (elect_one()) tc_commit_pair(drain);
-          __syncwarp();
-          mbar_drain(drain, 0);
-        }
-        settle_copies();
+        settle_copies();  // normally the MMAs have consumed every copy before the pair exits
       }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (rank == 0) {
+        const uint32_t idesc = idesc_bf16_f32(256, 0, 0, 0) | (uint32_t(tl.bn >> 3) << 17);
+        bool ok = true, issued = false;
+        int s = 0, it = 0, b = 0;  // ring stage, accumulators begun, the current one's buffer
+        uint32_t phase = 0;
+        for (int t = pair; t < tl.total && ok; t += pairs) {
+          for (int i = 0; i < nk; ++i) {
+            const int step = kLong ? i % kAccSteps : i;
+            if (step == 0) {
+              b = it & 1;
+              if (!(ok = warp_all(mbar_wait(acc_empty + b, ((it++ >> 1) & 1) ^ 1, st)))) break;
+            }
+            if (!(ok = warp_all(mbar_wait(full + s, phase, st)))) break;
+            tc_fence_after();
+            issued = true;
+            const uint32_t a = desc_lo_kmajor(sbase + s * tl.stage_bytes);
+            const uint32_t w = desc_lo_kmajor(sbase + s * tl.stage_bytes + kHalfTile);
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                tc_mma_ss_lo_pair(tmem + b * 256, a + kstep_kmajor(ks), w + kstep_kmajor(ks), idesc,
+                                  (step > 0 || ks > 0) ? 1u : 0u);
+              tc_commit_pair(empty + s);
+              if ((kLong && step == kAccSteps - 1) || i == nk - 1) tc_commit_pair(acc_full + b);
+            }
+            __syncwarp();
+            if (++s == tl.stages) s = 0, phase ^= 1;
+          }
+        }
+        if (!ok) {
+          if (lane == 0) raise_status(st, kStatusTimeout);
+          if (issued) {
+            if (elect_one()) tc_commit_pair(drain);
+            __syncwarp();
+            mbar_drain(drain, 0);
+          }
+          settle_copies();
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else {
+    if constexpr (kLong) registers_up<kEpiRegs>();
     const int e = warp - 4, quarter = e & 3, half = e >> 2;
     const uint32_t patch = sbase + kPatchOff + e * kPatch;
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
@@ -323,10 +332,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     if (add && pair < tl.total && half < nchunks) fetch(tile_at(tl, pair), half, 0);
     for (int t = pair; t < tl.total; t += pairs, ++it) {
+      [[maybe_unused]] float sum[kLong ? kPieces : 1][32];
       if constexpr (kLong) {
-        // the accumulators of the row are summed in registers; the sums take the last one's place in tensor memory
-        // and leave from there as those of a short row do
-        float sum[kPieces][32];
+        // The accumulators of the row are summed in registers. With kBack the sums go back over the last one, from
+        // where they leave as those of a short row do; otherwise its columns are the next tile's at once, and the
+        // pieces move up in registers.
         for (int i = 0;; i += kAccSteps, ++it) {
           const int b = it & 1;
           const bool last = i + kAccSteps >= nk;
@@ -337,29 +347,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (half + 2 * c >= nchunks) continue;
             const uint32_t at = tmem + lane_off + b * 256 + (half + 2 * c) * 32;
             if (i == 0) get_tmem32(at, sum[c]);
-            else add_tmem32<kPieces == 4 ? 16 : 32>(at, sum[c]);
-            if (last) put_tmem32(at, sum[c]);
+            else add_tmem32(at, sum[c]);
+            if (kBack && last) put_tmem32(at, sum[c]);
           }
-          if (last) {
+          if (kBack && last) {
             tmem_wait_st();
             break;
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
+          if (last) break;
         }
         if (!ok) break;
       }
       const int b = it & 1;
-      if (half >= nchunks) {  // nothing of this accumulator for this warp
+      constexpr bool kHeld = !kLong || kBack;  // the accumulator is still to be read
+      if (half >= nchunks) {             // nothing of it for this warp
         if (!kLong && !(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
-        if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
+        if (kHeld && lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
         continue;
       }
       const Tile ti = tile_at(tl, t);
       const int n0 = ti.row0 + rank * 128 + quarter * 32;
       const int n = n0 + lane, m = ti.sec * tl.rows + n;  // this lane's row
       const __nv_bfloat16* grow = gate ? gate + size_t(n < tl.rows ? tl.by_batch.div(m) : 0) * p.O : nullptr;
+      Words32 bw, gw;  // the current piece's bias and gate
+      auto read_rows = [&](int cc) {
+        const int o = ti.o0 + cc * 32;
+        if (vec && bias) bw = row32(bias, o, p.O);
+        if (vec && grow) gw = row32(grow, o, p.O);
+      };
+      read_rows(half);
 #pragma unroll 1
       for (int cc = half; cc < nchunks; cc += 2) {
         const int o = ti.o0 + cc * 32;
@@ -368,14 +387,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (cc + 2 < nchunks) fetch(ti, cc + 2, buf ^ 1);
           else if (t + pairs < tl.total) fetch(tile_at(tl, t + pairs), half, buf ^ 1);
         }
-        const bool biased = vec && live && bias != nullptr;
-        Words32 bw;
-        if (biased) bw = row32(bias, o, p.O);
         if (!kLong && cc == half && !(ok = warp_all(mbar_wait(acc_full + b, (it >> 1) & 1, st)))) break;
         tc_fence_after();
         float v[32];
-        get_tmem32(tmem + lane_off + b * 256 + cc * 32, v);
-        if (cc + 2 >= nchunks) {  // last read of this accumulator by this warp
+        if constexpr (kHeld) {
+          get_tmem32(tmem + lane_off + b * 256 + cc * 32, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = sum[0][i];
+#pragma unroll
+            for (int c = 1; c < kPieces; ++c) sum[c - 1][i] = sum[c][i];
+          }
+        }
+        if (kHeld && cc + 2 >= nchunks) {  // last read of this accumulator by this warp
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(cluster_map(smem_u32(acc_empty + b), 0));
@@ -390,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           buf ^= 1;
           continue;
         }
-        if (biased) {
+        if (bias) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float t8[8];
@@ -401,7 +426,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         activate<kAct>(v);
         if (grow) {
-          const Words32 gw = row32(grow, o, p.O);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float t8[8];
@@ -410,6 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 8; ++i) v[8 * q + i] *= t8[i];
           }
         }
+        if (cc + 2 < nchunks) read_rows(cc + 2);  // arrive while this piece leaves
         const uint32_t piece = patch + buf * (kPatch / 2);
         if (add) {
           if (!(ok = warp_all(mbar_wait(rbar + buf, (rphase >> buf) & 1, st)))) break;
@@ -463,15 +488,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
+// allow_smem for a kernel that moves registers between its warps, which must have been compiled with as many as
+// it counts on.
+template <auto kKern>
+cudaError_t allow_long() {
+  static std::atomic<bool> checked{false};
+  if (!checked.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa{};
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kKern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    checked.store(true, std::memory_order_relaxed);
+  }
+  return allow_smem<kKern>(kSmemAlloc);
+}
 template <int kAct>
 cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& my, const CUtensorMap& mr,
                        const LinearParams& p, const Tiling& t, int pairs, cudaStream_t s) {
   auto start = [&](auto kern, cudaError_t e) {
     return e != cudaSuccess ? e : launch_overlapped(kern, dim3(2 * pairs), kThreads, kSmemAlloc, s, 0, mx, mw, my, mr, p, t);
   };
-  if (p.K <= 64 * kOneAccSteps) return start(linear_pair_kernel<kAct, 0>, allow_smem<linear_pair_kernel<kAct, 0>>(kSmemAlloc));
-  return t.bn <= 192 ? start(linear_pair_kernel<kAct, 3>, allow_smem<linear_pair_kernel<kAct, 3>>(kSmemAlloc))
-                     : start(linear_pair_kernel<kAct, 4>, allow_smem<linear_pair_kernel<kAct, 4>>(kSmemAlloc));
+  if (p.K <= 64 * kOneAccSteps)
+    return start(linear_pair_kernel<kAct, 0, false>, allow_smem<linear_pair_kernel<kAct, 0, false>>(kSmemAlloc));
+  const bool one = t.total <= pairs;
+  if (t.bn <= 192)
+    return one ? start(linear_pair_kernel<kAct, 3, true>, allow_long<linear_pair_kernel<kAct, 3, true>>())
+               : start(linear_pair_kernel<kAct, 3, false>, allow_long<linear_pair_kernel<kAct, 3, false>>());
+  return one ? start(linear_pair_kernel<kAct, 4, true>, allow_long<linear_pair_kernel<kAct, 4, true>>())
+             : start(linear_pair_kernel<kAct, 4, false>, allow_long<linear_pair_kernel<kAct, 4, false>>());
 }
 
 cudaError_t launch_pair(const LinearParams& p, int bn, int num_sms, cudaStream_t s) {

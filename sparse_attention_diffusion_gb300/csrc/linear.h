@@ -12,7 +12,7 @@ namespace mcs {
 // sum, half a last bit on average. Up to kOneAccSteps (1,536 columns) a row has one accumulator;
 // a longer one takes one for every kAccSteps (1,024 columns), and they are added in fp32 registers,
 // to nearest. Against one accumulator for any length that costs about half a microsecond a call
-// (452 x 4,096 -> 5,120 18.1 -> 18.6 us, 2,048 x 8,192 -> 2,048 41.4 -> 42.1 us; 1,024 x 2,048 ->
+// (452 x 4,096 -> 5,120 18.1 -> 18.8 us, 2,048 x 8,192 -> 2,048 42.1 -> 42.8 us; 1,024 x 2,048 ->
 // 1,536 9.4 -> 10.2 us, which is why shorter rows are left whole), and at 5,120 columns 0.08 % of
 // the bf16 outputs instead of 0.28 % differ from the rounded fp32 sum's.
 constexpr int kOneAccSteps = 24;

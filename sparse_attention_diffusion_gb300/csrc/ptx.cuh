@@ -104,6 +104,17 @@ __device__ __forceinline__ T warp_uniform(T v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
+// Hand registers from one warpgroup of the block to another (each by all four warps of a warpgroup; an
+// increase waits until the block's pool of launch registers has enough).
+template <int kRegs>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // ---------------------------------------------------------------- clusters
 // All threads of all CTAs of the cluster; shared-memory writes before it are
 // visible to the other CTAs after it.
