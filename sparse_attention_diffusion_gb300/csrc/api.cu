@@ -1,6 +1,9 @@
 // C ABI of libmcs (declared in include/mcs.h): argument validation, workspace
 // layout, dispatch to the bf16 tcgen05 kernels or the fp32 SIMT kernels, and
 // the device status word. Nothing here allocates device memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -65,15 +68,25 @@ bool aligned16_or_null(const void* p) { return p == nullptr || aligned16(p); }
 
 using mcs::from_cuda;
 
+bool current_context(CUcontext* ctx) {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q{};
+  if (from_cuda(cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &fn, 12000, cudaEnableDefault, &q)) != MCS_OK ||
+      q != cudaDriverEntryPointSuccess)
+    return false;
+  return reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(fn)(ctx) == CUDA_SUCCESS;
+}
+
 mcs_status device_state(uint32_t** status, int* sms) {
   int dev = 0;
   if (from_cuda(cudaGetDevice(&dev)) != MCS_OK || dev < 0 || dev >= kMaxDevices) return MCS_ERR_CUDA;
-  // Tensor maps are encoded by the driver, which wants a current context; in a thread that has made no call yet
-  // there is none, and cudaGetDevice does not make one.
-  thread_local int bound = -1;
-  if (bound != dev) {
-    if (from_cuda(cudaSetDevice(dev)) != MCS_OK) return MCS_ERR_CUDA;
-    bound = dev;
+  // Tensor maps are encoded by the driver, which wants a current context; a thread that has made no call yet has
+  // none, and cudaGetDevice does not make one. One that is there, a caller's own too, stays.
+  thread_local bool bound = false;
+  if (!bound) {
+    CUcontext ctx = nullptr;
+    if (current_context(&ctx) && ctx == nullptr && from_cuda(cudaSetDevice(dev)) != MCS_OK) return MCS_ERR_CUDA;
+    bound = true;
   }
   uint32_t* ptr = g_status_ptr[dev].load(std::memory_order_acquire);
   if (ptr == nullptr) {

@@ -53,6 +53,46 @@ def test_first_call_of_a_thread():
     mcs.mcs_check_status()
 
 
+CONTEXT = """
+import ctypes, threading, torch
+from sparse_attention_diffusion_gb300 import mcs
+mcs.load()
+cu = ctypes.CDLL("libcuda.so.1")
+x, w = torch.randn(1, 40, 128).bfloat16().cuda(), torch.randn(72, 128).bfloat16().cuda()
+y = torch.zeros(1, 40, 72, dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+before, after = ctypes.c_void_p(), ctypes.c_void_p()
+cu.cuCtxGetCurrent(ctypes.byref(before))
+mcs.mcs_linear(mcs.linear_desc(1, 40, 128, 72, torch.bfloat16), x, w, None, None, None, y)
+cu.cuCtxGetCurrent(ctypes.byref(after))
+assert before.value and before.value == after.value
+failed = []
+def work():
+    # a thread with no context of its own gets the device's, and keeps it
+    now = ctypes.c_void_p()
+    cu.cuCtxGetCurrent(ctypes.byref(now))
+    if now.value:
+        failed.append("a new thread has a context")
+    mcs.mcs_linear(mcs.linear_desc(1, 40, 128, 72, torch.bfloat16), x, w, None, None, None, y, stream=torch.cuda.default_stream())
+    cu.cuCtxGetCurrent(ctypes.byref(now))
+    if now.value != before.value:
+        failed.append("another context")
+t = threading.Thread(target=work)
+t.start()
+t.join()
+assert not failed, failed
+torch.cuda.synchronize()
+mcs.mcs_check_status()
+"""
+
+
+def test_a_context_that_is_there_stays():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    mcs.load(build_if_missing=True)
+    r = subprocess.run([sys.executable, "-c", CONTEXT], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 THREADS = """
 import threading, torch
 from sparse_attention_diffusion_gb300 import mcs
