@@ -294,7 +294,8 @@ mcs_status mcs_rope_table(const mcs_rope *rope, float *table, mcs_stream stream)
  * fp32 arithmetic, one rounding. Errors: MCS_ERR_INVALID_ARG for a bad pointer,
  * stride or grid (the grid must fit in N), MCS_ERR_UNSUPPORTED for a rope
  * outside the set above. desc->C (which must be valid), scale and pddp_iters have no
- * effect here. */
+ * effect here. An element that is infinite or NaN leaves its pair so, in tokens that do
+ * not turn as well. */
 mcs_status mcs_rope_apply(const mcs_desc *desc, const mcs_rope *rope, const float *table, const int32_t *pos,
                           const void *x, const mcs_strides *xs, void *out, const mcs_strides *os, int inverse,
                           mcs_stream stream);
@@ -306,8 +307,8 @@ mcs_status mcs_rope_apply(const mcs_desc *desc, const mcs_rope *rope, const floa
  * packed output of a projection; q_out, k_out, v_out: contiguous [B,H,N,d], what
  * mcs_dense_attn and the others take. An output may take its own input's place if
  * that is contiguous; other overlaps are MCS_ERR_INVALID_ARG, as below. Each of the
- * three may be absent (input and output both NULL), not all. wq, wk: [d] in the I/O dtype, or NULL for 1.
- * eps: finite, > 0. */
+ * three may be absent (input and output both NULL), not all. wq, wk: [d] in the I/O
+ * dtype, or NULL for 1. eps: finite, > 0. */
 mcs_status mcs_qk_norm_rope(const mcs_desc *desc, const mcs_rope *rope, const float *table, const int32_t *pos,
                             const void *q, const void *k, const void *v, const mcs_strides *in, const void *wq,
                             const void *wk, float eps, void *q_out, void *k_out, void *v_out, mcs_stream stream);
