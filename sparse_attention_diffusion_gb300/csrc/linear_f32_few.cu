@@ -4,6 +4,7 @@
 #include "launch.cuh"
 #include "linear.h"
 #include "linear_epi.cuh"
+#include "linear_few.h"
 #include "ptx.cuh"
 
 namespace mcs {
@@ -105,7 +106,7 @@ LinearPlan plan_linear_f32(const LinearParams& p, int num_sms) {
   long long best = 0;
   int slices = 1;
   for (int splits = 1; splits <= 8 && splits <= nk; splits *= 2) {
-    const int slots = splits <= 2 ? num_sms : int(0.85 * num_sms) / splits * splits;
+    const int slots = few_slots(splits, num_sms);
     const long long cost = (tiles * splits + slots - 1) / slots *
                            (static_cast<long long>((nk + splits - 1) / splits) * 1150 + 6000 + (splits > 1 ? 3000 : 0));
     if (best == 0 || cost < best) best = cost, slices = splits;

@@ -13,7 +13,9 @@ struct FewPlan {
 // CTAs that run at once, one per SM: clusters of more than two leave SMs of a GPU
 // processing cluster over (144 CTAs in clusters of three took two waves on 152 SMs).
 inline int few_slots(int splits, int num_sms) {
-  return splits <= 2 ? num_sms : int(0.85 * num_sms) / splits * splits;
+  if (splits <= 2) return num_sms;
+  const int clusters = int(0.85 * num_sms) / splits;
+  return (clusters > 0 ? clusters : 1) * splits;
 }
 // Tensor memory: an accumulator's columns, and how many accumulators a slice of `steps` k steps holds at once. All
 // of them stay until the end where they fit in half of the tensor memory; otherwise, up to 128 tokens, two take turns

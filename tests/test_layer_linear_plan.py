@@ -43,3 +43,12 @@ def test_one_accumulator_takes_1536_columns_at_most(lib, B, N, heads):
         assert 16 <= tile <= 256 and 1 <= slices <= 8
         steps = -(-(-(-K // 64)) // slices)
         assert accs == (1 if steps <= 24 else -(-steps // 16))
+
+
+@pytest.mark.parametrize("sms", [8, 9, 12, 132, 1024])
+def test_any_number_of_sms(lib, sms):
+    for dtype in (torch.bfloat16, torch.float32):
+        for N in (1, 64, 700, 5000):
+            for K in (64, 512, 5120):
+                kernel, tile, slices, accs = plan(1, N, K, 1000, dtype, num_sms=sms)
+                assert 1 <= slices <= 8 and tile >= 2 and accs >= 1
