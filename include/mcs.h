@@ -349,8 +349,8 @@ mcs_status mcs_qk_norm_rope_bwd(const mcs_desc *desc, const mcs_rope *rope, cons
  * tensor cores, every number as the sum of three bf16 parts: a sum's error stays below
  * (12 * 2^-23 + (in / 32 + 9) * 2^-24) * sum |x w| + 2^-134 * sum (|x| + |w|) (numbers
  * keep their bits down to 2^-133) + (in / 32 + 1) * 2^-126; sums with numbers of 3.39e38
- * and more are added in order on the CUDA cores. Infinite elements give what their products and sums are. No
- * workspace. Equal calls give equal bits. */
+ * and more run on the CUDA cores. Infinite elements give what their products and sums
+ * are. No workspace. Equal calls give equal bits. */
 typedef enum { MCS_ACT_NONE = 0, MCS_ACT_GELU_TANH = 1, MCS_ACT_GELU_ERF = 2, MCS_ACT_SILU = 3 } mcs_act;
 typedef struct {
   int B, N;

@@ -127,23 +127,39 @@ __device__ __noinline__ void finish_not_finite(const LinearParams& p, const Spli
                                                int live, int o0, int rank, int warp, int lane) {
   const int d = p.heads > 0 ? p.K / p.heads : p.K, o = o0 + lane * 4;
   const size_t head = size_t(a.rows) * d;
-  const float* w = static_cast<const float*>(p.w);
   for (int r = rank + a.splits * warp; r < live; r += a.splits * kWarps) {
     float v[4];
     joined_sums(a, sbase, r, lane, v);
+    const bool bad = o < p.O && !isfinite(sum4(v));
     const float* x = static_cast<const float*>(p.x) + size_t(sec) * (p.heads > 0 ? p.heads : 1) * head + size_t(row0 + r) * d;
-    if (isfinite(sum4(v))) continue;
-    for (int i = 0; i < 4; ++i) {
-      if (isfinite(v[i]) || o + i >= p.O) continue;
-      float t = 0.f;
-      for (int k = 0; k < p.K && !isnan(t); k += 4) {  // NaN stays
-        const float4 f = *reinterpret_cast<const float4*>(x + (k >> a.head_shift) * head + (k & a.col_mask));
-        const float4 g = *reinterpret_cast<const float4*>(w + size_t(o + i) * p.K + k);
-        t = fmaf(f.w, g.w, fmaf(f.z, g.z, fmaf(f.y, g.y, fmaf(f.x, g.x, t))));
+    for (uint32_t left = __ballot_sync(0xffffffffu, bad); left != 0; left &= left - 1) {
+      const int owner = __ffs(left) - 1, first = o0 + owner * 4;  // the warp sums the four outputs of one lane
+      const float* w[4];
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = static_cast<const float*>(p.w) + size_t(min(first + i, p.O - 1)) * p.K;
+#pragma unroll 2
+      for (int k0 = 0; k0 < p.K; k0 += 128) {
+        const int k = k0 + lane * 4;
+        if (k < p.K) {
+          const float4 f = *reinterpret_cast<const float4*>(x + (k >> a.head_shift) * head + (k & a.col_mask));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 g = *reinterpret_cast<const float4*>(w[i] + k);
+            t[i] = fmaf(f.w, g.w, fmaf(f.z, g.z, fmaf(f.y, g.y, fmaf(f.x, g.x, t[i]))));
+          }
+        }
+        // NaN stays, so a NaN in x ends its row here
+        if (__any_sync(0xffffffffu, isnan(t[0]) && isnan(t[1]) && isnan(t[2]) && isnan(t[3]))) break;
       }
-      v[i] = t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int n = 16; n > 0; n >>= 1) t[i] += __shfl_xor_sync(0xffffffffu, t[i], n);
+        if (lane == owner && !isfinite(v[i])) v[i] = t[i];
+      }
     }
-    finish_row4<kAct>(p, sec * a.rows + row0 + r, o, v);
+    if (bad) finish_row4<kAct>(p, sec * a.rows + row0 + r, o, v);
   }
 }
 
