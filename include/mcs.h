@@ -376,6 +376,51 @@ typedef enum {
 typedef struct { int kernel, tile, slices, accumulators; } mcs_linear_choice;
 mcs_status mcs_linear_plan(const mcs_linear_desc *desc, int with_residual, int num_sms, mcs_linear_choice *choice);
 
+/* ---------------------------------------------------------------------------
+ * Requests of different lengths in one batch: attention over packed sequences, and
+ * (below mcs_linear) projections with an adapter for each request.
+ */
+
+/* S sequences laid one behind the other: queries [H, Tq, d], keys and values
+ * [Hk, Tk, d]. Sequence s holds queries q_start[s] .. q_start[s+1] - 1 and keys
+ * k_start[s] .. k_start[s+1] - 1. Head h reads key head h / (H / Hk). Supported: d in
+ * {64, 128}; H a multiple of Hk, H / Hk <= 64; S, Tq, Tk <= 2^30; H <= 2^20.
+ * scale <= 0 selects 1/sqrt(d). */
+typedef struct {
+  int S;
+  int Tq, Tk;
+  int H, Hk;
+  int d;
+  int dtype;       /* mcs_dtype */
+  int causal;      /* 0: every query sees its sequence's keys; else the last query sees all of them, each query
+                      before it one key less */
+  int max_q;       /* no sequence has more queries; 0: Tq */
+  float scale;
+} mcs_packed_desc;
+
+/* Softmax attention within each sequence: o_i = sum_j softmax_j(scale q_i.k_j) v_j
+ * over the keys that query i sees, and lse_i, the natural-log log-sum-exp. With nq queries and
+ * nk keys and causal, query i sees keys 0 .. i + nk - nq: whole prompts (nk = nq), chunks and
+ * single tokens that continue kept keys (nk > nq). A query that sees no key gets o = 0 and
+ * lse = -infinity. q, o: [H, Tq, d] views (strides qs, os); k, v: [Hk, Tk, d] views (ks,
+ * vs); of mcs_strides head and token count, each a multiple of 16 bytes and such that rows
+ * do not overlap; NULL: contiguous. q_start, k_start: int32 [S + 1] on the device, rising,
+ * 16-byte aligned (one array may serve as both). lse: fp32 [H, Tq] or NULL.
+ * Rows in no sequence (before q_start[0], behind q_start[S]) are left as they were. Bounds that
+ * fall or leave the buffers and sequences of more than max_q queries are flagged
+ * MCS_ERR_DEVICE_BOUNDS; o and lse are then undefined. Values of keys that a query does not see, another sequence's
+ * or later ones, have no effect on it, infinities and NaN included.
+ * BF16 runs on the tensor cores (weights are rounded to bf16 before the sum over the values, the
+ * sum of the weights is not), F32 in fp32. Sums and statistics are fp32, one rounding. Outputs
+ * may not overlap inputs. ws: at least mcs_packed_attn_workspace_size(desc) bytes (0 for an
+ * invalid description; host only); its contents on entry are ignored; calls that may run at the
+ * same time need one each. Equal calls give equal bits. */
+size_t mcs_packed_attn_workspace_size(const mcs_packed_desc *desc);
+mcs_status mcs_packed_attn(const mcs_packed_desc *desc, const void *q, const mcs_strides *qs, const void *k,
+                           const mcs_strides *ks, const void *v, const mcs_strides *vs, const int32_t *q_start,
+                           const int32_t *k_start, void *o, const mcs_strides *os, float *lse, void *ws,
+                           size_t ws_bytes, mcs_stream stream);
+
 /* Synchronises `stream`, then reports (and clears) the device-side flags raised
  * since the last call: MCS_ERR_DEVICE_BOUNDS, MCS_ERR_DEVICE_TIMEOUT, or a
  * sticky CUDA error as MCS_ERR_CUDA. MCS_OK if none. */

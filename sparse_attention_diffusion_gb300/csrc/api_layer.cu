@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "mcs.h"
+#include "api_checks.h"
 #include "api_internal.h"
 #include "common.cuh"
 #include "linear.h"
@@ -12,9 +13,12 @@
 
 namespace {
 
-bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned16_or_null(const void* p) { return p == nullptr || aligned16(p); }
+using mcs::aligned16;
+using mcs::aligned16_or_null;
 using mcs::from_cuda;
+using mcs::overlap;
+using mcs::Range;
+using mcs::range;
 
 // Checks a rope by itself and fills the kernels' geometry; entries: table pairs.
 mcs_status check_rope(const mcs_rope* r, mcs::RopeGeom* g, long long* entries) {
@@ -110,15 +114,6 @@ mcs_status check_linear(const mcs_linear_desc* desc, mcs::LinearParams* p) {
   return MCS_OK;
 }
 
-// Byte ranges, for the refusal of outputs that alias inputs. A null pointer is no range.
-struct Range {
-  const char* at;
-  long long bytes;
-};
-bool overlap(const Range& a, const Range& b) {
-  return a.at != nullptr && b.at != nullptr && a.at < b.at + b.bytes && b.at < a.at + a.bytes;
-}
-Range range(const void* p, long long bytes) { return {static_cast<const char*>(p), bytes}; }
 // From a view's first element to its last.
 Range range(const mcs_desc* d, const void* p, const mcs::ViewStrides& v) {
   const long long n = (d->B - 1) * v.b + (d->H - 1) * v.h + (d->N - 1) * v.n + d->d;

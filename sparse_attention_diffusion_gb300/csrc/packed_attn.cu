@@ -1,0 +1,606 @@
+// Softmax attention over packed sequences on the tcgen05 tensor cores, bf16:
+//   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  lse_i = log sum_j exp(scale q_i . k_j)
+// over the keys j of query i's own sequence that it sees (with a causal mask the last of its nq queries
+// sees all nk keys and each one before it one key less), grouped heads, lengths read on the device.
+//
+// A persistent grid, one CTA per SM, walks the items of packed.h; 224 threads:
+//   warp 5    finds the items (four ahead) and loads by TMA: the item's queries as one box of g heads x
+//             tq tokens, then rings of K and V tiles of 128 keys, K one tile ahead of V;
+//   warp 4    tensor-memory allocation, S_j = Q K_j^T into two buffers;
+//   warp 6    makes V tiles that hold masked keys harmless (below), O += P_j V_j, P from tensor memory;
+//   warps 0-3 softmax, a thread per row, and the row's way out.
+// Tensor memory: S0 [0,128), S1 [128,256), O [256,256+D), P [384,448) columns.
+// The next item's queries, keys and first two S run under the last P V and the way out.
+//
+// Masked keys: their scores become -inf by selection, whatever they are, so P is 0. But 0 times an infinity or a NaN
+// is NaN, and behind a sequence's last key lie another request's values. So in the tiles that hold a key some row
+// does not see, warp 6 (which waits for P meanwhile) overwrites rows past the item's keys with zeros, and replaces
+// what is not finite in the rows that only some tokens see by zero; rows that do see such an element add it on their way out
+// (an infinity or a NaN stays one whatever finite numbers are added).
+//
+// Cut sequences (chunk > 0): an item is one chunk of a sequence's keys, its sums leave as fp32 with the row's
+// maximum and sum, and a second launch joins them.
+#include <cfloat>
+
+#include "attn_common.cuh"
+#include "common.cuh"
+#include "launch.cuh"
+#include "packed.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+#include "tma.cuh"
+
+namespace mcs {
+namespace {
+
+constexpr int kThreads = 224;
+constexpr int kItems = 4;   // items found ahead
+constexpr int kFlags = 2;   // items whose V flags are kept: warp 6 is one item ahead of the way out at most
+
+template <int D>
+struct Cfg {
+  static constexpr int kStages = (D == 128) ? 3 : 6;
+  static constexpr int kTile = (D / 64) * kRegion;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kTile;
+  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kBar = kV + kStages * kTile;
+  static constexpr int kNumBars = 4 * kStages + 2 + 2 + 2 + 2 + 2 + 2 * kItems + 2;
+  static constexpr int kMisc = kBar + kNumBars * 8;  // tensor-memory slot, flags, items
+  static constexpr int kItem = (kMisc + 16 + kFlags * 4 + 15) / 16 * 16;
+  static constexpr int kBytes = kItem + kItems * int(sizeof(PackedItem));
+  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr uint32_t kColS = 0, kColO = 256, kColP = 384;
+};
+static_assert(Cfg<128>::kAlloc <= 227 * 1024 && Cfg<64>::kAlloc <= 227 * 1024, "shared memory");
+
+struct Walk {
+  Divisor by_tq, by_chunk, by_one;
+};
+
+__device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
+  return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
+}
+// Both halves, what is not finite as 0.
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// Rows some .. none - 1 of a V tile, which some tokens do not see, with what is not finite as 0, and rows from none
+// on, which nobody sees, as 0. Whether there was such an element. One warp, 16 bytes a lane.
+template <int D>
+__device__ __forceinline__ bool settle_v(uint32_t v, int some, int none, int lane) {
+  constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes;
+  const int ch = lane % kRowLanes;
+  bool found = false;
+#pragma unroll 4
+  for (int r = some + lane / kRowLanes; r < none; r += kRows) {
+    const uint32_t at = v + sw128_off(r, ch);
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+    if (!(finite_bf16x2(w.x) && finite_bf16x2(w.y) && finite_bf16x2(w.z) && finite_bf16x2(w.w))) {
+      found = true;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(finite_part(w.x)), "r"(finite_part(w.y)),
+                   "r"(finite_part(w.z)), "r"(finite_part(w.w))
+                   : "memory");
+    }
+  }
+  for (int r = none + lane / kRowLanes; r < 128; r += kRows)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + sw128_off(r, ch)), "r"(0) : "memory");
+  return found;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const PackedParams p, const Walk wk) {
+  using L = Cfg<D>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* k_empty = k_full + S;
+  uint64_t* v_full = k_empty + S;
+  uint64_t* v_empty = v_full + S;
+  uint64_t* s_full = v_empty + S;       // [2]
+  uint64_t* s_free = s_full + 2;        // [2]
+  uint64_t* p_full = s_free + 2;
+  uint64_t* p_empty = p_full + 1;
+  uint64_t* q_full = p_empty + 1;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* o_full = q_empty + 1;
+  uint64_t* o_free = o_full + 1;
+  uint64_t* it_full = o_free + 1;       // [kItems]
+  uint64_t* it_empty = it_full + kItems;
+  uint64_t* drain = it_empty + kItems;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile uint32_t* odd = tmem_slot + 4;  // [kFlags] the item's V held something that is not finite and not seen by all
+  PackedItem* items = reinterpret_cast<PackedItem*>(smem + L::kItem);
+
+  const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+  uint32_t* st = p.status;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(k_full + s, 1), mbar_init(k_empty + s, 1), mbar_init(v_full + s, 1), mbar_init(v_empty + s, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(s_full + b, 1), mbar_init(s_free + b, 128), mbar_init(drain + b, 1);
+    mbar_init(p_full, 128), mbar_init(p_empty, 1);
+    mbar_init(q_full, 1), mbar_init(q_empty, 1);
+    mbar_init(o_full, 2), mbar_init(o_free, 128);  // o_full: the products and the flag of V
+    for (int b = 0; b < kItems; ++b) mbar_init(it_full + b, 1), mbar_init(it_empty + b, 4 + 2);
+    fence_mbar_init();
+  }
+  if (warp == 5 && lane == 0) tma_prefetch_map(&map_q), tma_prefetch_map(&map_k), tma_prefetch_map(&map_v);
+  if (warp == 4) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = warp_uniform(*tmem_slot);
+  const uint32_t tS = tmem + L::kColS, tO = tmem + L::kColO, tP = tmem + L::kColP;
+  grid_inputs_ready();
+  grid_let_next_start();
+
+  // The next item for a role; its slot is given back at once. n: items taken so far.
+  auto take = [&](int n, PackedItem& it) -> bool {
+    const int b = n % kItems;
+    const bool ok = warp_all(mbar_wait(it_full + b, uint32_t(n / kItems) & 1, st));
+    if (!ok) return false;
+    it = items[b];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(it_empty + b);
+    return true;
+  };
+
+  if (warp == 5) {
+    // ------------------------------------------------------------ items and copies
+    for (int s = blockIdx.x * 32 + lane; s < p.S; s += gridDim.x * 32) {
+      int a, b, c, d;
+      if (!packed_sequence(p, s, a, b, c, d)) raise_status(st, kStatusBounds);
+    }
+    __syncwarp();
+    bool ok = true;
+    int n = 0, live = 0, kn = 0, vn = 0;  // items, those with keys, K and V tiles so far
+    auto load = [&](uint64_t* full, uint64_t* empty, int base, const CUtensorMap* map, int& cnt, const PackedItem& it, int j) -> bool {
+      const int s = cnt % S;
+      if (!warp_all(mbar_wait(empty + s, (uint32_t(cnt / S) & 1) ^ 1, st))) return false;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full + s, L::kTile);
+#pragma unroll
+        for (int rg = 0; rg < D / 64; ++rg)
+          tma_load_3d(sbase + base + s * L::kTile + rg * kRegion, map, rg * 64, it.hk, it.k0 + j * 128, smem_u32(full + s));
+      }
+      __syncwarp();
+      ++cnt;
+      return true;
+    };
+    for (long long i = blockIdx.x;; i += gridDim.x) {
+      PackedItem it;
+      bool last = i >= p.items;
+      if (!last && !packed_item(p, wk.by_tq, wk.by_chunk, i, lane, &it)) continue;
+      if (last) it.tiles = -1;
+      const int b = n % kItems;
+      if (!(ok = warp_all(mbar_wait(it_empty + b, (uint32_t(n / kItems) & 1) ^ 1, st)))) break;
+      if (lane == 0) {
+        items[b] = it;
+        mbar_arrive(it_full + b);
+      }
+      __syncwarp();
+      ++n;
+      if (last) break;
+      if (it.tiles == 0) continue;
+      // the first keys do not wait for the queries' place, which the last item's S products still read
+      for (int j = 0; j <= it.tiles && ok; ++j) {
+        if (j < it.tiles && !(ok = load(k_full, k_empty, L::kK, &map_k, kn, it, j))) break;
+        if (j == 0) {
+          if (!(ok = warp_all(mbar_wait(q_empty, (uint32_t(live) & 1) ^ 1, st)))) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(q_full, uint32_t(p.rows * 128 * (D / 64)));
+#pragma unroll
+            for (int rg = 0; rg < D / 64; ++rg)
+              tma_load_3d(sbase + L::kQ + rg * kRegion, &map_q, rg * 64, it.hk * p.g, it.q0, smem_u32(q_full));
+          }
+          __syncwarp();
+          ++live;
+        } else if (!(ok = load(v_full, v_empty, L::kV, &map_v, vn, it, j - 1))) {
+          break;
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok) {
+      if (lane == 0) raise_status(st, kStatusTimeout);
+      settle_copies();  // normally the MMAs have consumed every copy before the CTA exits
+    }
+    __syncwarp();
+  } else if (warp == 4 || warp == 6) {
+    // ------------------------------------------------------------ MMA issuers
+    constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
+    bool ok = true, issued = false;
+    int tile = 0, live = 0;
+    for (int n = 0; ok; ++n) {
+      PackedItem it;
+      if (!(ok = take(n, it))) break;
+      if (it.tiles < 0) break;
+      if (it.tiles == 0) continue;
+      if (warp == 4) {
+        if (!(ok = warp_all(mbar_wait(q_full, uint32_t(live) & 1, st)))) break;
+        const uint32_t qlo = desc_lo_kmajor(sbase + L::kQ);
+        for (int j = 0; j < it.tiles; ++j, ++tile) {
+          const int s = tile % S, b = tile & 1;
+          ok = warp_all(mbar_wait(k_full + s, uint32_t(tile / S) & 1, st) &&
+                        mbar_wait(s_free + b, (uint32_t(tile >> 1) & 1) ^ 1, st));
+          if (!ok) break;
+          tc_fence_after();
+          issued = true;
+          const uint32_t klo = desc_lo_kmajor(sbase + L::kK + s * L::kTile);
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              tc_mma_ss_lo(tS + b * 128, qlo + kstep_kmajor(ks), klo + kstep_kmajor(ks), kIdescQK, ks > 0 ? 1u : 0u);
+            tc_commit(s_full + b);
+            tc_commit(k_empty + s);
+            if (j == it.tiles - 1) tc_commit(q_empty);
+          }
+          __syncwarp();
+        }
+      } else {
+        const int all_see = visible_keys(it, p.causal, 0);
+        bool found = false;
+        for (int j = 0; j < it.tiles; ++j, ++tile) {
+          const int s = tile % S;
+          if (!(ok = warp_all(mbar_wait(v_full + s, uint32_t(tile / S) & 1, st)))) break;
+          if ((j + 1) * 128 > all_see) {
+            found |= settle_v<D>(sbase + L::kV + s * L::kTile, max(0, all_see - j * 128), min(128, it.nkeys - j * 128), lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (j == 0) ok = warp_all(mbar_wait(o_free, (uint32_t(live) & 1) ^ 1, st));
+          if (ok) ok = warp_all(mbar_wait(p_full, uint32_t(tile) & 1, st));
+          if (!ok) break;
+          tc_fence_after();
+          issued = true;
+          const uint32_t vlo = desc_lo_mnmajor(sbase + L::kV + s * L::kTile);
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma_ts_lo(tO, tP + ks * 8, vlo + kstep_mnmajor(ks), kIdescPV, (j > 0 || ks > 0) ? 1u : 0u);
+            tc_commit(p_empty);
+            tc_commit(v_empty + s);
+            if (j == it.tiles - 1) tc_commit(o_full);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        found = __any_sync(0xffffffffu, found);
+        if (lane == 0) {
+          odd[n % kFlags] = found;
+          mbar_arrive(o_full);
+        }
+      }
+      ++live;
+    }
+    if (!ok) {
+      if (lane == 0) raise_status(st, kStatusTimeout);
+      uint64_t* d = drain + (warp == 6 ? 1 : 0);
+      if (issued) {
+        if (elect_one()) tc_commit(d);
+        __syncwarp();
+        mbar_drain(d, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax and the way out
+    const int row = tid;
+    const int t = p.by_group.div(row), hh = row - t * p.g;  // this row's token of the tile and head of the group
+    const uint32_t lane_off = uint32_t(warp * 32) << 16;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int tile = 0, live = 0;
+    for (int n = 0; ok; ++n) {
+      PackedItem it;
+      if (!(ok = take(n, it))) break;
+      if (it.tiles < 0) break;
+      const bool mine = t < it.ntok && row < p.rows;
+      const int lim = mine ? visible_keys(it, p.causal, t) : it.nkeys;
+      const bool busy = warp * 32 < it.ntok * p.g;  // the warp has rows (those of single tokens lie in the first ones)
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < it.tiles; ++j, ++tile) {
+        const int b = tile & 1;
+        if (!(ok = warp_all(mbar_wait(s_full + b, uint32_t(tile >> 1) & 1, st)))) break;
+        tc_fence_after();
+        uint32_t pk[64];
+        bool need = false;
+        float alpha = 1.f;
+        if (busy) {
+          uint32_t r[128];
+          tmem_ld128(tS + lane_off + b * 128, r);
+          tc_fence_before();
+          mbar_arrive(s_free + b);
+          const int nvalid = lim - j * 128;
+          if (__any_sync(0xffffffffu, nvalid < 128)) {  // keys that this row does not see
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= nvalid) r[c] = __float_as_uint(-INFINITY);
+          }
+          float mp[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mp[i] = __uint_as_float(r[i]);
+#pragma unroll
+          for (int c = 8; c < 128; c += 2) mp[(c >> 1) & 7] = fmax3(mp[(c >> 1) & 7], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+          const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
+          const float m_new = fmaxf(m, mx * sl2);
+          need = m_new > m + 8.f;  // the sums are scaled anew only where the maximum grew by more than 2^8
+          const float m_use = need ? m_new : m;
+          alpha = need ? ex2_approx(m - m_new) : 1.f;
+          const float neg_m = m_use == -INFINITY ? 0.f : -m_use;
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), negmx2 = f2_pack(neg_m, neg_m);
+          uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sl2x2, negmx2), x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            ls2[c & 1] = f2_add(ls2[c & 1], f2_pack(p0, p1));
+            pk[c] = pack_bf16x2(p0, p1);
+          }
+          float la, lb;
+          f2_unpack(f2_add(ls2[0], ls2[1]), la, lb);
+          l = l * alpha + (la + lb);
+          m = m_use;
+        } else {
+          tc_fence_before();
+          mbar_arrive(s_free + b);
+        }
+        if (!(ok = warp_all(mbar_wait(p_empty, (uint32_t(tile) & 1) ^ 1, st)))) break;  // the last tile's P V is done
+        if (busy) {
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, need && j > 0)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + lane_off + c * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + lane_off + c * 32, o);
+            }
+          }
+          tmem_st64(tP + lane_off, pk);
+        }
+        tc_fence_before();
+        mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      if (it.tiles > 0) {
+        if (!(ok = warp_all(mbar_wait(o_full, uint32_t(live) & 1, st)))) break;
+        ++live;
+        tc_fence_after();
+      }
+      if (busy) {
+        const int h = it.hk * p.g + hh;
+        const bool cut = p.chunk > 0;
+        const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;  // rows that see nothing give 0
+        // elements of V that are not finite and that only some rows see (left out of the products)
+        const bool extra = it.tiles > 0 && odd[n % kFlags] != 0;
+        const int all_see = visible_keys(it, p.causal, 0);
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(h) * p.os.head + static_cast<long long>(it.q0 + t) * p.os.token);
+        float* prow = cut ? p.part_o + (it.part + row) * D : nullptr;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          float o[32];
+          if (it.tiles > 0) {
+            tmem_ld32(tO + lane_off + c * 32, u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(u[i]) * inv;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (!mine) continue;
+          if (extra) {
+            const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(p.v) + static_cast<long long>(it.hk) * p.vs.head + c * 32;
+            for (int j = all_see; j < lim; ++j) {
+              const __nv_bfloat16* vr = vb + static_cast<long long>(it.k0 + j) * p.vs.token;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float f = __bfloat162float(vr[i]);
+                if (!isfinite(f)) o[i] += f;
+              }
+            }
+          }
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(prow + c * 32 + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 w;
+              w.x = pack_bf16x2(o[i], o[i + 1]);
+              w.y = pack_bf16x2(o[i + 2], o[i + 3]);
+              w.z = pack_bf16x2(o[i + 4], o[i + 5]);
+              w.w = pack_bf16x2(o[i + 6], o[i + 7]);
+              *reinterpret_cast<uint4*>(orow + c * 32 + i) = w;
+            }
+          }
+        }
+        if (mine && cut) p.part_ml[it.part + row] = make_float2(m, l);
+        if (mine && !cut && p.lse != nullptr)
+          p.lse[static_cast<long long>(h) * p.Tq + it.q0 + t] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+      }
+      if (it.tiles > 0) {
+        tc_fence_before();
+        mbar_arrive(o_free);
+      }
+    }
+    if (!ok && lane == 0) raise_status(st, kStatusTimeout);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the chunks of a row: a warp per token and head. With M the largest of the chunks' maxima m_c,
+//   o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
+template <int D, typename T>
+__global__ void __launch_bounds__(256, 4) packed_join_kernel(const PackedParams p, const Walk wk) {
+  grid_inputs_ready();
+  grid_let_next_start();
+  const int lane = threadIdx.x & 31;
+  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int tok = int(w / p.H), h = int(w - static_cast<long long>(tok) * p.H);
+  if (tok >= p.Tq) return;
+  const int s = packed_find(p.q_start, p.S, wk.by_one, 0, tok, lane);
+  int q0, nq, k0, nk;
+  if (s < 0 || !packed_sequence(p, s, q0, nq, k0, nk) || tok < q0 || tok >= q0 + nq) return;
+  const int hk = p.by_group.div(h), hh = h - hk * p.g, i = tok - q0;
+  const int iq = wk.by_tq.div(i), last = min((iq + 1) * p.tq, nq);
+  const int seen = p.causal ? max(0, min(nk, last + nk - nq)) : nk;
+  const int chunks = wk.by_chunk.div(seen + p.chunk - 1), slot = wk.by_chunk.div(k0) + s;
+  const long long row = (i - iq * p.tq) * p.g + hh;
+  auto at = [&](int c) { return ((static_cast<long long>(slot + c) * p.tiles + iq) * p.Hk + hk) * p.rows + row; };
+  constexpr int kE = D / 32;
+  float M = -INFINITY, l = 0.f, o[kE] = {};
+  for (int c0 = 0; c0 < chunks; c0 += 32) {
+    const float2 ml = c0 + lane < chunks ? p.part_ml[at(c0 + lane)] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float Mn = fmaxf(M, top), keep = M == -INFINITY ? 0.f : exp2f(M - Mn);
+    // a chunk without a visible key has sum 0; one of NaN scores has maximum -inf but a sum that is NaN
+    // (and one far below M keeps the smallest weight, so that its infinities and NaN stay)
+    const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : fmaxf(exp2f(ml.x - Mn), FLT_MIN);
+    float sum = ml.y * f;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    l = l * keep + sum;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] *= keep;
+    const int n = min(32, chunks - c0);
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+      const float fc = __shfl_sync(0xffffffffu, f, c);
+      const float* po = p.part_o + at(c0 + c) * D + lane * kE;
+      float v[kE];
+      if constexpr (kE == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(po);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(po);
+        v[0] = x.x, v[1] = x.y;
+      }
+      if (fc != 0.f) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = fmaf(fc, v[e], o[e]);
+      }
+    }
+    M = Mn;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* orow = static_cast<T*>(p.o) + (static_cast<long long>(h) * p.os.head + static_cast<long long>(tok) * p.os.token) + lane * kE;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (kE == 4) *reinterpret_cast<uint2*>(orow) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    else *reinterpret_cast<uint32_t*>(orow) = pack_bf16x2(o[0], o[1]);
+  } else {
+    if constexpr (kE == 4) *reinterpret_cast<float4*>(orow) = make_float4(o[0], o[1], o[2], o[3]);
+    else *reinterpret_cast<float2*>(orow) = make_float2(o[0], o[1]);
+  }
+  if (p.lse != nullptr && lane == 0)
+    p.lse[static_cast<long long>(h) * p.Tq + tok] = l == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) * kLn2 + logf(l);
+}
+
+// Tiled map over a [heads, tokens, d] bf16 view, box = 64 columns x box_heads x box_tokens, 128-byte swizzle.
+bool make_view_map(CUtensorMap* m, const void* base, int heads, int tokens, int d, const PackedStrides& s, int box_heads, int box_tokens) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(tokens)};
+  // the stride of a dimension of one is never used
+  const cuuint64_t strides[2] = {cuuint64_t(heads > 1 ? s.head : d) * 2, cuuint64_t(tokens > 1 ? s.token : d) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+Walk walk_of(const PackedParams& p) { return {Divisor(p.tq), Divisor(p.chunk > 0 ? p.chunk : 1), Divisor(1)}; }
+
+template <int D>
+cudaError_t launch_tc(const PackedParams& p, int num_sms, cudaStream_t s) {
+  CUtensorMap mq, mk, mv;
+  if (!(make_view_map(&mq, p.q, p.H, p.Tq, D, p.qs, p.g, p.tq) && make_view_map(&mk, p.k, p.Hk, p.Tk, D, p.ks, 1, 128) &&
+        make_view_map(&mv, p.v, p.Hk, p.Tk, D, p.vs, 1, 128)))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem<packed_attn_kernel<D>>(Cfg<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int grid = p.items < num_sms ? int(p.items) : num_sms;
+  return launch_overlapped(packed_attn_kernel<D>, dim3(grid), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
+}
+
+}  // namespace
+
+// Tiles and chunks. A tile takes as many tokens as fit in 128 rows (64 on the CUDA cores). Sequences are cut where the
+// tiles alone do not fill the GPU twice over and a sequence has more than a thousand keys on average: into pieces of
+// which every SM gets about eight, of 256 keys at least.
+bool plan_packed(PackedParams* p, bool bf16) {
+  constexpr int kSms = 152;
+  p->g = p->H / p->Hk;
+  p->tq = (bf16 ? 128 : 64) / p->g;
+  p->rows = p->tq * p->g;
+  p->by_group = Divisor(p->g);
+  p->by_heads = Divisor(p->Hk);
+  const long long tiles = (static_cast<long long>(p->max_q) + p->tq - 1) / p->tq;
+  long long slots = static_cast<long long>(p->Tq) / p->tq + p->S;
+  // tiles of all sequences together: not more than the slots, nor than the longest's of each
+  const long long most = p->S * tiles < slots ? p->S * tiles : slots;
+  const long long keys = static_cast<long long>(p->Tk) / p->S;
+  p->chunk = 0;
+  p->tiles = 1;
+  const int piece = bf16 ? 128 : 64;
+  if (keys >= 4 * piece && tiles <= 64 && most * p->Hk < 8 * kSms) {
+    const long long work = most * keys * p->Hk;
+    long long chunk = (work / (8 * kSms) + piece - 1) / piece * piece;
+    if (chunk < 2 * piece) chunk = 2 * piece;
+    if (most * p->Hk < 2 * kSms || tiles == 1) {
+      p->chunk = int(chunk < (1 << 30) ? chunk : (1 << 30));
+      p->tiles = int(tiles);
+      slots = p->Tk / p->chunk + p->S;
+      p->by_tiles = Divisor(p->tiles);
+    }
+  }
+  p->items = slots * p->tiles * p->Hk;
+  if (p->items >= (1ll << 31) - 65536) return false;
+  p->slots = int(slots);
+  p->by_slots = Divisor(p->slots);
+  return true;
+}
+
+size_t packed_workspace_bytes(const PackedParams& p) {
+  if (p.chunk == 0) return 16;
+  return size_t(p.items) * p.rows * (size_t(p.d) * 4 + 8);
+}
+
+cudaError_t packed_attn_tc(const PackedParams& p, int num_sms, cudaStream_t s) {
+  const cudaError_t e = p.d == 128 ? launch_tc<128>(p, num_sms, s) : launch_tc<64>(p, num_sms, s);
+  return e != cudaSuccess || p.chunk == 0 ? e : packed_join(p, true, s);
+}
+
+cudaError_t packed_join(const PackedParams& p, bool bf16, cudaStream_t s) {
+  const long long blocks = (static_cast<long long>(p.Tq) * p.H + 7) / 8;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  auto go = [&](auto kern) { return launch_overlapped(kern, dim3(unsigned(blocks)), 256, 0, s, 0, p, walk_of(p)); };
+  if (bf16) return p.d == 128 ? go(packed_join_kernel<128, __nv_bfloat16>) : go(packed_join_kernel<64, __nv_bfloat16>);
+  return p.d == 128 ? go(packed_join_kernel<128, float>) : go(packed_join_kernel<64, float>);
+}
+
+}  // namespace mcs

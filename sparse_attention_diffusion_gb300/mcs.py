@@ -28,7 +28,8 @@ EXPORTS = ("mcs_workspace_size", "mcs_group_pddp", "mcs_dense_attn", "mcs_anchor
            "mcs_cache_ring_acquire", "mcs_cache_ring_release", "mcs_cache_ring_destroy",
            "mcs_selftest_wait_timeout", "mcs_pddp_dirs_size", "mcs_group_pddp_warm", "mcs_selftest_ex2_rate",
            "mcs_rope_table_size", "mcs_rope_table", "mcs_rope_apply", "mcs_qk_norm_rope",
-           "mcs_qk_norm_rope_bwd_workspace_size", "mcs_qk_norm_rope_bwd", "mcs_linear", "mcs_linear_plan")
+           "mcs_qk_norm_rope_bwd_workspace_size", "mcs_qk_norm_rope_bwd", "mcs_linear", "mcs_linear_plan",
+           "mcs_packed_attn_workspace_size", "mcs_packed_attn")
 
 
 class McsError(RuntimeError):
@@ -61,6 +62,12 @@ class mcs_linear_desc(ctypes.Structure):
 
 class mcs_linear_choice(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("tile", ctypes.c_int), ("slices", ctypes.c_int), ("accumulators", ctypes.c_int)]
+
+
+class mcs_packed_desc(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int), ("Tq", ctypes.c_int), ("Tk", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("causal", ctypes.c_int), ("max_q", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 ROPE_STYLES = {"interleaved": 0, "half": 1}
@@ -120,6 +127,8 @@ def load(build_if_missing: bool = False):
         "mcs_qk_norm_rope_bwd_workspace_size": (Z, [D]),
         "mcs_qk_norm_rope_bwd": (I, [D, R, P, P, P, P, V, P, P, F, P, P, P, P, P, P, P, P, P, Z, S]),
         "mcs_linear": (I, [ctypes.POINTER(mcs_linear_desc), P, P, P, P, P, P, S]),
+        "mcs_packed_attn_workspace_size": (Z, [ctypes.POINTER(mcs_packed_desc)]),
+        "mcs_packed_attn": (I, [ctypes.POINTER(mcs_packed_desc), P, V, P, V, P, V, P, P, P, V, P, P, Z, S]),
         "mcs_linear_plan": (I, [ctypes.POINTER(mcs_linear_desc), I, I, ctypes.POINTER(mcs_linear_choice)]),
     }
     for name, (res, args) in sig.items():
@@ -593,6 +602,49 @@ def mcs_linear_plan(desc, residual=False, num_sms=152):
     c = mcs_linear_choice()
     _check("mcs_linear_plan", load().mcs_linear_plan(desc, 1 if residual else 0, int(num_sms), ctypes.byref(c)))
     return LINEAR_KERNELS[c.kernel], c.tile, c.slices, c.accumulators
+
+
+# ---------------------------------------------------------------- requests of different lengths
+def packed_desc(S, Tq, Tk, H, Hk, d, dtype, causal=True, max_q=0, scale=0.0) -> mcs_packed_desc:
+    """S sequences laid one behind the other: queries [H, Tq, d], keys and values [Hk, Tk, d], H a multiple of Hk; no
+    sequence has more than max_q queries (0: Tq)."""
+    dt = MCS_BF16 if dtype in (torch.bfloat16, "bf16", MCS_BF16) else MCS_F32
+    return mcs_packed_desc(int(S), int(Tq), int(Tk), int(H), int(Hk), int(d), dt, 1 if causal else 0, int(max_q), float(scale))
+
+
+def packed_attn_workspace(desc, device="cuda") -> torch.Tensor:
+    n = int(load().mcs_packed_attn_workspace_size(ctypes.byref(desc)))
+    if n == 0:
+        raise McsError("mcs_packed_attn_workspace_size", 2)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _packed_view(name, t, shape, dtype):
+    """Address and strides of a [heads, tokens, d] view with contiguous d."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    sh, sn, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {sd}")
+    return t.data_ptr(), mcs_strides(0, sh, sn)
+
+
+def mcs_packed_attn(desc, q, k, v, q_start, k_start, o, lse, ws, stream=None):
+    """Attention within each of desc.S packed sequences: q, o [H, Tq, d] and k, v [Hk, Tk, d] views with contiguous d
+    (token-major tensors are passed transposed), q_start, k_start int32 [S + 1] (the same tensor where every sequence
+    attends over its own tokens), lse fp32 [H, Tq] or None."""
+    dt, f = _io_dtype(desc), (desc.S + 1,)
+    rows, keys = (desc.H, desc.Tq, desc.d), (desc.Hk, desc.Tk, desc.d)
+    qp, qs = _packed_view("q", q, rows, dt)
+    kp, ks = _packed_view("k", k, keys, dt)
+    vp, vs = _packed_view("v", v, keys, dt)
+    op, os_ = _packed_view("o", o, rows, dt)
+    qa, ka = _exactly("q_start", q_start, f, torch.int32), _exactly("k_start", k_start, f, torch.int32)
+    lp = _exactly("lse", lse, (desc.H, desc.Tq), torch.float32)
+    wsp = _address("ws", ws)
+    _on_device(q, k, v, q_start, k_start, o, lse, ws)
+    _check("mcs_packed_attn", load().mcs_packed_attn(desc, qp, qs, kp, ks, vp, vs, qa, ka, op, os_, lp, wsp,
+                                                     ws.numel() * ws.element_size(), _raw_stream(stream)))
 
 
 # ---------------------------------------------------------------- convenience: buffers for one layer
