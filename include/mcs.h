@@ -378,7 +378,7 @@ mcs_status mcs_linear_plan(const mcs_linear_desc *desc, int with_residual, int n
 
 /* ---------------------------------------------------------------------------
  * Requests of different lengths in one batch: attention over packed sequences, and
- * (below mcs_linear) projections with an adapter for each request.
+ * projections with an adapter for each request.
  */
 
 /* S sequences laid one behind the other: queries [H, Tq, d], keys and values
@@ -420,6 +420,36 @@ mcs_status mcs_packed_attn(const mcs_packed_desc *desc, const void *q, const mcs
                            const mcs_strides *ks, const void *v, const mcs_strides *vs, const int32_t *q_start,
                            const int32_t *k_start, void *o, const mcs_strides *os, float *lse, void *ws,
                            size_t ws_bytes, mcs_stream stream);
+
+/* mcs_linear with a low-rank adapter for each segment of rows, several requests' adapters in one
+ * call: y = residual + gate_b * act(x w^T + bias + scale[a] * (x down_a^T) up_a^T).
+ * Rows count through the batches (row b * N + n); segment s holds rows start[s] ..
+ * start[s+1] - 1 and takes adapter a = which[s], none where which[s] is negative; rows in no
+ * segment take none. A segment may span batches and adapters may serve several segments.
+ * down: [count, rank, in], up: [count, out, rank], I/O dtype (smaller adapters of a set
+ * are padded with zeros); scale: fp32 [count]; start: int32 [segments + 1], rising from 0 or
+ * more to B * N at most, which: int32 [segments], on the device; all 16-byte aligned. Other
+ * arguments, layouts, limits and aliases as mcs_linear; y and ws overlap no input. Supported:
+ * rank a multiple of 8 (BF16) or 4 (F32), at most 256; count, segments <= 2^20. Bounds that
+ * fall or leave the rows (y is then undefined) and which[s] >= count (none is taken) are flagged
+ * MCS_ERR_DEVICE_BOUNDS.
+ * The inner sums h = scale[a] * x down_a^T are fp32 and kept as two bf16 parts (BF16: to 2^-17, the
+ * tensor core's truncation moves a sum by less than in / 16 * 5.25 * 2^-23 of sum |x down|) or
+ * as they are (F32). BF16: an adapter whose `up` holds an infinity or a NaN makes all outputs of its
+ * own rows NaN; F32: what the sums give. No row depends on another segment's adapter.
+ * ws: at least mcs_linear_adapters_workspace_size(desc, adapters) bytes (0 for an invalid
+ * description; host only); its contents on entry are ignored; calls that may run at the
+ * same time need one each. Equal calls give equal bits. */
+typedef struct {
+  int count;       /* adapters */
+  int rank;
+  int segments;
+} mcs_adapters;
+size_t mcs_linear_adapters_workspace_size(const mcs_linear_desc *desc, const mcs_adapters *adapters);
+mcs_status mcs_linear_adapters(const mcs_linear_desc *desc, const mcs_adapters *adapters, const void *x, const void *w,
+                               const void *bias, const void *gate, const void *residual, const void *down,
+                               const void *up, const float *scale, const int32_t *start, const int32_t *which, void *y,
+                               void *ws, size_t ws_bytes, mcs_stream stream);
 
 /* Synchronises `stream`, then reports (and clears) the device-side flags raised
  * since the last call: MCS_ERR_DEVICE_BOUNDS, MCS_ERR_DEVICE_TIMEOUT, or a

@@ -92,6 +92,20 @@ bool view(const mcs_desc* desc, const mcs_strides* s, bool written, mcs::ViewStr
   return true;
 }
 
+// From a view's first element to its last.
+Range range(const mcs_desc* d, const void* p, const mcs::ViewStrides& v) {
+  const long long n = (d->B - 1) * v.b + (d->H - 1) * v.h + (d->N - 1) * v.n + d->d;
+  return {static_cast<const char*>(p), n * (d->dtype == MCS_BF16 ? 2 : 4)};
+}
+bool contiguous(const mcs_desc* d, const mcs::ViewStrides& v) {
+  return (d->B == 1 || v.b == static_cast<long long>(d->H) * d->N * d->d) &&
+         (d->H == 1 || v.h == static_cast<long long>(d->N) * d->d) && (d->N == 1 || v.n == d->d);
+}
+
+}  // namespace
+
+namespace mcs {
+
 // The checks of a product's description; fills its sizes.
 mcs_status check_linear(const mcs_linear_desc* desc, mcs::LinearParams* p) {
   if (desc == nullptr) return MCS_ERR_INVALID_ARG;
@@ -114,17 +128,7 @@ mcs_status check_linear(const mcs_linear_desc* desc, mcs::LinearParams* p) {
   return MCS_OK;
 }
 
-// From a view's first element to its last.
-Range range(const mcs_desc* d, const void* p, const mcs::ViewStrides& v) {
-  const long long n = (d->B - 1) * v.b + (d->H - 1) * v.h + (d->N - 1) * v.n + d->d;
-  return {static_cast<const char*>(p), n * (d->dtype == MCS_BF16 ? 2 : 4)};
-}
-bool contiguous(const mcs_desc* d, const mcs::ViewStrides& v) {
-  return (d->B == 1 || v.b == static_cast<long long>(d->H) * d->N * d->d) &&
-         (d->H == 1 || v.h == static_cast<long long>(d->N) * d->d) && (d->N == 1 || v.n == d->d);
-}
-
-}  // namespace
+}  // namespace mcs
 
 extern "C" {
 
@@ -267,7 +271,7 @@ mcs_status mcs_qk_norm_rope_bwd(const mcs_desc* desc, const mcs_rope* rope, cons
 mcs_status mcs_linear(const mcs_linear_desc* desc, const void* x, const void* w, const void* bias, const void* gate,
                       const void* residual, void* y, mcs_stream stream) {
   mcs::LinearParams p{};
-  mcs_status st = check_linear(desc, &p);
+  mcs_status st = mcs::check_linear(desc, &p);
   if (st != MCS_OK) return st;
   if (!aligned16(x) || !aligned16(w) || !aligned16(y)) return MCS_ERR_INVALID_ARG;
   if (!aligned16_or_null(bias) || !aligned16_or_null(gate) || !aligned16_or_null(residual)) return MCS_ERR_INVALID_ARG;
@@ -292,7 +296,7 @@ mcs_status mcs_linear(const mcs_linear_desc* desc, const void* x, const void* w,
 
 mcs_status mcs_linear_plan(const mcs_linear_desc* desc, int with_residual, int num_sms, mcs_linear_choice* choice) {
   mcs::LinearParams p{};
-  const mcs_status st = check_linear(desc, &p);
+  const mcs_status st = mcs::check_linear(desc, &p);
   if (st != MCS_OK) return st;
   if (num_sms < 8 || num_sms > 1024 || choice == nullptr) return MCS_ERR_INVALID_ARG;
   p.residual = with_residual ? choice : nullptr;  // only whether there is one

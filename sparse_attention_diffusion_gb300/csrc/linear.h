@@ -25,6 +25,7 @@ struct LinearParams {
   const void* bias;      // [O] or null
   const void* gate;      // [B, O] or null
   const void* residual;  // [M, O] or null
+  const float* add;      // [M, O] added before the activation, or null (fp32 only)
   void* y;               // [M, O]
   int B, N, M;           // M = B * N rows
   int K, O;

@@ -42,6 +42,7 @@ __device__ __forceinline__ void activate(float (&v)[n]) {
 template <int kAct, typename T>
 __device__ __forceinline__ void finish_one(const LinearParams& p, int m, int o, float acc) {
   if (p.bias) acc += to_f32(static_cast<const T*>(p.bias)[o]);
+  if (sizeof(T) == 4 && p.add) acc += p.add[size_t(m) * p.O + o];
   float v[1] = {acc};
   activate<kAct, sizeof(T) == 4>(v);
   acc = v[0];
@@ -101,6 +102,10 @@ __device__ __forceinline__ void finish_row4(const LinearParams& p, int m, int o,
   const size_t at = size_t(m) * p.O + o;
   if (p.bias) {
     const float4 t = at4(p.bias, o);
+    v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
+  }
+  if (p.add) {
+    const float4 t = at4(p.add, at);
     v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
   }
   activate<kAct, true>(v);

@@ -29,7 +29,8 @@ EXPORTS = ("mcs_workspace_size", "mcs_group_pddp", "mcs_dense_attn", "mcs_anchor
            "mcs_selftest_wait_timeout", "mcs_pddp_dirs_size", "mcs_group_pddp_warm", "mcs_selftest_ex2_rate",
            "mcs_rope_table_size", "mcs_rope_table", "mcs_rope_apply", "mcs_qk_norm_rope",
            "mcs_qk_norm_rope_bwd_workspace_size", "mcs_qk_norm_rope_bwd", "mcs_linear", "mcs_linear_plan",
-           "mcs_packed_attn_workspace_size", "mcs_packed_attn")
+           "mcs_packed_attn_workspace_size", "mcs_packed_attn", "mcs_linear_adapters_workspace_size",
+           "mcs_linear_adapters")
 
 
 class McsError(RuntimeError):
@@ -68,6 +69,10 @@ class mcs_packed_desc(ctypes.Structure):
     _fields_ = [("S", ctypes.c_int), ("Tq", ctypes.c_int), ("Tk", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int),
                 ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("causal", ctypes.c_int), ("max_q", ctypes.c_int),
                 ("scale", ctypes.c_float)]
+
+
+class mcs_adapters(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int), ("rank", ctypes.c_int), ("segments", ctypes.c_int)]
 
 
 ROPE_STYLES = {"interleaved": 0, "half": 1}
@@ -127,6 +132,8 @@ def load(build_if_missing: bool = False):
         "mcs_qk_norm_rope_bwd_workspace_size": (Z, [D]),
         "mcs_qk_norm_rope_bwd": (I, [D, R, P, P, P, P, V, P, P, F, P, P, P, P, P, P, P, P, P, Z, S]),
         "mcs_linear": (I, [ctypes.POINTER(mcs_linear_desc), P, P, P, P, P, P, S]),
+        "mcs_linear_adapters_workspace_size": (Z, [ctypes.POINTER(mcs_linear_desc), ctypes.POINTER(mcs_adapters)]),
+        "mcs_linear_adapters": (I, [ctypes.POINTER(mcs_linear_desc), ctypes.POINTER(mcs_adapters)] + [P] * 12 + [Z, S]),
         "mcs_packed_attn_workspace_size": (Z, [ctypes.POINTER(mcs_packed_desc)]),
         "mcs_packed_attn": (I, [ctypes.POINTER(mcs_packed_desc), P, V, P, V, P, V, P, P, P, V, P, P, Z, S]),
         "mcs_linear_plan": (I, [ctypes.POINTER(mcs_linear_desc), I, I, ctypes.POINTER(mcs_linear_choice)]),
@@ -645,6 +652,35 @@ def mcs_packed_attn(desc, q, k, v, q_start, k_start, o, lse, ws, stream=None):
     _on_device(q, k, v, q_start, k_start, o, lse, ws)
     _check("mcs_packed_attn", load().mcs_packed_attn(desc, qp, qs, kp, ks, vp, vs, qa, ka, op, os_, lp, wsp,
                                                      ws.numel() * ws.element_size(), _raw_stream(stream)))
+
+
+def adapters_desc(count, rank, segments) -> mcs_adapters:
+    """A set of `count` low-rank adapters of one rank, for the rows of `segments` segments."""
+    return mcs_adapters(int(count), int(rank), int(segments))
+
+
+def linear_adapters_workspace(desc, adapters, device="cuda") -> torch.Tensor:
+    n = int(load().mcs_linear_adapters_workspace_size(ctypes.byref(desc), ctypes.byref(adapters)))
+    if n == 0:
+        raise McsError("mcs_linear_adapters_workspace_size", 2)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mcs_linear_adapters(desc, adapters, x, w, bias, gate, residual, down, up, scale, start, which, y, ws, stream=None):
+    """mcs_linear plus scale[a] (x down_a^T) up_a^T before the activation, a = which[s] for the rows start[s] ..
+    start[s + 1] - 1 (counted through the batches; negative: none). down [count, rank, in], up [count, out, rank],
+    scale fp32 [count], start int32 [segments + 1], which int32 [segments]."""
+    B, N, I, O, h = desc.B, desc.N, desc.in_features, desc.out_features, desc.heads
+    n, R, S = adapters.count, adapters.rank, adapters.segments
+    dt, rows = _io_dtype(desc), (B, N, O)
+    xp = _exactly("x", x, (B, h, N, I // h) if h > 0 else (B, N, I), dt)
+    wp, bp, gp = _exactly("w", w, (O, I), dt), _exactly("bias", bias, (O,), dt), _exactly("gate", gate, (B, O), dt)
+    rp, yp = _exactly("residual", residual, rows, dt), _exactly("y", y, rows, dt)
+    dp, up_, sp = _exactly("down", down, (n, R, I), dt), _exactly("up", up, (n, O, R), dt), _exactly("scale", scale, (n,), torch.float32)
+    st, wh, wsp = _exactly("start", start, (S + 1,), torch.int32), _exactly("which", which, (S,), torch.int32), _address("ws", ws)
+    _on_device(x, w, bias, gate, residual, down, up, scale, start, which, y, ws)
+    _check("mcs_linear_adapters", load().mcs_linear_adapters(desc, adapters, xp, wp, bp, gp, rp, dp, up_, sp, st, wh, yp, wsp,
+                                                             ws.numel() * ws.element_size(), _raw_stream(stream)))
 
 
 # ---------------------------------------------------------------- convenience: buffers for one layer
