@@ -33,6 +33,21 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// allow_smem for a kernel that moves registers between its warps, which must have been compiled with as many as
+// it counts on.
+template <auto kKern>
+cudaError_t allow_smem_and_regs(int bytes, int regs) {
+  static std::atomic<bool> checked{false};
+  if (!checked.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa{};
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kKern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < regs) return cudaErrorInvalidConfiguration;
+    checked.store(true, std::memory_order_relaxed);
+  }
+  return allow_smem<kKern>(bytes);
+}
+
 // cluster: CTAs of a cluster along x (0: the kernel's own attribute, or none).
 template <typename... Params, typename... Args>
 cudaError_t launch_overlapped(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, unsigned cluster,

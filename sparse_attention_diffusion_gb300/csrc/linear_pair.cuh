@@ -534,20 +534,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// allow_smem for a kernel that moves registers between its warps, which must have been compiled with as many as
-// it counts on.
-template <auto kKern>
-cudaError_t allow_long() {
-  static std::atomic<bool> checked{false};
-  if (!checked.load(std::memory_order_relaxed)) {
-    cudaFuncAttributes fa{};
-    const cudaError_t e = cudaFuncGetAttributes(&fa, kKern);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-    checked.store(true, std::memory_order_relaxed);
-  }
-  return allow_smem<kKern>(kSmemAlloc);
-}
 template <int kAct, bool kAdapt>
 cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& my, const CUtensorMap& mr,
                        const AdapterArgs<kAdapt>& ad, const LinearParams& p, const Tiling& t, int pairs, cudaStream_t s) {
@@ -558,10 +544,10 @@ cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUten
     return start(linear_pair_kernel<kAct, 0, false, kAdapt>, allow_smem<linear_pair_kernel<kAct, 0, false, kAdapt>>(kSmemAlloc));
   const bool one = t.total <= pairs;
   if (t.bn <= 192)
-    return one ? start(linear_pair_kernel<kAct, 3, true, kAdapt>, allow_long<linear_pair_kernel<kAct, 3, true, kAdapt>>())
-               : start(linear_pair_kernel<kAct, 3, false, kAdapt>, allow_long<linear_pair_kernel<kAct, 3, false, kAdapt>>());
-  return one ? start(linear_pair_kernel<kAct, 4, true, kAdapt>, allow_long<linear_pair_kernel<kAct, 4, true, kAdapt>>())
-             : start(linear_pair_kernel<kAct, 4, false, kAdapt>, allow_long<linear_pair_kernel<kAct, 4, false, kAdapt>>());
+    return one ? start(linear_pair_kernel<kAct, 3, true, kAdapt>, allow_smem_and_regs<linear_pair_kernel<kAct, 3, true, kAdapt>>(kSmemAlloc, kLaunchRegs))
+               : start(linear_pair_kernel<kAct, 3, false, kAdapt>, allow_smem_and_regs<linear_pair_kernel<kAct, 3, false, kAdapt>>(kSmemAlloc, kLaunchRegs));
+  return one ? start(linear_pair_kernel<kAct, 4, true, kAdapt>, allow_smem_and_regs<linear_pair_kernel<kAct, 4, true, kAdapt>>(kSmemAlloc, kLaunchRegs))
+             : start(linear_pair_kernel<kAct, 4, false, kAdapt>, allow_smem_and_regs<linear_pair_kernel<kAct, 4, false, kAdapt>>(kSmemAlloc, kLaunchRegs));
 }
 
 // adapters: null without adapters.

@@ -32,7 +32,8 @@ struct PackedParams {
   int S, Tq, Tk, H, Hk, g, d;
   int causal, max_q;
   float scale_log2;       // scale * log2(e)
-  int tq, rows;           // tokens and rows (tq * g) of a tile
+  int tq, rows;           // tokens and rows (tq * g) of a tile (of two tiles: pair)
+  int pair;               // bf16, two tiles of 128 rows an item
   int chunk;              // keys of a piece of a sequence, 0: sequences are not cut
   int tiles;              // with chunk > 0: query tiles of the longest sequence
   long long items;        // slots of all heads (and tiles)
@@ -47,6 +48,7 @@ struct PackedParams {
 bool plan_packed(PackedParams* p, bool bf16);
 size_t packed_workspace_bytes(const PackedParams& p);
 cudaError_t packed_attn_tc(const PackedParams& p, int num_sms, cudaStream_t s);
+cudaError_t packed_attn_pair(const PackedParams& p, int num_sms, cudaStream_t s);
 cudaError_t packed_attn_f32(const PackedParams& p, cudaStream_t s);
 cudaError_t packed_join(const PackedParams& p, bool bf16, cudaStream_t s);
 

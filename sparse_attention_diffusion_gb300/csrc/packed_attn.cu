@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "launch.cuh"
 #include "packed.h"
+#include "packed_tc.cuh"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 #include "tma.cuh"
@@ -54,48 +55,10 @@ struct Cfg {
 };
 static_assert(Cfg<128>::kAlloc <= 227 * 1024 && Cfg<64>::kAlloc <= 227 * 1024, "shared memory");
 
-struct Walk {
-  Divisor by_tq, by_chunk, by_one;
-};
-
-__device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
-  return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
-}
-// Both halves, what is not finite as 0.
-__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
-  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-  return w;
-}
-
-// Rows some .. none - 1 of a V tile, which some tokens do not see, with what is not finite as 0, and rows from none
-// on, which nobody sees, as 0. Whether there was such an element. One warp, 16 bytes a lane.
-template <int D>
-__device__ __forceinline__ bool settle_v(uint32_t v, int some, int none, int lane) {
-  constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes;
-  const int ch = lane % kRowLanes;
-  bool found = false;
-#pragma unroll 4
-  for (int r = some + lane / kRowLanes; r < none; r += kRows) {
-    const uint32_t at = v + sw128_off(r, ch);
-    uint4 w;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
-    if (!(finite_bf16x2(w.x) && finite_bf16x2(w.y) && finite_bf16x2(w.z) && finite_bf16x2(w.w))) {
-      found = true;
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(finite_part(w.x)), "r"(finite_part(w.y)),
-                   "r"(finite_part(w.z)), "r"(finite_part(w.w))
-                   : "memory");
-    }
-  }
-  for (int r = none + lane / kRowLanes; r < 128; r += kRows)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + sw128_off(r, ch)), "r"(0) : "memory");
-  return found;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const PackedParams p, const Walk wk) {
+                       const __grid_constant__ CUtensorMap map_v, const PackedParams p, const PackedWalk wk) {
   using L = Cfg<D>;
   constexpr int S = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -255,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = tile % S;
           if (!(ok = warp_all(mbar_wait(v_full + s, uint32_t(tile / S) & 1, st)))) break;
           if ((j + 1) * 128 > all_see) {
-            found |= settle_v<D>(sbase + L::kV + s * L::kTile, max(0, all_see - j * 128), min(128, it.nkeys - j * 128), lane);
+            found |= settle_v<D>(sbase + L::kV + s * L::kTile, max(0, all_see - j * 128), min(128, it.nkeys - j * 128), 0, lane);
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -318,16 +281,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool need = false;
         float alpha = 1.f;
         if (busy) {
+          const int nvalid = lim - j * 128;
+          if (__any_sync(0xffffffffu, nvalid < 128)) mask_scores(tS + lane_off + b * 128, nvalid);
           uint32_t r[128];
           tmem_ld128(tS + lane_off + b * 128, r);
           tc_fence_before();
           mbar_arrive(s_free + b);
-          const int nvalid = lim - j * 128;
-          if (__any_sync(0xffffffffu, nvalid < 128)) {  // keys that this row does not see
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= nvalid) r[c] = __float_as_uint(-INFINITY);
-          }
           float mp[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) mp[i] = __uint_as_float(r[i]);
@@ -361,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (busy) {
           tc_fence_after();
           if (__any_sync(0xffffffffu, need && j > 0)) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               tmem_ld32(tO + lane_off + c * 32, o);
@@ -390,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_see = visible_keys(it, p.causal, 0);
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(h) * p.os.head + static_cast<long long>(it.q0 + t) * p.os.token);
         float* prow = cut ? p.part_o + (it.part + row) * D : nullptr;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t u[32];
           float o[32];
@@ -452,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the chunks of a row: a warp per token and head. With M the largest of the chunks' maxima m_c,
 //   o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
 template <int D, typename T>
-__global__ void __launch_bounds__(256, 4) packed_join_kernel(const PackedParams p, const Walk wk) {
+__global__ void __launch_bounds__(256, 4) packed_join_kernel(const PackedParams p, const PackedWalk wk) {
   grid_inputs_ready();
   grid_let_next_start();
   const int lane = threadIdx.x & 31;
@@ -520,21 +479,6 @@ __global__ void __launch_bounds__(256, 4) packed_join_kernel(const PackedParams 
     p.lse[static_cast<long long>(h) * p.Tq + tok] = l == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) * kLn2 + logf(l);
 }
 
-// Tiled map over a [heads, tokens, d] bf16 view, box = 64 columns x box_heads x box_tokens, 128-byte swizzle.
-bool make_view_map(CUtensorMap* m, const void* base, int heads, int tokens, int d, const PackedStrides& s, int box_heads, int box_tokens) {
-  auto enc = tensor_map_encoder();
-  if (enc == nullptr) return false;
-  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(tokens)};
-  // the stride of a dimension of one is never used
-  const cuuint64_t strides[2] = {cuuint64_t(heads > 1 ? s.head : d) * 2, cuuint64_t(tokens > 1 ? s.token : d) * 2};
-  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-Walk walk_of(const PackedParams& p) { return {Divisor(p.tq), Divisor(p.chunk > 0 ? p.chunk : 1), Divisor(1)}; }
-
 template <int D>
 cudaError_t launch_tc(const PackedParams& p, int num_sms, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
@@ -551,12 +495,11 @@ cudaError_t launch_tc(const PackedParams& p, int num_sms, cudaStream_t s) {
 
 // Tiles and chunks. A tile takes as many tokens as fit in 128 rows (64 on the CUDA cores). Sequences are cut where the
 // tiles alone do not fill the GPU twice over and a sequence has more than a thousand keys on average: into pieces of
-// which every SM gets about eight, of 256 keys at least.
+// which every SM gets about eight, of 256 keys at least. Whole sequences of more than one tile go two tiles at a time.
 bool plan_packed(PackedParams* p, bool bf16) {
   constexpr int kSms = 152;
   p->g = p->H / p->Hk;
   p->tq = (bf16 ? 128 : 64) / p->g;
-  p->rows = p->tq * p->g;
   p->by_group = Divisor(p->g);
   p->by_heads = Divisor(p->Hk);
   const long long tiles = (static_cast<long long>(p->max_q) + p->tq - 1) / p->tq;
@@ -578,6 +521,12 @@ bool plan_packed(PackedParams* p, bool bf16) {
       p->by_tiles = Divisor(p->tiles);
     }
   }
+  p->pair = bf16 && p->chunk == 0 && p->max_q > p->tq;
+  if (p->pair) {
+    p->tq *= 2;
+    slots = static_cast<long long>(p->Tq) / p->tq + p->S;
+  }
+  p->rows = p->tq * p->g;
   p->items = slots * p->tiles * p->Hk;
   if (p->items >= (1ll << 31) - 65536) return false;
   p->slots = int(slots);
@@ -591,6 +540,7 @@ size_t packed_workspace_bytes(const PackedParams& p) {
 }
 
 cudaError_t packed_attn_tc(const PackedParams& p, int num_sms, cudaStream_t s) {
+  if (p.pair) return packed_attn_pair(p, num_sms, s);
   const cudaError_t e = p.d == 128 ? launch_tc<128>(p, num_sms, s) : launch_tc<64>(p, num_sms, s);
   return e != cudaSuccess || p.chunk == 0 ? e : packed_join(p, true, s);
 }

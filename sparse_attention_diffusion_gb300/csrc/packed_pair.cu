@@ -1,0 +1,516 @@
+// Softmax attention over packed sequences, bf16, two tiles of 128 query rows at a time: prompts of more than one tile,
+// whose keys are not cut. Formula, items, masks and what lies in masked places as in packed_attn.cu.
+//
+// One tile alone leaves the tensor core idle while its softmax runs, and the other way round: 1,850 clocks a tile of 128 x
+// 128 scores of which the products take 1,024. Here two tiles, A and B, share every K and V tile and take turns: while
+// A's softmax runs, B's P V and next S do. A persistent grid, one CTA per SM, 512 threads:
+//   warps 0-3, 4-7  softmax of A and of B, a thread per row
+//   warps 8-11      the rows' way out, of A and then of B, while the softmax is at the next item
+//   warp 12         finds the items and loads by TMA: the queries of A and of B, and one ring of K_0, V_0, K_1, V_1, ...
+//   warp 13         the products: S_0 of both; then for every tile P_j V_j and S_{j+1} of A, the same of B. In turn from
+//                   one warp: A and B issued by a warp each fell into step, both softmaxes and then both products
+//                   (3,200 clocks a pair of tiles at d = 128)
+//   warps 14, 15    make V tiles that hold masked keys harmless, half of the rows each, and let the products go
+// The product warp waits on one barrier a step: a wait that is satisfied already takes it 200 clocks beside eight
+// softmax warps, and about as much is hidden by the products that are still queued. So warps 14 and 15 look after everything
+// else that a step needs (keys, values, a free O) and arrive together with the softmax's threads.
+// Tensor memory: S_A, S_B, O_A, O_B of 128 columns each, P_j written over S_j (a row per lane, so a thread overwrites only
+// what it has read); the products of one warp run in order, so S_{j+1} cannot meet P_j.
+// A sees fewer keys than B under a causal mask and leaves its last tiles out. Softmax warps take the registers that the
+// others hand over (128 at launch; 184, 88 on the way out, 56).
+#include "attn_common.cuh"
+#include "common.cuh"
+#include "launch.cuh"
+#include "packed.h"
+#include "packed_tc.cuh"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+#include "tma.cuh"
+
+namespace mcs {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kLaunchRegs = 128, kControlRegs = 56, kOutRegs = 88, kSoftmaxRegs = 184;
+static_assert(128 * kControlRegs + 128 * kOutRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "an increase would wait forever");
+constexpr int kItems = 4;   // items found ahead
+constexpr int kFlags = 8;   // items whose V flags are kept (warps 14, 15 are at most kItems ahead of the way out)
+constexpr int kPatch = 32 * 128;  // a warp's rows x 128 bytes on their way out
+
+template <int D>
+struct Cfg {
+  static constexpr int kStages = (D == 128) ? 4 : 8;  // K and V tiles
+  static constexpr int kTile = (D / 64) * kRegion;
+  static constexpr int kQ = 0;                        // [2]
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kOut = kRing + kStages * kTile;
+  static constexpr int kStats = kOut + 4 * kPatch;    // (maximum, sum) of A's and B's rows
+  static constexpr int kBar = kStats + 2 * 128 * 8;
+  static constexpr int kNumBars = 2 * kStages + 2 * 7 + 2 * kItems + 1;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kItem = (kMisc + 16 + kFlags * 8 + 15) / 16 * 16;
+  static constexpr int kBytes = kItem + kItems * int(sizeof(PackedItem));
+  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr uint32_t kColS = 0, kColO = 256;  // of A; B's lie 128 behind
+};
+static_assert(Cfg<128>::kAlloc <= 227 * 1024 && Cfg<64>::kAlloc <= 227 * 1024, "shared memory");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const PackedParams p, const PackedWalk wk) {
+  using L = Cfg<D>;
+  constexpr int R = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);  // K or V tile landed
+  uint64_t* empty = full + R;         // its products of A and of B are done
+  uint64_t* q_full = empty + R;       // [2] and so on: of A and of B
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_go = q_empty + 2;       // queries and first keys are there
+  uint64_t* s_full = s_go + 2;
+  uint64_t* p_full = s_full + 2;      // P written (128 threads), and all else that P V and the next S need (warps 14, 15)
+  uint64_t* o_full = p_full + 2;
+  uint64_t* o_free = o_full + 2;
+  uint64_t* it_full = o_free + 2;     // [kItems]
+  uint64_t* it_empty = it_full + kItems;
+  uint64_t* drain = it_empty + kItems;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile uint32_t* odd = tmem_slot + 4;  // [kFlags][2] the item's V held something that is not finite and not seen by all
+  float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
+  PackedItem* items = reinterpret_cast<PackedItem*>(smem + L::kItem);
+
+  const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+  uint32_t* st = p.status;
+  if (tid == 0) {
+    for (int s = 0; s < R; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(q_full + c, 1), mbar_init(q_empty + c, 1), mbar_init(s_go + c, 2), mbar_init(s_full + c, 1);
+      mbar_init(p_full + c, 130), mbar_init(o_full + c, 130), mbar_init(o_free + c, 128);
+    }
+    mbar_init(drain, 1);
+    for (int b = 0; b < kItems; ++b) mbar_init(it_full + b, 1), mbar_init(it_empty + b, 8 + 4 + 3);
+    fence_mbar_init();
+  }
+  if (warp == 12 && lane == 0) tma_prefetch_map(&map_q), tma_prefetch_map(&map_k), tma_prefetch_map(&map_v);
+  if (warp == 13) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = warp_uniform(*tmem_slot);
+  grid_inputs_ready();
+  grid_let_next_start();
+  const int half = p.tq / 2;  // tokens of a tile
+
+  // The next item for a role; its slot is given back at once. n: items taken so far.
+  auto take = [&](int n, PackedItem& it) -> bool {
+    const int b = n % kItems;
+    if (!warp_all(mbar_wait(it_full + b, uint32_t(n / kItems) & 1, st))) return false;
+    it = items[b];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(it_empty + b);
+    return true;
+  };
+  // Key tiles of A (c = 0) or B; 0 where it has no tokens or they see nothing.
+  auto tiles_of = [&](const PackedItem& it, int c) -> int {
+    const int n = min(it.ntok - c * half, half);
+    return n <= 0 ? 0 : (visible_keys(it, p.causal, c * half + n - 1) + 127) >> 7;
+  };
+
+  if (warp >= 12) {
+    registers_down<kControlRegs>();
+    if (warp == 12) {
+      // ---------------------------------------------------------- items and copies
+      for (int s = blockIdx.x * 32 + lane; s < p.S; s += gridDim.x * 32) {
+        int a, b, c, d;
+        if (!packed_sequence(p, s, a, b, c, d)) raise_status(st, kStatusBounds);
+      }
+      __syncwarp();
+      bool ok = true;
+      int n = 0, cnt = 0, live0 = 0, live1 = 0;  // items, K and V tiles, items of A and B so far
+      auto load = [&](const CUtensorMap* map, const PackedItem& it, int j) -> bool {
+        const int s = cnt % R;
+        if (!warp_all(mbar_wait(empty + s, (uint32_t(cnt / R) & 1) ^ 1, st))) return false;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full + s, L::kTile);
+#pragma unroll
+          for (int rg = 0; rg < D / 64; ++rg)
+            tma_load_3d(sbase + L::kRing + s * L::kTile + rg * kRegion, map, rg * 64, it.hk, it.k0 + j * 128, smem_u32(full + s));
+        }
+        __syncwarp();
+        ++cnt;
+        return true;
+      };
+      long long i = blockIdx.x;
+      // the next item that has something to do (tiles -1: none is left)
+      auto next = [&](PackedItem& it) {
+        for (;; i += gridDim.x) {
+          if (i >= p.items) {
+            it.tiles = -1;
+            return;
+          }
+          if (!packed_item(p, wk.by_tq, wk.by_chunk, i, lane, &it)) continue;
+          i += gridDim.x;
+          return;
+        }
+      };
+      PackedItem it{}, following{};  // the first turn finds an item and loads nothing
+      for (bool begun = false;; it = following, begun = true) {
+        if (begun) {
+          const int b = n % kItems;
+          if (!(ok = warp_all(mbar_wait(it_empty + b, (uint32_t(n / kItems) & 1) ^ 1, st)))) break;
+          if (lane == 0) {
+            items[b] = it;
+            mbar_arrive(it_full + b);
+          }
+          __syncwarp();
+          ++n;
+          if (it.tiles < 0) break;
+        }
+        for (int x = 0; x < max(2 * it.tiles, 2); ++x) {  // K_0, queries, the item after this one, V_0, K_1, V_1, ...
+          if (x < 2 * it.tiles) {
+            if (!(ok = load(x & 1 ? &map_v : &map_k, it, x >> 1))) break;
+          }
+          if (x > 0) continue;
+#pragma unroll 1
+          for (int c = 0; c < 2 && ok && it.tiles > 0; ++c) {
+            if (tiles_of(it, c) == 0) continue;
+            const int nth = c ? live1++ : live0++;
+            if (!(ok = warp_all(mbar_wait(q_empty + c, (uint32_t(nth) & 1) ^ 1, st)))) break;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(q_full + c, uint32_t(half * p.g * 128 * (D / 64)));
+#pragma unroll
+              for (int rg = 0; rg < D / 64; ++rg)
+                tma_load_3d(sbase + L::kQ + c * L::kTile + rg * kRegion, &map_q, rg * 64, it.hk * p.g, it.q0 + c * half, smem_u32(q_full + c));
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          next(following);
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        if (lane == 0) raise_status(st, kStatusTimeout);
+        settle_copies();  // normally the products have consumed every copy before the CTA exits
+      }
+      __syncwarp();
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- products, of A and B in turn
+      constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
+      bool ok = true, issued = false;
+      int tile = 0, done0 = 0, done1 = 0, live0 = 0, live1 = 0;  // K/V tiles so far, those of each chain, its items
+      for (int n = 0; ok; ++n) {
+        PackedItem it;
+        if (!(ok = take(n, it))) break;
+        if (it.tiles < 0) break;
+        const int T0 = tiles_of(it, 0), T1 = tiles_of(it, 1);  // A's are not more than B's, unless B has none
+        // S_0 of both; then P_j V_j and S_{j+1}. The last chain that takes a tile lets its stage go.
+        for (int j = -1; j < it.tiles && ok; ++j) {
+          const uint32_t sv = uint32_t(2 * (tile + j) + 1) % R, sk = (sv + 1) % R;
+          const uint32_t vlo = desc_lo_mnmajor(sbase + L::kRing + sv * L::kTile), klo = desc_lo_kmajor(sbase + L::kRing + sk * L::kTile);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int T = c ? T1 : T0;
+            if (j >= T || T == 0) continue;
+            if (!(ok = warp_all(mbar_wait((j < 0 ? s_go : p_full) + c, j < 0 ? uint32_t(c ? live1 : live0) & 1 : uint32_t((c ? done1 : done0) + j) & 1, st)))) break;
+            tc_fence_after();
+            issued = true;
+            const uint32_t tO = tmem + L::kColO + c * 128, tS = tmem + L::kColS + c * 128;
+            if (elect_one()) {
+              if (j >= 0) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                  tc_mma_ts_lo(tO, tS + ks * 8, vlo + kstep_mnmajor(ks), kIdescPV, (j > 0 || ks > 0) ? 1u : 0u);
+                if (c == 1 || j >= T1) tc_commit(empty + sv);
+                if (j == T - 1) {
+                  tc_commit(o_full + c);
+                  mbar_arrive(o_full + c);  // passes on the flags of V
+                }
+              }
+              if (j + 1 < T) {
+                const uint32_t qlo = desc_lo_kmajor(sbase + L::kQ + c * L::kTile);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                  tc_mma_ss_lo(tS, qlo + kstep_kmajor(ks), klo + kstep_kmajor(ks), kIdescQK, ks > 0 ? 1u : 0u);
+                tc_commit(s_full + c);
+                if (c == 1 || j + 1 >= T1) tc_commit(empty + sk);
+                if (j + 2 == T) tc_commit(q_empty + c);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok) break;
+        tile += it.tiles;
+        done0 += T0, done1 += T1, live0 += T0 > 0, live1 += T1 > 0;
+      }
+      if (!ok) {
+        if (lane == 0) raise_status(st, kStatusTimeout);
+        if (issued) {
+          if (elect_one()) tc_commit(drain);
+          __syncwarp();
+          mbar_drain(drain, 0);
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- V tiles, and what lets the products go
+      bool ok = true;
+      int tile = 0, done0 = 0, done1 = 0, live0 = 0, live1 = 0;
+      auto landed = [&](int x) { return warp_all(mbar_wait(full + x % R, uint32_t(x / R) & 1, st)); };
+      for (int n = 0; ok; ++n) {
+        PackedItem it;
+        if (!(ok = take(n, it))) break;
+        if (it.tiles < 0) break;
+        const int T0 = tiles_of(it, 0), T1 = tiles_of(it, 1);
+        const int all_see = visible_keys(it, p.causal, 0);
+        bool found = false;
+        const int part = warp - 14;
+        if (lane == 0) odd[n % kFlags * 2 + part] = 0;
+        if (it.tiles > 0 && !(ok = landed(2 * tile))) break;
+#pragma unroll 1
+        for (int x = -2; x < 2 * it.tiles && ok; ++x) {
+          const int j = x >> 1, c = x & 1, T = c ? T1 : T0, live = c ? live1 : live0;
+          if (j >= 0 && c == 0) {
+            const int v = 2 * (tile + j) + 1;
+            if (!(ok = landed(v))) break;
+            if ((j + 1) * 128 > all_see) {
+              found |= settle_v<D, 2>(sbase + L::kRing + v % R * L::kTile, max(0, all_see - j * 128), min(128, it.nkeys - j * 128), part, lane);
+              fence_proxy_async_smem();
+              if (__any_sync(0xffffffffu, found) && lane == 0) odd[n % kFlags * 2 + part] = 1;
+              __syncwarp();
+            }
+            if (j + 1 < it.tiles && !(ok = landed(v + 1))) break;
+          }
+          if (j >= T || T == 0) continue;
+          if (j < 0) {
+            ok = warp_all(mbar_wait(q_full + c, uint32_t(live) & 1, st));
+          } else {
+            if (j == 0) ok = warp_all(mbar_wait(o_free + c, (uint32_t(live) & 1) ^ 1, st));
+            // one arrival of each warp a phase: the last tile's has to be complete
+            if (ok) ok = warp_all(mbar_wait(p_full + c, (uint32_t((c ? done1 : done0) + j) & 1) ^ 1, st));
+          }
+          if (ok && lane == 0) mbar_arrive((j < 0 ? s_go : p_full) + c);
+        }
+        tile += it.tiles;
+        done0 += T0, done1 += T1, live0 += T0 > 0, live1 += T1 > 0;
+      }
+      if (!ok && lane == 0) raise_status(st, kStatusTimeout);
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    registers_down<kOutRegs>();
+    // ------------------------------------------------------------ the way out
+    const int w4 = warp & 3, row = w4 * 32 + lane;
+    const int tt = p.by_group.div(row), hh = row - tt * p.g;  // this row's token of a tile and head of the group
+    bool ok = true;
+    int live0 = 0, live1 = 0;
+    const uint32_t patch = sbase + L::kOut + w4 * kPatch;
+    for (int n = 0; ok; ++n) {
+      PackedItem it;
+      if (!(ok = take(n, it))) break;
+      if (it.tiles < 0) break;
+      const int all_see = visible_keys(it, p.causal, 0);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        const int ntok = min(it.ntok - c * half, half);
+        if (ntok <= 0) continue;
+        const bool some = tiles_of(it, c) > 0;  // otherwise no row sees anything
+        const uint32_t tO = tmem + L::kColO + c * 128 + (uint32_t(w4 * 32) << 16);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (some) {
+          if (!(ok = warp_all(mbar_wait(o_full + c, uint32_t(c ? live1++ : live0++) & 1, st)))) break;
+          tc_fence_after();
+          ml = stats[c * 128 + row];
+        }
+        const bool mine = tt < ntok;
+        const int rows = min(32, ntok * p.g - w4 * 32);  // of this warp
+        if (rows > 0) {
+          const float l = ml.y, inv = l == 0.f ? 0.f : 1.f / l;  // rows that see nothing give 0
+          // elements of V that are not finite and that only some rows see (left out of the products)
+          const bool extra = some && all_see < it.nkeys && (odd[n % kFlags * 2] | odd[n % kFlags * 2 + 1]) != 0;
+          const int lim = visible_keys(it, p.causal, c * half + tt);
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + static_cast<long long>(it.hk) * p.g * p.os.head +
+                               static_cast<long long>(it.q0 + c * half) * p.os.token;
+#pragma unroll 1
+          for (int q = 0; q < D / 64; ++q) {  // 64 columns: 128 bytes a row
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {  // 16 columns
+              float o[16];
+              if (some) {
+                uint32_t u[16];
+                tmem_ld16(tO + q * 64 + x * 16, u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(u[i]) * inv;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = 0.f;
+              }
+              if (extra && mine) {
+                const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(p.v) + static_cast<long long>(it.hk) * p.vs.head + q * 64 + x * 16;
+#pragma unroll 1
+                for (int j = all_see; j < lim; ++j) {
+                  const __nv_bfloat16* vr = vb + static_cast<long long>(it.k0 + j) * p.vs.token;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const float f = __bfloat162float(vr[i]);
+                    if (!isfinite(f)) o[i] += f;
+                  }
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + (((x * 2 + i) ^ (lane & 7)) << 4)),
+                             "r"(pack_bf16x2(o[8 * i], o[8 * i + 1])), "r"(pack_bf16x2(o[8 * i + 2], o[8 * i + 3])),
+                             "r"(pack_bf16x2(o[8 * i + 4], o[8 * i + 5])), "r"(pack_bf16x2(o[8 * i + 6], o[8 * i + 7]))
+                             : "memory");
+            }
+            if (q == D / 64 - 1 && some) {  // the sums have been read
+              tc_fence_before();
+              mbar_arrive(o_free + c);
+            }
+            __syncwarp();
+            // along rows: eight lanes a row
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + (lane >> 3), ch = lane & 7;
+              if (r < rows) {
+                uint4 w;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                             : "r"(patch + r * 128 + ((ch ^ (r & 7)) << 4))
+                             : "memory");
+                const int rr = w4 * 32 + r, rt = p.by_group.div(rr), rh = rr - rt * p.g;
+                *reinterpret_cast<uint4*>(out + rh * p.os.head + rt * p.os.token + q * 64 + ch * 8) = w;
+              }
+            }
+            __syncwarp();
+          }
+          if (mine && p.lse != nullptr)
+            p.lse[static_cast<long long>(it.hk * p.g + hh) * p.Tq + it.q0 + c * half + tt] = l == 0.f ? -INFINITY : (ml.x + __log2f(l)) * kLn2;
+        } else if (some) {
+          tc_fence_before();
+          mbar_arrive(o_free + c);
+        }
+      }
+    }
+    if (!ok && lane == 0) raise_status(st, kStatusTimeout);
+    __syncwarp();
+  } else {
+    registers_up<kSoftmaxRegs>();
+    // ------------------------------------------------------------ softmax
+    const int c = warp >> 2, w4 = warp & 3;
+    const int row = tid & 127;
+    const int tt = p.by_group.div(row), t = c * half + tt;  // this row's token of the tile, of the item
+    const uint32_t lane_off = uint32_t(w4 * 32) << 16;
+    const uint32_t tS = tmem + L::kColS + c * 128 + lane_off, tO = tmem + L::kColO + c * 128 + lane_off;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int tile = 0, live = 0;  // of this chain
+    for (int n = 0; ok; ++n) {
+      PackedItem it;
+      if (!(ok = take(n, it))) break;
+      if (it.tiles < 0) break;
+      const int ntok = min(it.ntok - c * half, half);
+      if (ntok <= 0) continue;
+      const int T = tiles_of(it, c);
+      const bool mine = tt < ntok;  // ntok <= half, so a row past the tile's last is nobody's
+      const int lim = mine ? visible_keys(it, p.causal, t) : it.nkeys;
+      const bool busy = w4 * 32 < ntok * p.g;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < T; ++j, ++tile) {
+        if (!(ok = warp_all(mbar_wait(s_full + c, uint32_t(tile) & 1, st)))) break;
+        tc_fence_after();
+        uint32_t pk[64];
+        bool need = false;
+        float alpha = 1.f;
+        if (busy) {
+          const int nvalid = lim - j * 128;
+          if (__any_sync(0xffffffffu, nvalid < 128)) mask_scores(tS, nvalid);
+          uint32_t r[128];
+          tmem_ld128(tS, r);
+          float mp[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mp[i] = __uint_as_float(r[i]);
+#pragma unroll
+          for (int i = 8; i < 128; i += 2) mp[(i >> 1) & 7] = fmax3(mp[(i >> 1) & 7], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+          const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
+          const float m_new = fmaxf(m, mx * sl2);
+          need = m_new > m + 8.f;  // the sums are scaled anew only where the maximum grew by more than 2^8
+          const float m_use = need ? m_new : m;
+          alpha = need ? ex2_approx(m - m_new) : 1.f;
+          const float neg_m = m_use == -INFINITY ? 0.f : -m_use;
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), negmx2 = f2_pack(neg_m, neg_m);
+          uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), sl2x2, negmx2), x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            ls2[i & 1] = f2_add(ls2[i & 1], f2_pack(p0, p1));
+            pk[i] = pack_bf16x2(p0, p1);
+          }
+          float la, lb;
+          f2_unpack(f2_add(ls2[0], ls2[1]), la, lb);
+          l = l * alpha + (la + lb);
+          m = m_use;
+          // the last tile's P V is done: S came behind it
+          if (__any_sync(0xffffffffu, need && j > 0)) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(tO + q * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + q * 32, o);
+            }
+          }
+          tmem_st64(tS, pk);
+        }
+        tc_fence_before();
+        mbar_arrive(p_full + c);
+      }
+      if (!ok) break;
+      if (T == 0) continue;
+      // the last item's rows have been read
+      if (!(ok = warp_all(mbar_wait(o_free + c, (uint32_t(live) & 1) ^ 1, st)))) break;
+      ++live;
+      stats[c * 128 + row] = make_float2(m, l);
+      mbar_arrive(o_full + c);
+    }
+    if (!ok && lane == 0) raise_status(st, kStatusTimeout);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_two(const PackedParams& p, int num_sms, cudaStream_t s) {
+  CUtensorMap mq, mk, mv;
+  if (!(make_view_map(&mq, p.q, p.H, p.Tq, D, p.qs, p.g, p.tq / 2) && make_view_map(&mk, p.k, p.Hk, p.Tk, D, p.ks, 1, 128) &&
+        make_view_map(&mv, p.v, p.Hk, p.Tk, D, p.vs, 1, 128)))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem_and_regs<packed_pair_kernel<D>>(Cfg<D>::kAlloc, kLaunchRegs);
+  if (e != cudaSuccess) return e;
+  const int grid = p.items < num_sms ? int(p.items) : num_sms;
+  return launch_overlapped(packed_pair_kernel<D>, dim3(grid), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
+}
+
+}  // namespace
+
+cudaError_t packed_attn_pair(const PackedParams& p, int num_sms, cudaStream_t s) {
+  return p.d == 128 ? launch_two<128>(p, num_sms, s) : launch_two<64>(p, num_sms, s);
+}
+
+}  // namespace mcs

@@ -88,6 +88,19 @@ def test_against_oracle(dtype, causal, heads, case):
     check(q, k, v, qs, ks, causal, out="tokens" if case % 2 else "heads")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", [(3, 3), (6, 2), (8, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_long_prompts(d, heads, causal):
+    """Several tiles of queries and of keys, prompts and chunks, more blocks than items a head and the other way round."""
+    H, Hk = heads
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for nq, nk in (([700, 259, 30], [700, 259, 30]), ([300, 5, 600], [1111, 900, 200])):
+        qs, ks = starts(nq), starts(nk)
+        q, k, v = view(g, H, qs[-1], d, torch.bfloat16, "tokens", 2.0), view(g, Hk, ks[-1], d, torch.bfloat16, "tokens"), view(g, Hk, ks[-1], d, torch.bfloat16, "heads")
+        check(q, k, v, qs, ks, causal)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("nq,nk", [([1] * 4, [2000, 700, 5, 1500]), ([3, 1, 2], [900, 0, 2500]), ([40, 7], [1100, 1300])])
