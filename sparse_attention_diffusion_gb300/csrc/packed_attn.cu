@@ -540,7 +540,7 @@ size_t packed_workspace_bytes(const PackedParams& p) {
 }
 
 cudaError_t packed_attn_tc(const PackedParams& p, int num_sms, cudaStream_t s) {
-  if (p.pair) return packed_attn_pair(p, num_sms, s);
+  if (p.pair) return packed_attn_pair(p, s);
   const cudaError_t e = p.d == 128 ? launch_tc<128>(p, num_sms, s) : launch_tc<64>(p, num_sms, s);
   return e != cudaSuccess || p.chunk == 0 ? e : packed_join(p, true, s);
 }

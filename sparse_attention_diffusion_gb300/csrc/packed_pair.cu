@@ -3,7 +3,8 @@
 //
 // One tile alone leaves the tensor core idle while its softmax runs, and the other way round: 1,850 clocks a tile of 128 x
 // 128 scores of which the products take 1,024. Here two tiles, A and B, share every K and V tile and take turns: while
-// A's softmax runs, B's P V and next S do. A persistent grid, one CTA per SM, 512 threads:
+// A's softmax runs, B's P V and next S do. A block an item, of which one an SM runs and takes over the items of blocks that have not started (cluster launch
+// control), so that items of unlike length spread by themselves; 512 threads:
 //   warps 0-3, 4-7  softmax of A and of B, a thread per row
 //   warps 8-11      the rows' way out, of A and then of B, while the softmax is at the next item
 //   warp 12         finds the items and loads by TMA: the queries of A and of B, and one ring of K_0, V_0, K_1, V_1, ...
@@ -46,8 +47,9 @@ struct Cfg {
   static constexpr int kOut = kRing + kStages * kTile;
   static constexpr int kStats = kOut + 4 * kPatch;    // (maximum, sum) of A's and B's rows
   static constexpr int kBar = kStats + 2 * 128 * 8;
-  static constexpr int kNumBars = 2 * kStages + 2 * 7 + 2 * kItems + 1;
-  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kNumBars = 2 * kStages + 2 * 7 + 2 * kItems + 2;
+  static constexpr int kSteal = (kBar + kNumBars * 8 + 15) / 16 * 16;  // the answer to a request for a block
+  static constexpr int kMisc = kSteal + 16;
   static constexpr int kItem = (kMisc + 16 + kFlags * 8 + 15) / 16 * 16;
   static constexpr int kBytes = kItem + kItems * int(sizeof(PackedItem));
   static constexpr int kAlloc = kBytes + 1024;
@@ -76,6 +78,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* it_full = o_free + 2;     // [kItems]
   uint64_t* it_empty = it_full + kItems;
   uint64_t* drain = it_empty + kItems;
+  uint64_t* steal = drain + 1;
+  const uint32_t steal_slot = sbase + L::kSteal;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* odd = tmem_slot + 4;  // [kFlags][2] the item's V held something that is not finite and not seen by all
   float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(q_full + c, 1), mbar_init(q_empty + c, 1), mbar_init(s_go + c, 2), mbar_init(s_full + c, 1);
       mbar_init(p_full + c, 130), mbar_init(o_full + c, 130), mbar_init(o_free + c, 128);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 1), mbar_init(steal, 1);
     for (int b = 0; b < kItems; ++b) mbar_init(it_full + b, 1), mbar_init(it_empty + b, 8 + 4 + 3);
     fence_mbar_init();
   }
@@ -125,11 +129,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     registers_down<kControlRegs>();
     if (warp == 12) {
       // ---------------------------------------------------------- items and copies
-      for (int s = blockIdx.x * 32 + lane; s < p.S; s += gridDim.x * 32) {
-        int a, b, c, d;
-        if (!packed_sequence(p, s, a, b, c, d)) raise_status(st, kStatusBounds);
-      }
-      __syncwarp();
       bool ok = true;
       int n = 0, cnt = 0, live0 = 0, live1 = 0;  // items, K and V tiles, items of A and B so far
       auto load = [&](const CUtensorMap* map, const PackedItem& it, int j) -> bool {
@@ -145,17 +144,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++cnt;
         return true;
       };
-      long long i = blockIdx.x;
-      // the next item that has something to do (tiles -1: none is left)
-      auto next = [&](PackedItem& it) {
-        for (;; i += gridDim.x) {
-          if (i >= p.items) {
-            it.tiles = -1;
-            return;
+      // The next item that has something to do (tiles -1: none is left): this block's own, then those of blocks that have
+      // not started yet, which it asks the hardware for, one request ahead.
+      int steals = 0;
+      bool own = true;
+      auto ask = [&]() {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(steal, 16);
+          steal_block(steal_slot, steal);
+        }
+        __syncwarp();
+      };
+      ask();
+      auto next = [&](PackedItem& it) -> bool {
+        while (true) {
+          int i = int(blockIdx.x);
+          if (!own) {
+            if (!warp_all(mbar_wait(steal, uint32_t(steals++) & 1, st))) return false;
+            i = stolen_block(steal_slot);
+            if (i < 0) {
+              it.tiles = -1;
+              return true;
+            }
+            fence_proxy_async_smem();  // the answer has been read; the next one may overwrite it
+            __syncwarp();
+            ask();
           }
-          if (!packed_item(p, wk.by_tq, wk.by_chunk, i, lane, &it)) continue;
-          i += gridDim.x;
-          return;
+          own = false;
+          if (const long long s = static_cast<long long>(i) * 32 + lane; s < p.S) {  // there are more items than sequences
+            int a, b, c, d;
+            if (!packed_sequence(p, int(s), a, b, c, d)) raise_status(st, kStatusBounds);
+          }
+          __syncwarp();
+          if (packed_item(p, wk.by_tq, wk.by_chunk, i, lane, &it)) return true;
         }
       };
       PackedItem it{}, following{};  // the first turn finds an item and loads nothing
@@ -190,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (!ok) break;
-          next(following);
+          if (!(ok = next(following))) break;
         }
         if (!ok) break;
       }
@@ -496,21 +517,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_two(const PackedParams& p, int num_sms, cudaStream_t s) {
+cudaError_t launch_two(const PackedParams& p, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   if (!(make_view_map(&mq, p.q, p.H, p.Tq, D, p.qs, p.g, p.tq / 2) && make_view_map(&mk, p.k, p.Hk, p.Tk, D, p.ks, 1, 128) &&
         make_view_map(&mv, p.v, p.Hk, p.Tk, D, p.vs, 1, 128)))
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem_and_regs<packed_pair_kernel<D>>(Cfg<D>::kAlloc, kLaunchRegs);
   if (e != cudaSuccess) return e;
-  const int grid = p.items < num_sms ? int(p.items) : num_sms;
-  return launch_overlapped(packed_pair_kernel<D>, dim3(grid), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
+  return launch_overlapped(packed_pair_kernel<D>, dim3(unsigned(p.items)), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
 }
 
 }  // namespace
 
-cudaError_t packed_attn_pair(const PackedParams& p, int num_sms, cudaStream_t s) {
-  return p.d == 128 ? launch_two<128>(p, num_sms, s) : launch_two<64>(p, num_sms, s);
+cudaError_t packed_attn_pair(const PackedParams& p, cudaStream_t s) {
+  return p.d == 128 ? launch_two<128>(p, s) : launch_two<64>(p, s);
 }
 
 }  // namespace mcs

@@ -134,6 +134,27 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// ---------------------------------------------------------------- cluster launch control
+// Ask for a block of this grid that has not started: 16 bytes arrive at `slot` (16-byte aligned shared memory) and on the
+// barrier. Not to be asked again after an answer that there was none.
+__device__ __forceinline__ void steal_block(uint32_t slot, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(slot),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The answer: the block's index along x, which will not start by itself any more, or -1.
+__device__ __forceinline__ int stolen_block(uint32_t slot) {
+  int x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 h;\n .reg .b32 y, z, w;\n ld.shared.b128 h, [%1];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n mov.b32 %0, -1;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n}\n"
+      : "=r"(x)
+      : "r"(slot)
+      : "memory");
+  return x;
+}
+
 // ---------------------------------------------------------------- cp.async (16 B, zero-fill)
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   const uint32_t n = valid ? 16u : 0u;  // src-size 0 writes 16 zero bytes
