@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The next item for a role; its slot is given back at once. n: items taken so far.
   auto take = [&](int n, PackedItem& it) -> bool {
     const int b = n % kItems;
-    if (!warp_all(mbar_wait(it_full + b, uint32_t(n / kItems) & 1, st))) return false;
+    if (!warp_all(mbar_wait_short(it_full + b, uint32_t(n / kItems) & 1))) return false;
     it = items[b];
     __syncwarp();
     if (lane == 0) mbar_arrive(it_empty + b);
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0, cnt = 0, live0 = 0, live1 = 0;  // items, K and V tiles, items of A and B so far
       auto load = [&](const CUtensorMap* map, const PackedItem& it, int j) -> bool {
         const int s = cnt % R;
-        if (!warp_all(mbar_wait(empty + s, (uint32_t(cnt / R) & 1) ^ 1, st))) return false;
+        if (!warp_all(mbar_wait_short(empty + s, (uint32_t(cnt / R) & 1) ^ 1))) return false;
         if (elect_one()) {
           mbar_arrive_expect_tx(full + s, L::kTile);
 #pragma unroll
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (true) {
           int i = int(blockIdx.x);
           if (!own) {
-            if (!warp_all(mbar_wait(steal, uint32_t(steals++) & 1, st))) return false;
+            if (!warp_all(mbar_wait_short(steal, uint32_t(steals++) & 1))) return false;
             i = stolen_block(steal_slot);
             if (i < 0) {
               it.tiles = -1;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool begun = false;; it = following, begun = true) {
         if (begun) {
           const int b = n % kItems;
-          if (!(ok = warp_all(mbar_wait(it_empty + b, (uint32_t(n / kItems) & 1) ^ 1, st)))) break;
+          if (!(ok = warp_all(mbar_wait_short(it_empty + b, (uint32_t(n / kItems) & 1) ^ 1)))) break;
           if (lane == 0) {
             items[b] = it;
             mbar_arrive(it_full + b);
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 2 && ok && it.tiles > 0; ++c) {
             if (tiles_of(it, c) == 0) continue;
             const int nth = c ? live1++ : live0++;
-            if (!(ok = warp_all(mbar_wait(q_empty + c, (uint32_t(nth) & 1) ^ 1, st)))) break;
+            if (!(ok = warp_all(mbar_wait_short(q_empty + c, (uint32_t(nth) & 1) ^ 1)))) break;
             if (elect_one()) {
               mbar_arrive_expect_tx(q_full + c, uint32_t(half * p.g * 128 * (D / 64)));
 #pragma unroll
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 2; ++c) {
             const int T = c ? T1 : T0;
             if (j >= T || T == 0) continue;
-            if (!(ok = warp_all(mbar_wait((j < 0 ? s_go : p_full) + c, j < 0 ? uint32_t(c ? live1 : live0) & 1 : uint32_t((c ? done1 : done0) + j) & 1, st)))) break;
+            if (!(ok = warp_all(mbar_wait_short((j < 0 ? s_go : p_full) + c, j < 0 ? uint32_t(c ? live1 : live0) & 1 : uint32_t((c ? done1 : done0) + j) & 1)))) break;
             tc_fence_after();
             issued = true;
             const uint32_t tO = tmem + L::kColO + c * 128, tS = tmem + L::kColS + c * 128;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- V tiles, and what lets the products go
       bool ok = true;
       int tile = 0, done0 = 0, done1 = 0, live0 = 0, live1 = 0;
-      auto landed = [&](int x) { return warp_all(mbar_wait(full + x % R, uint32_t(x / R) & 1, st)); };
+      auto landed = [&](int x) { return warp_all(mbar_wait_short(full + x % R, uint32_t(x / R) & 1)); };
       for (int n = 0; ok; ++n) {
         PackedItem it;
         if (!(ok = take(n, it))) break;
@@ -311,11 +311,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j >= T || T == 0) continue;
           if (j < 0) {
-            ok = warp_all(mbar_wait(q_full + c, uint32_t(live) & 1, st));
+            ok = warp_all(mbar_wait_short(q_full + c, uint32_t(live) & 1));
           } else {
-            if (j == 0) ok = warp_all(mbar_wait(o_free + c, (uint32_t(live) & 1) ^ 1, st));
+            if (j == 0) ok = warp_all(mbar_wait_short(o_free + c, (uint32_t(live) & 1) ^ 1));
             // one arrival of each warp a phase: the last tile's has to be complete
-            if (ok) ok = warp_all(mbar_wait(p_full + c, (uint32_t((c ? done1 : done0) + j) & 1) ^ 1, st));
+            if (ok) ok = warp_all(mbar_wait_short(p_full + c, (uint32_t((c ? done1 : done0) + j) & 1) ^ 1));
           }
           if (ok && lane == 0) mbar_arrive((j < 0 ? s_go : p_full) + c);
         }
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tmem + L::kColO + c * 128 + (uint32_t(w4 * 32) << 16);
         float2 ml = make_float2(-INFINITY, 0.f);
         if (some) {
-          if (!(ok = warp_all(mbar_wait(o_full + c, uint32_t(c ? live1++ : live0++) & 1, st)))) break;
+          if (!(ok = warp_all(mbar_wait_short(o_full + c, uint32_t(c ? live1++ : live0++) & 1)))) break;
           tc_fence_after();
           ml = stats[c * 128 + row];
         }
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool busy = w4 * 32 < ntok * p.g;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < T; ++j, ++tile) {
-        if (!(ok = warp_all(mbar_wait(s_full + c, uint32_t(tile) & 1, st)))) break;
+        if (!(ok = warp_all(mbar_wait_short(s_full + c, uint32_t(tile) & 1)))) break;
         tc_fence_after();
         uint32_t pk[64];
         bool need = false;
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (T == 0) continue;
       // the last item's rows have been read
-      if (!(ok = warp_all(mbar_wait(o_free + c, (uint32_t(live) & 1) ^ 1, st)))) break;
+      if (!(ok = warp_all(mbar_wait_short(o_free + c, (uint32_t(live) & 1) ^ 1)))) break;
       ++live;
       stats[c * 128 + row] = make_float2(m, l);
       mbar_arrive(o_full + c);

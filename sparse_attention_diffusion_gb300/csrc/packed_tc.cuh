@@ -12,16 +12,13 @@ struct PackedWalk {
   Divisor by_tq, by_chunk, by_one;
 };
 
-__device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
-  return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
-}
-// Both halves, what is not finite as 0.
+// Whether one of two bf16 numbers is infinite or NaN: adding 1 to an exponent of ones carries into the sign's place.
+__device__ __forceinline__ uint32_t odd_bf16x2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+// Both, what is not finite as 0.
 __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
-  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-  return w;
+  const uint32_t o = odd_bf16x2(w);
+  return w & ~((o >> 15 & 0x00010001u) * 0xffffu);
 }
-
 // Rows some .. none - 1 of a V tile, which some tokens do not see, with what is not finite as 0, and rows from none
 // on, which nobody sees, as 0. Whether there was such an element. Warp `part` of kParts, 16 bytes a lane.
 template <int D, int kParts = 1>
@@ -29,18 +26,31 @@ __device__ __forceinline__ bool settle_v(uint32_t v, int some, int none, int par
   constexpr int kRowLanes = D / 8, kRows = kParts * 32 / kRowLanes;
   const int ch = lane % kRowLanes, row0 = part * (32 / kRowLanes) + lane / kRowLanes;
   bool found = false;
-#pragma unroll 4
-  for (int r = some + row0; r < none; r += kRows) {
-    const uint32_t at = v + sw128_off(r, ch);
-    uint4 w;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
-    if (!(finite_bf16x2(w.x) && finite_bf16x2(w.y) && finite_bf16x2(w.z) && finite_bf16x2(w.w))) {
-      found = true;
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(finite_part(w.x)), "r"(finite_part(w.y)),
-                   "r"(finite_part(w.z)), "r"(finite_part(w.w))
+#pragma unroll 1
+  for (int r0 = some + row0; r0 < none; r0 += 4 * kRows) {
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // rows from `none` on are overwritten below, where they are looked at here
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "r"(v + sw128_off(min(r0 + i * kRows, 127), ch))
+                   : "memory");
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) odd |= odd_bf16x2(w[i].x) | odd_bf16x2(w[i].y) | odd_bf16x2(w[i].z) | odd_bf16x2(w[i].w);
+    if (odd == 0) continue;
+#pragma unroll 1
+    for (int r = r0; r < min(none, r0 + 4 * kRows); r += kRows) {
+      const uint32_t at = v + sw128_off(r, ch);
+      uint4 x;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+      found |= (odd_bf16x2(x.x) | odd_bf16x2(x.y) | odd_bf16x2(x.z) | odd_bf16x2(x.w)) != 0;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(finite_part(x.x)), "r"(finite_part(x.y)),
+                   "r"(finite_part(x.z)), "r"(finite_part(x.w))
                    : "memory");
     }
   }
+#pragma unroll 1
   for (int r = none + row0; r < 128; r += kRows)
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + sw128_off(r, ch)), "r"(0) : "memory");
   return found;

@@ -74,6 +74,28 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// The same in fewer instructions, for kernels with many waits, which would not fit the instruction cache otherwise: the
+// clock is looked at after every 1,024 tries only, and other blocks' timeouts are not.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b32 n;\n mov.b32 n, 0;\nAGAIN_%=:\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE_%=;\n add.u32 n, n, 1;\n"
+        " setp.ge.u32 p, n, 1024;\n @!p bra AGAIN_%=;\n mov.b32 %0, 0;\n bra END_%=;\nDONE_%=:\n mov.b32 %0, 1;\nEND_%=:\n}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok != 0) return true;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) return false;
+  }
+}
+
 // On the way out of a failed kernel: wait for MMAs already issued, whatever the
 // timeout flag (which is set by then) says, with a limit of its own.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
