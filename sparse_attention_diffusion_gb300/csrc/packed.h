@@ -47,7 +47,7 @@ struct PackedParams {
 // Fills the tiles, chunks and item counts; false where they do not fit in 31 bits.
 bool plan_packed(PackedParams* p, bool bf16);
 size_t packed_workspace_bytes(const PackedParams& p);
-cudaError_t packed_attn_tc(const PackedParams& p, int num_sms, cudaStream_t s);
+cudaError_t packed_attn_tc(const PackedParams& p, cudaStream_t s);
 cudaError_t packed_attn_pair(const PackedParams& p, cudaStream_t s);
 cudaError_t packed_attn_f32(const PackedParams& p, cudaStream_t s);
 cudaError_t packed_join(const PackedParams& p, bool bf16, cudaStream_t s);

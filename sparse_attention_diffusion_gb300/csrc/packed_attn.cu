@@ -3,7 +3,8 @@
 // over the keys j of query i's own sequence that it sees (with a causal mask the last of its nq queries
 // sees all nk keys and each one before it one key less), grouped heads, lengths read on the device.
 //
-// A persistent grid, one CTA per SM, walks the items of packed.h; 224 threads:
+// A block an item of packed.h, of which one an SM runs and takes over the items of blocks that have not started (cluster
+// launch control), so that items of unlike length spread by themselves; 224 threads:
 //   warp 5    finds the items (four ahead) and loads by TMA: the item's queries as one box of g heads x
 //             tq tokens, then rings of K and V tiles of 128 keys, K one tile ahead of V;
 //   warp 4    tensor-memory allocation, S_j = Q K_j^T into two buffers;
@@ -46,8 +47,9 @@ struct Cfg {
   static constexpr int kK = kQ + kTile;
   static constexpr int kV = kK + kStages * kTile;
   static constexpr int kBar = kV + kStages * kTile;
-  static constexpr int kNumBars = 4 * kStages + 2 + 2 + 2 + 2 + 2 + 2 * kItems + 2;
-  static constexpr int kMisc = kBar + kNumBars * 8;  // tensor-memory slot, flags, items
+  static constexpr int kNumBars = 4 * kStages + 2 + 2 + 2 + 2 + 2 + 2 * kItems + 2 + 1;
+  static constexpr int kSteal = (kBar + kNumBars * 8 + 15) / 16 * 16;  // the answer to a request for a block
+  static constexpr int kMisc = kSteal + 16;  // tensor-memory slot, flags, items
   static constexpr int kItem = (kMisc + 16 + kFlags * 4 + 15) / 16 * 16;
   static constexpr int kBytes = kItem + kItems * int(sizeof(PackedItem));
   static constexpr int kAlloc = kBytes + 1024;
@@ -79,6 +81,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* it_full = o_free + 1;       // [kItems]
   uint64_t* it_empty = it_full + kItems;
   uint64_t* drain = it_empty + kItems;  // [2]
+  uint64_t* steal = drain + 2;
+  const uint32_t steal_slot = sbase + L::kSteal;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* odd = tmem_slot + 4;  // [kFlags] the item's V held something that is not finite and not seen by all
   PackedItem* items = reinterpret_cast<PackedItem*>(smem + L::kItem);
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < S; ++s) mbar_init(k_full + s, 1), mbar_init(k_empty + s, 1), mbar_init(v_full + s, 1), mbar_init(v_empty + s, 1);
     for (int b = 0; b < 2; ++b) mbar_init(s_full + b, 1), mbar_init(s_free + b, 128), mbar_init(drain + b, 1);
     mbar_init(p_full, 128), mbar_init(p_empty, 1);
-    mbar_init(q_full, 1), mbar_init(q_empty, 1);
+    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(steal, 1);
     mbar_init(o_full, 2), mbar_init(o_free, 128);  // o_full: the products and the flag of V
     for (int b = 0; b < kItems; ++b) mbar_init(it_full + b, 1), mbar_init(it_empty + b, 4 + 2);
     fence_mbar_init();
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The next item for a role; its slot is given back at once. n: items taken so far.
   auto take = [&](int n, PackedItem& it) -> bool {
     const int b = n % kItems;
-    const bool ok = warp_all(mbar_wait(it_full + b, uint32_t(n / kItems) & 1, st));
+    const bool ok = warp_all(mbar_wait_short(it_full + b, uint32_t(n / kItems) & 1));
     if (!ok) return false;
     it = items[b];
     __syncwarp();
@@ -120,16 +124,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 5) {
     // ------------------------------------------------------------ items and copies
-    for (int s = blockIdx.x * 32 + lane; s < p.S; s += gridDim.x * 32) {
-      int a, b, c, d;
-      if (!packed_sequence(p, s, a, b, c, d)) raise_status(st, kStatusBounds);
-    }
-    __syncwarp();
     bool ok = true;
     int n = 0, live = 0, kn = 0, vn = 0;  // items, those with keys, K and V tiles so far
     auto load = [&](uint64_t* full, uint64_t* empty, int base, const CUtensorMap* map, int& cnt, const PackedItem& it, int j) -> bool {
       const int s = cnt % S;
-      if (!warp_all(mbar_wait(empty + s, (uint32_t(cnt / S) & 1) ^ 1, st))) return false;
+      if (!warp_all(mbar_wait_short(empty + s, (uint32_t(cnt / S) & 1) ^ 1))) return false;
       if (elect_one()) {
         mbar_arrive_expect_tx(full + s, L::kTile);
 #pragma unroll
@@ -140,37 +139,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++cnt;
       return true;
     };
-    for (long long i = blockIdx.x;; i += gridDim.x) {
-      PackedItem it;
-      bool last = i >= p.items;
-      if (!last && !packed_item(p, wk.by_tq, wk.by_chunk, i, lane, &it)) continue;
-      if (last) it.tiles = -1;
-      const int b = n % kItems;
-      if (!(ok = warp_all(mbar_wait(it_empty + b, (uint32_t(n / kItems) & 1) ^ 1, st)))) break;
-      if (lane == 0) {
-        items[b] = it;
-        mbar_arrive(it_full + b);
-      }
-      __syncwarp();
-      ++n;
-      if (last) break;
-      if (it.tiles == 0) continue;
-      // the first keys do not wait for the queries' place, which the last item's S products still read
-      for (int j = 0; j <= it.tiles && ok; ++j) {
-        if (j < it.tiles && !(ok = load(k_full, k_empty, L::kK, &map_k, kn, it, j))) break;
-        if (j == 0) {
-          if (!(ok = warp_all(mbar_wait(q_empty, (uint32_t(live) & 1) ^ 1, st)))) break;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(q_full, uint32_t(p.rows * 128 * (D / 64)));
-#pragma unroll
-            for (int rg = 0; rg < D / 64; ++rg)
-              tma_load_3d(sbase + L::kQ + rg * kRegion, &map_q, rg * 64, it.hk * p.g, it.q0, smem_u32(q_full));
-          }
-          __syncwarp();
-          ++live;
-        } else if (!(ok = load(v_full, v_empty, L::kV, &map_v, vn, it, j - 1))) {
-          break;
+    PackedBlocks blocks(steal, steal_slot);
+    PackedItem it{}, following{};  // the first turn finds an item and loads nothing
+    for (bool begun = false;; it = following, begun = true) {
+      if (begun) {
+        const int b = n % kItems;
+        if (!(ok = warp_all(mbar_wait_short(it_empty + b, (uint32_t(n / kItems) & 1) ^ 1)))) break;
+        if (lane == 0) {
+          items[b] = it;
+          mbar_arrive(it_full + b);
         }
+        __syncwarp();
+        ++n;
+        if (it.tiles < 0) break;
+      }
+      // K_0, queries, K_1, V_0; the item after this one; K_2, V_1, ...: the first keys do not wait for the queries'
+      // place, which the last item's S products still read
+      const int loads = 2 * it.tiles, found_at = min(loads, 3);
+      for (int x = 0; x <= loads && ok; ++x) {
+        if (x == found_at && !(ok = blocks.next(p, wk, lane, following))) break;
+        if (x == loads) break;
+        // in turn K_0, then K_{j+1} and V_j, at last V
+        const bool is_v = x == loads - 1 || (x > 0 && (x & 1) == 0);
+        const int j = is_v ? (x == loads - 1 ? it.tiles - 1 : x / 2 - 1) : (x + 1) / 2;
+        if (!(ok = is_v ? load(v_full, v_empty, L::kV, &map_v, vn, it, j) : load(k_full, k_empty, L::kK, &map_k, kn, it, j))) break;
+        if (x > 0) continue;
+        if (!(ok = warp_all(mbar_wait_short(q_empty, (uint32_t(live) & 1) ^ 1)))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(q_full, uint32_t(p.rows * 128 * (D / 64)));
+#pragma unroll
+          for (int rg = 0; rg < D / 64; ++rg)
+            tma_load_3d(sbase + L::kQ + rg * kRegion, &map_q, rg * 64, it.hk * p.g, it.q0, smem_u32(q_full));
+        }
+        __syncwarp();
+        ++live;
       }
       if (!ok) break;
     }
@@ -191,12 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.tiles < 0) break;
       if (it.tiles == 0) continue;
       if (warp == 4) {
-        if (!(ok = warp_all(mbar_wait(q_full, uint32_t(live) & 1, st)))) break;
+        if (!(ok = warp_all(mbar_wait_short(q_full, uint32_t(live) & 1)))) break;
         const uint32_t qlo = desc_lo_kmajor(sbase + L::kQ);
         for (int j = 0; j < it.tiles; ++j, ++tile) {
           const int s = tile % S, b = tile & 1;
-          ok = warp_all(mbar_wait(k_full + s, uint32_t(tile / S) & 1, st) &&
-                        mbar_wait(s_free + b, (uint32_t(tile >> 1) & 1) ^ 1, st));
+          ok = warp_all(mbar_wait_short(k_full + s, uint32_t(tile / S) & 1) &&
+                        mbar_wait_short(s_free + b, (uint32_t(tile >> 1) & 1) ^ 1));
           if (!ok) break;
           tc_fence_after();
           issued = true;
@@ -216,14 +218,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool found = false;
         for (int j = 0; j < it.tiles; ++j, ++tile) {
           const int s = tile % S;
-          if (!(ok = warp_all(mbar_wait(v_full + s, uint32_t(tile / S) & 1, st)))) break;
+          if (!(ok = warp_all(mbar_wait_short(v_full + s, uint32_t(tile / S) & 1)))) break;
           if ((j + 1) * 128 > all_see) {
             found |= settle_v<D>(sbase + L::kV + s * L::kTile, max(0, all_see - j * 128), min(128, it.nkeys - j * 128), 0, lane);
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (j == 0) ok = warp_all(mbar_wait(o_free, (uint32_t(live) & 1) ^ 1, st));
-          if (ok) ok = warp_all(mbar_wait(p_full, uint32_t(tile) & 1, st));
+          if (j == 0) ok = warp_all(mbar_wait_short(o_free, (uint32_t(live) & 1) ^ 1));
+          if (ok) ok = warp_all(mbar_wait_short(p_full, uint32_t(tile) & 1));
           if (!ok) break;
           tc_fence_after();
           issued = true;
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < it.tiles; ++j, ++tile) {
         const int b = tile & 1;
-        if (!(ok = warp_all(mbar_wait(s_full + b, uint32_t(tile >> 1) & 1, st)))) break;
+        if (!(ok = warp_all(mbar_wait_short(s_full + b, uint32_t(tile >> 1) & 1)))) break;
         tc_fence_after();
         uint32_t pk[64];
         bool need = false;
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           mbar_arrive(s_free + b);
         }
-        if (!(ok = warp_all(mbar_wait(p_empty, (uint32_t(tile) & 1) ^ 1, st)))) break;  // the last tile's P V is done
+        if (!(ok = warp_all(mbar_wait_short(p_empty, (uint32_t(tile) & 1) ^ 1)))) break;  // the last tile's P V is done
         if (busy) {
           tc_fence_after();
           if (__any_sync(0xffffffffu, need && j > 0)) {
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (it.tiles > 0) {
-        if (!(ok = warp_all(mbar_wait(o_full, uint32_t(live) & 1, st)))) break;
+        if (!(ok = warp_all(mbar_wait_short(o_full, uint32_t(live) & 1)))) break;
         ++live;
         tc_fence_after();
       }
@@ -408,87 +410,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the chunks of a row: a warp per token and head. With M the largest of the chunks' maxima m_c,
+// Joins the chunks of a row: a block or more per token, a warp per head and turn. With M the largest of the chunks' maxima m_c,
 //   o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
 template <int D, typename T>
 __global__ void __launch_bounds__(256, 4) packed_join_kernel(const PackedParams p, const PackedWalk wk) {
   grid_inputs_ready();
   grid_let_next_start();
-  const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int tok = int(w / p.H), h = int(w - static_cast<long long>(tok) * p.H);
-  if (tok >= p.Tq) return;
+  const int lane = threadIdx.x & 31, tok = blockIdx.x;
   const int s = packed_find(p.q_start, p.S, wk.by_one, 0, tok, lane);
   int q0, nq, k0, nk;
   if (s < 0 || !packed_sequence(p, s, q0, nq, k0, nk) || tok < q0 || tok >= q0 + nq) return;
-  const int hk = p.by_group.div(h), hh = h - hk * p.g, i = tok - q0;
-  const int iq = wk.by_tq.div(i), last = min((iq + 1) * p.tq, nq);
+  const int i = tok - q0, iq = wk.by_tq.div(i), last = min((iq + 1) * p.tq, nq);
   const int seen = p.causal ? max(0, min(nk, last + nk - nq)) : nk;
   const int chunks = wk.by_chunk.div(seen + p.chunk - 1), slot = wk.by_chunk.div(k0) + s;
-  const long long row = (i - iq * p.tq) * p.g + hh;
-  auto at = [&](int c) { return ((static_cast<long long>(slot + c) * p.tiles + iq) * p.Hk + hk) * p.rows + row; };
-  constexpr int kE = D / 32;
-  float M = -INFINITY, l = 0.f, o[kE] = {};
-  for (int c0 = 0; c0 < chunks; c0 += 32) {
-    const float2 ml = c0 + lane < chunks ? p.part_ml[at(c0 + lane)] : make_float2(-INFINITY, 0.f);
-    float top = ml.x;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float Mn = fmaxf(M, top), keep = M == -INFINITY ? 0.f : exp2f(M - Mn);
-    // a chunk without a visible key has sum 0; one of NaN scores has maximum -inf but a sum that is NaN
-    // (and one far below M keeps the smallest weight, so that its infinities and NaN stay)
-    const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : fmaxf(exp2f(ml.x - Mn), FLT_MIN);
-    float sum = ml.y * f;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = l * keep + sum;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] *= keep;
-    const int n = min(32, chunks - c0);
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
-      const float fc = __shfl_sync(0xffffffffu, f, c);
-      const float* po = p.part_o + at(c0 + c) * D + lane * kE;
-      float v[kE];
-      if constexpr (kE == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(po);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(po);
-        v[0] = x.x, v[1] = x.y;
+  for (int h = blockIdx.y * 8 + (threadIdx.x >> 5); h < p.H; h += 8 * gridDim.y) {
+    const int hk = p.by_group.div(h), hh = h - hk * p.g;
+    const long long row = (i - iq * p.tq) * p.g + hh;
+    auto at = [&](int c) { return ((static_cast<long long>(slot + c) * p.tiles + iq) * p.Hk + hk) * p.rows + row; };
+    constexpr int kE = D / 32;
+    float M = -INFINITY, l = 0.f, o[kE] = {};
+    for (int c0 = 0; c0 < chunks; c0 += 32) {
+      const float2 ml = c0 + lane < chunks ? p.part_ml[at(c0 + lane)] : make_float2(-INFINITY, 0.f);
+      float top = ml.x;
+  #pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float Mn = fmaxf(M, top), keep = M == -INFINITY ? 0.f : exp2f(M - Mn);
+      // a chunk without a visible key has sum 0; one of NaN scores has maximum -inf but a sum that is NaN
+      // (and one far below M keeps the smallest weight, so that its infinities and NaN stay)
+      const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : fmaxf(exp2f(ml.x - Mn), FLT_MIN);
+      float sum = ml.y * f;
+  #pragma unroll
+      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l = l * keep + sum;
+  #pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] *= keep;
+      const int n = min(32, chunks - c0);
+  #pragma unroll 8
+      for (int c = 0; c < n; ++c) {
+        const float fc = __shfl_sync(0xffffffffu, f, c);
+        const float* po = p.part_o + at(c0 + c) * D + lane * kE;
+        float v[kE];
+        if constexpr (kE == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(po);
+          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(po);
+          v[0] = x.x, v[1] = x.y;
+        }
+        if (fc != 0.f) {
+  #pragma unroll
+          for (int e = 0; e < kE; ++e) o[e] = fmaf(fc, v[e], o[e]);
+        }
       }
-      if (fc != 0.f) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = fmaf(fc, v[e], o[e]);
-      }
+      M = Mn;
     }
-    M = Mn;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* orow = static_cast<T*>(p.o) + (static_cast<long long>(h) * p.os.head + static_cast<long long>(tok) * p.os.token) + lane * kE;
+  #pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+    if constexpr (sizeof(T) == 2) {
+      if constexpr (kE == 4) *reinterpret_cast<uint2*>(orow) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+      else *reinterpret_cast<uint32_t*>(orow) = pack_bf16x2(o[0], o[1]);
+    } else {
+      if constexpr (kE == 4) *reinterpret_cast<float4*>(orow) = make_float4(o[0], o[1], o[2], o[3]);
+      else *reinterpret_cast<float2*>(orow) = make_float2(o[0], o[1]);
+    }
+    if (p.lse != nullptr && lane == 0)
+      p.lse[static_cast<long long>(h) * p.Tq + tok] = l == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) * kLn2 + logf(l);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* orow = static_cast<T*>(p.o) + (static_cast<long long>(h) * p.os.head + static_cast<long long>(tok) * p.os.token) + lane * kE;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-  if constexpr (sizeof(T) == 2) {
-    if constexpr (kE == 4) *reinterpret_cast<uint2*>(orow) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-    else *reinterpret_cast<uint32_t*>(orow) = pack_bf16x2(o[0], o[1]);
-  } else {
-    if constexpr (kE == 4) *reinterpret_cast<float4*>(orow) = make_float4(o[0], o[1], o[2], o[3]);
-    else *reinterpret_cast<float2*>(orow) = make_float2(o[0], o[1]);
-  }
-  if (p.lse != nullptr && lane == 0)
-    p.lse[static_cast<long long>(h) * p.Tq + tok] = l == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) * kLn2 + logf(l);
 }
 
 template <int D>
-cudaError_t launch_tc(const PackedParams& p, int num_sms, cudaStream_t s) {
+cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   if (!(make_view_map(&mq, p.q, p.H, p.Tq, D, p.qs, p.g, p.tq) && make_view_map(&mk, p.k, p.Hk, p.Tk, D, p.ks, 1, 128) &&
         make_view_map(&mv, p.v, p.Hk, p.Tk, D, p.vs, 1, 128)))
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<packed_attn_kernel<D>>(Cfg<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  const int grid = p.items < num_sms ? int(p.items) : num_sms;
-  return launch_overlapped(packed_attn_kernel<D>, dim3(grid), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
+  return launch_overlapped(packed_attn_kernel<D>, dim3(unsigned(p.items)), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
 }
 
 }  // namespace
@@ -510,16 +510,14 @@ bool plan_packed(PackedParams* p, bool bf16) {
   p->chunk = 0;
   p->tiles = 1;
   const int piece = bf16 ? 128 : 64;
-  if (keys >= 4 * piece && tiles <= 64 && most * p->Hk < 8 * kSms) {
-    const long long work = most * keys * p->Hk;
-    long long chunk = (work / (8 * kSms) + piece - 1) / piece * piece;
+  if (keys >= 4 * piece && tiles <= 64 && (most * p->Hk < 2 * kSms || (tiles == 1 && most * p->Hk < 8 * kSms))) {
+    const long long work = most * keys * p->Hk, each = tiles == 1 ? 8 : 4;
+    long long chunk = (work / (each * kSms) + piece - 1) / piece * piece;
     if (chunk < 2 * piece) chunk = 2 * piece;
-    if (most * p->Hk < 2 * kSms || tiles == 1) {
-      p->chunk = int(chunk < (1 << 30) ? chunk : (1 << 30));
-      p->tiles = int(tiles);
-      slots = p->Tk / p->chunk + p->S;
-      p->by_tiles = Divisor(p->tiles);
-    }
+    p->chunk = int(chunk < (1 << 30) ? chunk : (1 << 30));
+    p->tiles = int(tiles);
+    slots = p->Tk / p->chunk + p->S;
+    p->by_tiles = Divisor(p->tiles);
   }
   p->pair = bf16 && p->chunk == 0 && p->max_q > p->tq;
   if (p->pair) {
@@ -539,16 +537,16 @@ size_t packed_workspace_bytes(const PackedParams& p) {
   return size_t(p.items) * p.rows * (size_t(p.d) * 4 + 8);
 }
 
-cudaError_t packed_attn_tc(const PackedParams& p, int num_sms, cudaStream_t s) {
+cudaError_t packed_attn_tc(const PackedParams& p, cudaStream_t s) {
   if (p.pair) return packed_attn_pair(p, s);
-  const cudaError_t e = p.d == 128 ? launch_tc<128>(p, num_sms, s) : launch_tc<64>(p, num_sms, s);
+  const cudaError_t e = p.d == 128 ? launch_tc<128>(p, s) : launch_tc<64>(p, s);
   return e != cudaSuccess || p.chunk == 0 ? e : packed_join(p, true, s);
 }
 
 cudaError_t packed_join(const PackedParams& p, bool bf16, cudaStream_t s) {
-  const long long blocks = (static_cast<long long>(p.Tq) * p.H + 7) / 8;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  auto go = [&](auto kern) { return launch_overlapped(kern, dim3(unsigned(blocks)), 256, 0, s, 0, p, walk_of(p)); };
+  // as many blocks a token as fill the GPU twice, a turn of eight heads each at least
+  const int turns = (p.H + 7) / 8, want = (2 * 152 + p.Tq - 1) / p.Tq, each = want < turns ? want : turns;
+  auto go = [&](auto kern) { return launch_overlapped(kern, dim3(unsigned(p.Tq), unsigned(each)), 256, 0, s, 0, p, walk_of(p)); };
   if (bf16) return p.d == 128 ? go(packed_join_kernel<128, __nv_bfloat16>) : go(packed_join_kernel<64, __nv_bfloat16>);
   return p.d == 128 ? go(packed_join_kernel<128, float>) : go(packed_join_kernel<64, float>);
 }

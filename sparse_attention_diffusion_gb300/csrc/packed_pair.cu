@@ -144,41 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++cnt;
         return true;
       };
-      // The next item that has something to do (tiles -1: none is left): this block's own, then those of blocks that have
-      // not started yet, which it asks the hardware for, one request ahead.
-      int steals = 0;
-      bool own = true;
-      auto ask = [&]() {
-        if (elect_one()) {
-          mbar_arrive_expect_tx(steal, 16);
-          steal_block(steal_slot, steal);
-        }
-        __syncwarp();
-      };
-      ask();
-      auto next = [&](PackedItem& it) -> bool {
-        while (true) {
-          int i = int(blockIdx.x);
-          if (!own) {
-            if (!warp_all(mbar_wait_short(steal, uint32_t(steals++) & 1))) return false;
-            i = stolen_block(steal_slot);
-            if (i < 0) {
-              it.tiles = -1;
-              return true;
-            }
-            fence_proxy_async_smem();  // the answer has been read; the next one may overwrite it
-            __syncwarp();
-            ask();
-          }
-          own = false;
-          if (const long long s = static_cast<long long>(i) * 32 + lane; s < p.S) {  // there are more items than sequences
-            int a, b, c, d;
-            if (!packed_sequence(p, int(s), a, b, c, d)) raise_status(st, kStatusBounds);
-          }
-          __syncwarp();
-          if (packed_item(p, wk.by_tq, wk.by_chunk, i, lane, &it)) return true;
-        }
-      };
+      PackedBlocks blocks(steal, steal_slot);
       PackedItem it{}, following{};  // the first turn finds an item and loads nothing
       for (bool begun = false;; it = following, begun = true) {
         if (begun) {
@@ -211,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (!ok) break;
-          if (!(ok = next(following))) break;
+          if (!(ok = blocks.next(p, wk, lane, following))) break;
         }
         if (!ok) break;
       }

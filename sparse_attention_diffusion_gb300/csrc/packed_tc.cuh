@@ -70,6 +70,46 @@ __device__ __forceinline__ void mask_scores(uint32_t tS, int nvalid) {
   }
 }
 
+// The items of one block: its own, then those of blocks that have not started yet, which it asks the hardware for, one
+// request ahead. One warp; `bar` has a count of one, `slot` is 16 aligned bytes of shared memory.
+struct PackedBlocks {
+  uint64_t* bar;
+  uint32_t slot, answers = 0;
+  bool own = true;
+  __device__ __forceinline__ PackedBlocks(uint64_t* b, uint32_t s) : bar(b), slot(s) { ask(); }
+  __device__ __forceinline__ void ask() {
+    if (elect_one()) {
+      mbar_arrive_expect_tx(bar, 16);
+      steal_block(slot, bar);
+    }
+    __syncwarp();
+  }
+  // The next item that has something to do (tiles -1: none is left). False if a wait ran out.
+  __device__ __forceinline__ bool next(const PackedParams& p, const PackedWalk& wk, int lane, PackedItem& it) {
+    while (true) {
+      int i = int(blockIdx.x);
+      if (!own) {
+        if (!warp_all(mbar_wait_short(bar, answers++ & 1))) return false;
+        i = stolen_block(slot);
+        if (i < 0) {
+          it.tiles = -1;
+          return true;
+        }
+        fence_proxy_async_smem();  // the answer has been read; the next one may overwrite it
+        __syncwarp();
+        ask();
+      }
+      own = false;
+      if (const long long s = static_cast<long long>(i) * 32 + lane; s < p.S) {  // there are more items than sequences
+        int a, b, c, d;
+        if (!packed_sequence(p, int(s), a, b, c, d)) raise_status(p.status, kStatusBounds);
+      }
+      __syncwarp();
+      if (packed_item(p, wk.by_tq, wk.by_chunk, i, lane, &it)) return true;
+    }
+  }
+};
+
 // Tiled map over a [heads, tokens, d] bf16 view, box = 64 columns x box_heads x box_tokens, 128-byte swizzle.
 bool make_view_map(CUtensorMap* m, const void* base, int heads, int tokens, int d, const PackedStrides& s, int box_heads, int box_tokens) {
   auto enc = tensor_map_encoder();
