@@ -435,8 +435,8 @@ mcs_status mcs_packed_attn(const mcs_packed_desc *desc, const void *q, const mcs
  * MCS_ERR_DEVICE_BOUNDS.
  * The inner sums h = scale[a] * x down_a^T are fp32 and kept as two bf16 parts (BF16: to 2^-17, the
  * tensor core's truncation moves a sum by less than in / 16 * 5.25 * 2^-23 of sum |x down|) or
- * as they are (F32). BF16: an adapter whose `up` holds an infinity or a NaN makes all outputs of its
- * own rows NaN; F32: what the sums give. No row depends on another segment's adapter.
+ * as they are (F32). BF16: an adapter whose `up` holds an infinity or a NaN may make all outputs of
+ * its own rows NaN; F32: what the sums give. No row depends on another segment's adapter.
  * ws: at least mcs_linear_adapters_workspace_size(desc, adapters) bytes (0 for an invalid
  * description; host only); its contents on entry are ignored; calls that may run at the
  * same time need one each. Equal calls give equal bits. */

@@ -66,20 +66,32 @@ struct AdapterView {
   RowTiles tiles;
   Divisor by_one;
 };
-template <bool kAdapt>
+// How a product takes its adapters: as more k steps from the slabs, or, where few rows share one, on the CUDA cores while
+// the sums leave, from h as it is: h [M][R] and every row's adapter (negative: none) lie in the workspace then.
+enum { kNoAdapters = 0, kAdapterSteps = 1, kAdapterRows = 2 };
+template <int kAdapt>
 struct AdapterArgs {};
 template <>
-struct AdapterArgs<true> {
+struct AdapterArgs<kAdapterSteps> {
   CUtensorMap h;      // slabs [2 slot + part][height][R]
   CUtensorMap mask;   // [slot][height][8]: NaN in the segment's rows
   CUtensorMap up;     // [count][O][R]
   AdapterView v;
 };
+template <>
+struct AdapterArgs<kAdapterRows> {
+  const float* h;         // [M][R]
+  const int32_t* of_row;  // [M]
+  const __nv_bfloat16* up;
+  int R;
+};
 
 size_t adapters_workspace_bytes(const LinearParams& p, const AdapterParams& a, bool bf16);
 // First step, bf16: slabs for `t`'s tiles; fills the view and the maps (boxes of `box` slab rows and `wbox` rows of up).
 cudaError_t adapters_down_tc(const LinearParams& p, const AdapterParams& a, const RowTiles& t, int box, int wbox, int num_sms,
-                             AdapterArgs<true>* args, cudaStream_t s);
+                             AdapterArgs<kAdapterSteps>* args, cudaStream_t s);
+// First step with rows of their own: h and every row's adapter (of_row may be null).
+cudaError_t adapters_down_rows(const LinearParams& p, const AdapterParams& a, bool bf16, float* h, int32_t* of_row, cudaStream_t s);
 cudaError_t linear_adapters_tc(const LinearParams& p, const AdapterParams& a, int num_sms, cudaStream_t s);
 cudaError_t linear_adapters_f32(const LinearParams& p, const AdapterParams& a, int num_sms, cudaStream_t s);
 

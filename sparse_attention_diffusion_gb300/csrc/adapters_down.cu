@@ -285,8 +285,8 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
-// bf16: slabs, masks and the bytes of `up`'s shares, for row tiles of any height up to 256. fp32: h and the adapters'
-// part of the sums.
+// bf16: slabs, masks and the bytes of `up`'s shares, for row tiles of any height up to 256 (h and the rows' adapters are
+// smaller). fp32: h and the adapters' part of the sums.
 size_t adapters_workspace_bytes(const LinearParams& p, const AdapterParams& a, bool bf16) {
   if (!bf16) return align256(size_t(p.M) * a.R * 4) + align256(size_t(p.M) * p.O * 4);
   const size_t sections = p.heads > 0 ? p.B : 1;
@@ -295,7 +295,7 @@ size_t adapters_workspace_bytes(const LinearParams& p, const AdapterParams& a, b
 }
 
 cudaError_t adapters_down_tc(const LinearParams& p, const AdapterParams& a, const RowTiles& t, int box, int wbox, int num_sms,
-                             AdapterArgs<true>* args, cudaStream_t s) {
+                             AdapterArgs<kAdapterSteps>* args, cudaStream_t s) {
   DownArgs d{};
   const size_t slots = size_t(t.tiles) * t.sections + a.S, rows = slots * t.height;
   d.halves = (t.height + 127) / 128;

@@ -10,79 +10,6 @@
 namespace mcs {
 namespace {
 
-// h: a block takes 4 rows and 8 columns, its four warps a quarter of K each, lanes along K; rows of several
-// segments are worked off one segment after another.
-constexpr int kRows = 4, kCols = 8, kWarps = 4;
-__global__ void __launch_bounds__(32 * kWarps) adapters_f32_down_kernel(const LinearParams p, const AdapterParams a, float* h) {
-  __shared__ float part[kWarps][kRows * kCols];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long m0 = static_cast<long long>(blockIdx.x) * kRows;
-  const int c0 = blockIdx.y * kCols;
-  grid_inputs_ready();
-  grid_let_next_start();
-  if (blockIdx.y == 0 && warp == 0) {
-    for (long long s = static_cast<long long>(blockIdx.x) * 32 + lane; s < a.S; s += static_cast<long long>(gridDim.x) * 32) {
-      int x, y;
-      if (!segment_rows(a.start, int(s), p.M, x, y) || a.which[s] >= a.count) raise_status(p.status, kStatusBounds);
-    }
-    __syncwarp();
-  }
-  const int m1 = int(min(static_cast<long long>(p.M), m0 + kRows));
-  const float* x[kRows];  // row m's columns, by head if they lie so
-  const int hd = p.heads > 0 ? p.K / p.heads : p.K;
-  const long long head = static_cast<long long>(p.N) * hd;  // from one head's column to the next head's
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int m = min(int(m0) + r, p.M - 1), b = m / p.N;
-    x[r] = static_cast<const float*>(p.x) + (p.heads > 0 ? b * p.heads * head + static_cast<long long>(m - b * p.N) * hd
-                                                         : static_cast<long long>(m) * p.K);
-  }
-  for (int s = max(0, segment_at(a.start, a.S, int(m0), lane)); s < a.S; ++s) {
-    if (a.start[s] >= m1) break;
-    int ra, rb;
-    segment_rows(a.start, s, p.M, ra, rb);
-    const int lo = max(ra, int(m0)), hi = min(rb, m1);
-    if (lo >= hi) continue;
-    const int ad = a.which[s];
-    if (ad < 0 || ad >= a.count) continue;
-    const float* down = static_cast<const float*>(a.down) + static_cast<size_t>(ad) * a.R * p.K;
-    uint64_t sum[kRows][kCols] = {};
-    for (int k = (warp * 32 + lane) * 4; k < p.K; k += 128 * kWarps) {
-      const int q = k / hd;
-      ulonglong2 xv[kRows];
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) xv[r] = *reinterpret_cast<const ulonglong2*>(x[r] + (p.heads > 0 ? q * head + (k - q * hd) : k));
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        if (c0 + c >= a.R) break;
-        const ulonglong2 dv = *reinterpret_cast<const ulonglong2*>(down + static_cast<size_t>(c0 + c) * p.K + k);
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) sum[r][c] = f2_fma(xv[r].y, dv.y, f2_fma(xv[r].x, dv.x, sum[r][c]));
-      }
-    }
-    __syncthreads();  // the last segment's sums have been read
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        float e, o;
-        f2_unpack(sum[r][c], e, o);
-        e += o;
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) e += __shfl_xor_sync(0xffffffffu, e, w);
-        if (lane == 0) part[warp][r * kCols + c] = e;
-      }
-    __syncthreads();
-    if (warp == 0) {
-      const int r = lane / kCols, c = lane % kCols, m = int(m0) + r;
-      float e = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) e += part[w][lane];
-      if (m >= lo && m < hi && c0 + c < a.R) h[static_cast<size_t>(m) * a.R + c0 + c] = a.scale[ad] * e;
-    }
-  }
-}
-
 // z = h up_a^T, 0 in rows without an adapter: 64 x 64 outputs a block, 4 x 4 a thread, 16 columns of R at a time.
 constexpr int kTile = 64, kStep = 16, kLd = kStep + 4;
 __global__ void __launch_bounds__(256) adapters_f32_up_kernel(const LinearParams p, const AdapterParams a, const float* h, float* z) {
@@ -149,9 +76,8 @@ __global__ void __launch_bounds__(256) adapters_f32_up_kernel(const LinearParams
 cudaError_t linear_adapters_f32(const LinearParams& p, const AdapterParams& a, int num_sms, cudaStream_t s) {
   float* h = static_cast<float*>(a.ws);
   float* z = h + (size_t(p.M) * a.R + 63) / 64 * 64;
-  const dim3 down((unsigned(p.M) + kRows - 1) / kRows, (a.R + kCols - 1) / kCols);
   const dim3 up((unsigned(p.M) + kTile - 1) / kTile, (p.O + kTile - 1) / kTile);
-  cudaError_t e = launch_overlapped(adapters_f32_down_kernel, down, 32 * kWarps, 0, s, 0, p, a, h);
+  cudaError_t e = adapters_down_rows(p, a, false, h, nullptr, s);
   if (e == cudaSuccess) e = launch_overlapped(adapters_f32_up_kernel, up, 256, 0, s, 0, p, a, h, z);
   if (e != cudaSuccess) return e;
   LinearParams with = p;

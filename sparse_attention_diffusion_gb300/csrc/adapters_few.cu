@@ -5,10 +5,15 @@ namespace mcs {
 
 cudaError_t linear_adapters_pair(const LinearParams& p, int bn, const AdapterParams& a, int num_sms, cudaStream_t s);
 
+// Few rows: a segment's k steps cost some 400 clocks for 64 columns of either part of h, whatever its rows; on the CUDA
+// cores a row costs its block 128 x R elements of `up` (4 R clocks at what an SM reads from L2). So segments of less
+// than 800 / 4 R rows on average go there.
 cudaError_t linear_adapters_tc(const LinearParams& p, const AdapterParams& a, int num_sms, cudaStream_t s) {
   const LinearPlan plan = plan_linear_tc(p, num_sms);
-  return plan.kernel == MCS_LINEAR_FEW ? launch_few<true>(p, {plan.tile, plan.slices}, &a, num_sms, s)
-                                       : linear_adapters_pair(p, plan.tile, a, num_sms, s);
+  if (plan.kernel != MCS_LINEAR_FEW) return linear_adapters_pair(p, plan.tile, a, num_sms, s);
+  const bool rows = static_cast<long long>(p.M) * a.R <= 200ll * ((a.R + 63) / 64) * a.S;
+  return rows ? launch_few<kAdapterRows>(p, {plan.tile, plan.slices}, &a, num_sms, s)
+              : launch_few<kAdapterSteps>(p, {plan.tile, plan.slices}, &a, num_sms, s);
 }
 
 }  // namespace mcs

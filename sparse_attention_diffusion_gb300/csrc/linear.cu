@@ -66,7 +66,7 @@ LinearPlan plan_linear_tc(const LinearParams& p, int num_sms) {
 cudaError_t linear_tc(const LinearParams& p, int num_sms, cudaStream_t s) {
   const LinearPlan plan = plan_linear_tc(p, num_sms);
   return plan.kernel == MCS_LINEAR_FEW ? linear_few(p, {plan.tile, plan.slices}, num_sms, s)
-                                       : launch_pair<false>(p, plan.tile, nullptr, num_sms, s);
+                                       : launch_pair<kNoAdapters>(p, plan.tile, nullptr, num_sms, s);
 }
 
 }  // namespace mcs

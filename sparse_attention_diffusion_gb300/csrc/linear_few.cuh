@@ -32,8 +32,8 @@ namespace {
 constexpr int kThreads = 192, kWarps = kThreads / 32;
 constexpr int kWTile = 128 * 128;  // bytes of 128 rows of w x 64 columns
 // barriers, the tensor-memory slot and with adapters a word a stage, after the ring
-template <bool kAdapt>
-constexpr int kBarBytes = kAdapt ? 320 : 256;
+template <int kAdapt>
+constexpr int kBarBytes = kAdapt == kAdapterSteps ? 320 : 256;
 constexpr int kMaxStages = 12;
 
 struct FewArgs {
@@ -52,10 +52,32 @@ __device__ __forceinline__ uint32_t peer_word(uint32_t addr, int r, int splits) 
   return v;
 }
 
+// Adds a row's adapter to four of its sums: 16 bytes of `up` a load, a warp's lanes along the outputs.
+__device__ __forceinline__ void add_adapter(const AdapterArgs<kAdapterRows>& ad, const LinearParams& p, int m, int o, float (&v)[4]) {
+  const int a = ad.of_row[m];
+  if (a < 0) return;
+  const float4* h = reinterpret_cast<const float4*>(ad.h + size_t(m) * ad.R);
+  const __nv_bfloat16* up = ad.up + (size_t(a) * p.O + o) * ad.R;
+#pragma unroll 2
+  for (int r = 0; r < ad.R; r += 8) {
+    const float4 x = h[r / 4], y = h[r / 4 + 1];
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = o + i < p.O ? __ldg(reinterpret_cast<const uint4*>(up + size_t(i) * ad.R + r)) : uint4{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float u[8];
+      unpack8(w[i], u);
+      v[i] = fmaf(x.x, u[0], fmaf(x.y, u[1], fmaf(x.z, u[2], fmaf(x.w, u[3], v[i]))));
+      v[i] = fmaf(y.x, u[4], fmaf(y.y, u[5], fmaf(y.z, u[6], fmaf(y.w, u[7], v[i]))));
+    }
+  }
+}
+
 // This CTA's share of the outputs: tokens rank, rank + splits, ... over its warps,
 // kTok of them and kRanks partial accumulators at a time, ranks added in order.
-template <int kAct, int kTok, int kRanks>
-__device__ __forceinline__ void final_sums(const LinearParams& p, const FewArgs& a, uint32_t sbase, int rank, int warp,
+template <int kAct, int kTok, int kRanks, int kAdapt>
+__device__ __forceinline__ void final_sums(const LinearParams& p, const FewArgs& a, const AdapterArgs<kAdapt>& ad, uint32_t sbase, int rank, int warp,
                                            int lane, int m0, int ntok, int o0) {
   const int o = o0 + lane * 4;
   const bool vec = p.O % 4 == 0;
@@ -89,6 +111,11 @@ __device__ __forceinline__ void final_sums(const LinearParams& p, const FewArgs&
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[t][i] += f[t][r][i];
     }
+    if constexpr (kAdapt == kAdapterRows) {
+#pragma unroll
+      for (int t = 0; t < kTok; ++t)
+        if (c0 + t * stride < ntok) add_adapter(ad, p, m0 + c0 + t * stride, o, v[t]);
+    }
 #pragma unroll
     for (int t = 0; t < kTok; ++t) {
       const int c = c0 + t * stride;
@@ -105,9 +132,11 @@ __device__ __forceinline__ void final_sums(const LinearParams& p, const FewArgs&
 }
 
 // kTurns: two accumulators take turns and their sums are kept in registers; otherwise all stay until the end.
-// kAdapt: the segments of a tile with an adapter add their k steps, shared among the slices, after those of w,
-// into a slice's last accumulator (adapters.h).
-template <int kAct, bool kTurns, bool kAdapt>
+// kAdapt: with kAdapterSteps the segments of a tile with an adapter add their k steps, shared among the slices, after
+// those of w, into a slice's last accumulator (adapters.h); with kAdapterRows a row's adapter is added to its sums on
+// their way out, and only that waits for the kernel before, which makes h: that one has waited for what it follows
+// itself, so x and w are there.
+template <int kAct, bool kTurns, int kAdapt>
 __global__ void __launch_bounds__(kThreads, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ AdapterArgs<kAdapt> ad, const LinearParams p, const FewArgs a) {
@@ -151,8 +180,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
-  grid_inputs_ready();
-  grid_let_next_start();
+  if constexpr (kAdapt != kAdapterRows) {
+    grid_inputs_ready();
+    grid_let_next_start();
+  }
 
   bool ok = true;
   if (warp == 0) {
@@ -163,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!(ok = warp_all(mbar_wait(empty + s, phase ^ 1, st)))) return;
       const uint32_t dst = sbase + s * stage_bytes;
       if (elect_one()) {
-        if (kAdapt) stage_info[s] = info;
+        if (kAdapt == kAdapterSteps) stage_info[s] = info;
         mbar_arrive_expect_tx(full + s, stage_bytes);
         tma_load_3d(dst, mw, cw, o0, zw, smem_u32(full + s));
         tma_load_3d(dst + kWTile, mx, cx, rx, zx, smem_u32(full + s));
@@ -171,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       if (++s == a.stages) s = 0, phase ^= 1;
     };
-    if constexpr (kAdapt) {
+    if constexpr (kAdapt == kAdapterSteps) {
       const int row0 = ad.v.tiles.first(tt), row1 = ad.v.tiles.end(tt), chunks = (ad.v.R + 63) / 64;
       int steps = 0;  // of all slices
       for_segments(ad.v, row0, row1, lane, [&](int, int, bool odd) { steps += odd ? 1 : 2 * chunks; });
@@ -210,21 +241,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     int s = 0;
     uint32_t phase = 0;
     int step = 0, c = 0;  // k steps in the accumulator c
-    for (int i = k_beg; kAdapt || i < k_end; ++i) {
-      const bool extra = kAdapt && i >= k_end;  // into the accumulator that is there
+    constexpr bool kSteps = kAdapt == kAdapterSteps;
+    for (int i = k_beg; kSteps || i < k_end; ++i) {
+      const bool extra = kSteps && i >= k_end;  // into the accumulator that is there
       const int b = kTurns ? c & 1 : c;
       if (kTurns && step == 0 && !extra && !(ok = warp_all(mbar_wait(acc_empty + b, ((c >> 1) & 1) ^ 1, st)))) break;
       if (!(ok = warp_all(mbar_wait(full + s, phase, st)))) break;
       tc_fence_after();
       issued = true;
-      const uint32_t info = kAdapt ? warp_uniform(stage_info[s]) : 4u;
-      const bool last = kAdapt ? (info & 8) != 0 : i == k_end - 1;
+      const uint32_t info = kSteps ? warp_uniform(stage_info[s]) : 4u;
+      const bool last = kSteps ? (info & 8) != 0 : i == k_end - 1;
       const uint32_t w = desc_lo_kmajor(sbase + s * stage_bytes);
       const uint32_t x = desc_lo_kmajor(sbase + s * stage_bytes + kWTile);
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          if (!kAdapt || ks < int(info & 7))
+          if (!kSteps || ks < int(info & 7))
             tc_mma_ss_lo(tmem + b * a.acc_cols, w + kstep_kmajor(ks), x + kstep_kmajor(ks), idesc,
                          (step > 0 || ks > 0 || extra) ? 1u : 0u);
         tc_commit(empty + s);
@@ -314,26 +346,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     tmem_dealloc(tmem, a.tmem_cols);
   }
+  if constexpr (kAdapt == kAdapterRows) {
+    grid_inputs_ready();
+    grid_let_next_start();
+  }
   // sums with a failed CTA's share are not written anywhere
   ok = true;
   for (int r = 0; r < a.splits; ++r) ok = ok && peer_word(smem_u32(tmem_slot + 1), r, a.splits) == 0;
   const int ntok = min(a.bn, a.rows - tok0);
   // several reads in flight: a remote one takes several hundred clocks
   if (ok) {
-    if (a.splits == 1) final_sums<kAct, 4, 1>(p, a, sbase, rank, warp, lane, sec * a.rows + tok0, ntok, o0);
-    else final_sums<kAct, 2, 4>(p, a, sbase, rank, warp, lane, sec * a.rows + tok0, ntok, o0);
+    if (a.splits == 1) final_sums<kAct, 4, 1>(p, a, ad, sbase, rank, warp, lane, sec * a.rows + tok0, ntok, o0);
+    else final_sums<kAct, 2, 4>(p, a, ad, sbase, rank, warp, lane, sec * a.rows + tok0, ntok, o0);
   }
   if (a.splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
 }
 
-template <int kAct, bool kTurns, bool kAdapt>
+template <int kAct, bool kTurns, int kAdapt>
 cudaError_t start_few_act(const CUtensorMap& mx, const CUtensorMap& mw, const AdapterArgs<kAdapt>& ad, const LinearParams& p,
                       const FewArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
   const cudaError_t e = allow_smem<linear_few_kernel<kAct, kTurns, kAdapt>>(226 * 1024);
   if (e != cudaSuccess) return e;
   return launch_overlapped(linear_few_kernel<kAct, kTurns, kAdapt>, grid, kThreads, smem, s, unsigned(a.splits), mx, mw, ad, p, a);
 }
-template <bool kTurns, bool kAdapt>
+template <bool kTurns, int kAdapt>
 cudaError_t start_few(const CUtensorMap& mx, const CUtensorMap& mw, const AdapterArgs<kAdapt>& ad, const LinearParams& p,
                       const FewArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
   switch (p.act) {
@@ -346,7 +382,7 @@ cudaError_t start_few(const CUtensorMap& mx, const CUtensorMap& mw, const Adapte
 
 
 // adapters: null without adapters.
-template <bool kAdapt>
+template <int kAdapt>
 cudaError_t launch_few(const LinearParams& p, const FewPlan& plan, const AdapterParams* adapters, int num_sms, cudaStream_t s) {
   FewArgs a{};
   CUtensorMap mx, mw;
@@ -384,9 +420,16 @@ cudaError_t launch_few(const LinearParams& p, const FewPlan& plan, const Adapter
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const size_t smem = size_t(a.stages) * stage + kBarBytes<kAdapt> + 1024;
   AdapterArgs<kAdapt> ad{};
-  if constexpr (kAdapt) {
+  if constexpr (kAdapt == kAdapterSteps) {
     const cudaError_t e = adapters_down_tc(p, *adapters, RowTiles(a.rows, a.sections, a.bn), a.bn, 128, num_sms, &ad, s);
     if (e != cudaSuccess) return e;
+  }
+  if constexpr (kAdapt == kAdapterRows) {
+    float* h = static_cast<float*>(adapters->ws);
+    int32_t* of_row = reinterpret_cast<int32_t*>(h + size_t(p.M) * adapters->R);
+    const cudaError_t e = adapters_down_rows(p, *adapters, true, h, of_row, s);
+    if (e != cudaSuccess) return e;
+    ad = {h, of_row, static_cast<const __nv_bfloat16*>(adapters->up), adapters->R};
   }
   const dim3 grid(unsigned(a.splits) * a.tiles * a.sections, (p.O + 127) / 128);
   return few_turns(a.bn, steps) ? start_few<true>(mx, mw, ad, p, a, grid, smem, s)

@@ -200,7 +200,7 @@ __device__ __forceinline__ void store_odd(const LinearParams& p, int rows, int s
 // kAdapt: the segments of a tile with an adapter add their k steps after those of w, into the row's last accumulator
 // (adapters.h); the producers leave a word a stage that says how many 16-column products it takes and whether it is
 // the tile's last.
-template <int kAct, int kPieces, bool kBack, bool kAdapt>
+template <int kAct, int kPieces, bool kBack, int kAdapt>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_r,
@@ -534,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int kAct, bool kAdapt>
+template <int kAct, int kAdapt>
 cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& my, const CUtensorMap& mr,
                        const AdapterArgs<kAdapt>& ad, const LinearParams& p, const Tiling& t, int pairs, cudaStream_t s) {
   auto start = [&](auto kern, cudaError_t e) {
@@ -551,7 +551,7 @@ cudaError_t start_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUten
 }
 
 // adapters: null without adapters.
-template <bool kAdapt>
+template <int kAdapt>
 cudaError_t launch_pair(const LinearParams& p, int bn, const AdapterParams* adapters, int num_sms, cudaStream_t s) {
   Tiling t{};
   CUtensorMap mx, mw, my{}, mr{};
