@@ -11,7 +11,7 @@
 namespace mcs {
 namespace {
 
-constexpr int kCols = 8, kWarps = 4;
+constexpr int kCols = 8;
 
 // Elements of a 16-byte load as packed fp32 pairs.
 template <typename T>
@@ -29,9 +29,9 @@ __device__ __forceinline__ Pairs<__nv_bfloat16> pairs16(const __nv_bfloat16* p) 
   return {{f2_pack(f[0], f[1]), f2_pack(f[2], f[3]), f2_pack(f[4], f[5]), f2_pack(f[6], f[7])}};
 }
 
-// A block takes kRows rows and 8 columns of h, its four warps a quarter of K each, lanes along K; rows of several
+// A block takes kRows rows and 8 columns of h, its warps a share of K each, lanes along K; rows of several
 // segments are worked off one segment after another.
-template <typename T, int kRows>
+template <typename T, int kRows, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) adapters_rows_kernel(const LinearParams p, const AdapterParams a, float* h, int32_t* of_row) {
   __shared__ float part[kWarps][kRows * kCols];
   constexpr int kV = 16 / sizeof(T);
@@ -76,9 +76,8 @@ __global__ void __launch_bounds__(32 * kWarps) adapters_rows_kernel(const Linear
 #pragma unroll
       for (int r = 0; r < kRows; ++r) xv[r] = pairs16(x[r] + (q * head + (k - q * hd)));
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        if (c0 + c >= a.R) break;
-        const Pairs<T> dv = pairs16(down + static_cast<size_t>(c0 + c) * p.K + k);
+      for (int c = 0; c < kCols; ++c) {  // columns past the last are not written
+        const Pairs<T> dv = pairs16(down + static_cast<size_t>(min(c0 + c, a.R - 1)) * p.K + k);
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
 #pragma unroll
@@ -112,14 +111,14 @@ __global__ void __launch_bounds__(32 * kWarps) adapters_rows_kernel(const Linear
 }  // namespace
 
 cudaError_t adapters_down_rows(const LinearParams& p, const AdapterParams& a, bool bf16, float* h, int32_t* of_row, cudaStream_t s) {
-  auto go = [&](auto kern, int rows) {
+  auto go = [&](auto kern, int rows, int warps) {
     const dim3 grid((unsigned(p.M) + rows - 1) / rows, (a.R + kCols - 1) / kCols);
-    return launch_overlapped(kern, grid, 32 * kWarps, 0, s, 0, p, a, h, of_row);
+    return launch_overlapped(kern, grid, 32 * warps, 0, s, 0, p, a, h, of_row);
   };
   // a row a block where no two rows share a segment to speak of
   const bool single = p.M <= 2ll * a.S;
-  if (bf16) return single ? go(adapters_rows_kernel<__nv_bfloat16, 1>, 1) : go(adapters_rows_kernel<__nv_bfloat16, 4>, 4);
-  return single ? go(adapters_rows_kernel<float, 1>, 1) : go(adapters_rows_kernel<float, 4>, 4);
+  if (bf16) return single ? go(adapters_rows_kernel<__nv_bfloat16, 1, 8>, 1, 8) : go(adapters_rows_kernel<__nv_bfloat16, 4, 4>, 4, 4);
+  return single ? go(adapters_rows_kernel<float, 1, 8>, 1, 8) : go(adapters_rows_kernel<float, 4, 4>, 4, 4);
 }
 
 }  // namespace mcs

@@ -134,7 +134,7 @@ __device__ __forceinline__ void final_sums(const LinearParams& p, const FewArgs&
 // kTurns: two accumulators take turns and their sums are kept in registers; otherwise all stay until the end.
 // kAdapt: with kAdapterSteps the segments of a tile with an adapter add their k steps, shared among the slices, after
 // those of w, into a slice's last accumulator (adapters.h); with kAdapterRows a row's adapter is added to its sums on
-// their way out, and only that waits for the kernel before, which makes h: that one has waited for what it follows
+// their way out. Only what reads h waits for the kernel before, which makes it: that one has waited for what it follows
 // itself, so x and w are there.
 template <int kAct, bool kTurns, int kAdapt>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
-  if constexpr (kAdapt != kAdapterRows) {
+  if constexpr (kAdapt == kNoAdapters) {
     grid_inputs_ready();
     grid_let_next_start();
   }
@@ -204,12 +204,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     if constexpr (kAdapt == kAdapterSteps) {
       const int row0 = ad.v.tiles.first(tt), row1 = ad.v.tiles.end(tt), chunks = (ad.v.R + 63) / 64;
+      for (int i = k_beg; i < k_end - 1 && ok; ++i) {  // the last one when it is known whether more follow
+        const int k = i * 64;
+        load(&map_w, k, 0, &map_x, k & a.col_mask, tok0, z0 + (k >> a.head_shift), 4);
+      }
+      grid_inputs_ready();
+      grid_let_next_start();
       int steps = 0;  // of all slices
       for_segments(ad.v, row0, row1, lane, [&](int, int, bool odd) { steps += odd ? 1 : 2 * chunks; });
       const int beg = int(static_cast<long long>(steps) * rank / a.splits), end = int(static_cast<long long>(steps) * (rank + 1) / a.splits);
-      for (int i = k_beg; i < k_end && ok; ++i) {
-        const int k = i * 64;
-        load(&map_w, k, 0, &map_x, k & a.col_mask, tok0, z0 + (k >> a.head_shift), 4 | (beg == end && i == k_end - 1 ? 8 : 0));
+      if (ok) {
+        const int k = (k_end - 1) * 64;
+        load(&map_w, k, 0, &map_x, k & a.col_mask, tok0, z0 + (k >> a.head_shift), 4 | (beg == end ? 8 : 0));
       }
       int n = 0;
       for_segments(ad.v, row0, row1, lane, [&](int seg, int which, bool odd) {
@@ -281,6 +287,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
   } else {
+    if constexpr (kAdapt == kAdapterRows) {  // the rows' adapters come to the L2 cache while the products run
+      grid_inputs_ready();
+      const int live = min(128, p.O - o0), lines = (live * ad.R * 2 + 127) / 128;
+      for (int c = rank + a.splits * (warp - 2); c < min(a.bn, a.rows - tok0); c += 4 * a.splits) {
+        const int which = ad.of_row[sec * a.rows + tok0 + c];
+        if (which < 0) continue;
+        const char* up = reinterpret_cast<const char*>(ad.up + (size_t(which) * p.O + o0) * ad.R);
+        for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(up + min(i * 128, live * ad.R * 2 - 1)));
+      }
+      __syncwarp();
+    }
     const int quarter = warp & 3;
     const uint32_t acc = tmem + (uint32_t(quarter * 32) << 16);
     float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;

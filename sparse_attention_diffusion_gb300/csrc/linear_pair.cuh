@@ -199,7 +199,8 @@ __device__ __forceinline__ void store_odd(const LinearParams& p, int rows, int s
 // 2.33).
 // kAdapt: the segments of a tile with an adapter add their k steps after those of w, into the row's last accumulator
 // (adapters.h); the producers leave a word a stage that says how many 16-column products it takes and whether it is
-// the tile's last.
+// the tile's last. Only they wait for the kernel before, which makes the slabs, and only when they come to them: that one
+// has waited for what it follows itself, so x and w are there.
 template <int kAct, int kPieces, bool kBack, int kAdapt>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
@@ -243,8 +244,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
-  grid_inputs_ready();
-  grid_let_next_start();
+  if constexpr (!kAdapt) {
+    grid_inputs_ready();
+    grid_let_next_start();
+  }
 
   if (warp < 4) {
     if constexpr (kLong) registers_down<kControlRegs>();
@@ -275,9 +278,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int rt = row_tile(tl, t), row0 = ad.v.tiles.first(rt), row1 = ad.v.tiles.end(rt);
           const int chunks = (ad.v.R + 63) / 64;
           int more = 0;
-          for_segments(ad.v, row0, row1, lane, [&](int, int, bool odd) { more += odd ? 1 : 2 * chunks; });
           for (int i = 0; i < nk && ok; ++i) {
             const int k = i * 64;
+            if (i == nk - 1) {
+              if (t == pair) {
+                grid_inputs_ready();
+                grid_let_next_start();
+              }
+              for_segments(ad.v, row0, row1, lane, [&](int, int, bool odd) { more += odd ? 1 : 2 * chunks; });
+            }
             load(&map_x, k & tl.col_mask, xrow, z0 + (k >> tl.head_shift), &map_w, k, 0, 4 | (more == 0 && i == nk - 1 ? 8 : 0));
           }
           for_segments(ad.v, row0, row1, lane, [&](int seg, int which, bool odd) {
