@@ -104,6 +104,20 @@ class MetaCacheLayer:
         return self.out
 
 
+@dataclass
+class BlockAdapters:
+    """Low-rank adapters of an AttentionBlock's two projections for the requests of a batch: adapter a adds
+    scale[a] * (x down_a^T) up_a^T to a projection of the rows whose segment takes it. start [segments + 1] cuts the rows
+    (counted through the batches), which [segments] names each segment's adapter (negative: none); both int32."""
+    down_qkv: torch.Tensor   # [count, rank, in]
+    up_qkv: torch.Tensor     # [count, 3 * H * d, rank]
+    down_out: torch.Tensor   # [count, rank, H * d]
+    up_out: torch.Tensor     # [count, in, rank]
+    scale: torch.Tensor      # [count] fp32
+    start: torch.Tensor
+    which: torch.Tensor
+
+
 class AttentionBlock:
     """The projections around a MetaCacheLayer, from a block's hidden states x
     [B, N, in] and back: packed q, k, v projection, per-head norms of q and k with
@@ -111,12 +125,13 @@ class AttentionBlock:
     projection added to the hidden states through a gate.
 
     w_qkv: [3 * H * d, in], rows ordered q heads, k heads, v heads; w_out: [in, H * d];
-    wq, wk: norm weights [d] or None; biases may be None. The block owns its buffers;
-    q, k, v are overwritten by every inputs() call. With run():
+    wq, wk: norm weights [d] or None; biases may be None. adapters: BlockAdapters of the
+    requests in the batch, or None; its tensors may be refilled between steps. The block owns
+    its buffers; q, k, v are overwritten by every inputs() call. With run():
         run(layer, sched, lambda: block.inputs(x), advance,
             on_output=lambda t, kind, o: block.output(o, x, gate, x))"""
 
-    def __init__(self, layer: MetaCacheLayer, rope, w_qkv, b_qkv, wq, wk, w_out, b_out, eps=1e-6):
+    def __init__(self, layer: MetaCacheLayer, rope, w_qkv, b_qkv, wq, wk, w_out, b_out, eps=1e-6, adapters=None):
         d = layer.desc
         hd, dt, dev = d.H * d.d, layer.out.dtype, layer.out.device
         self.layer, self.rope, self.eps = layer, rope, eps
@@ -126,18 +141,32 @@ class AttentionBlock:
         self.proj_out = mcs.linear_desc(d.B, d.N, hd, w_out.shape[0], dt, heads=d.H)
         self.qkv = torch.empty((d.B, d.N, 3 * hd), dtype=dt, device=dev)
         self.q, self.k, self.v = (torch.empty_like(layer.out) for _ in range(3))
+        self.adapters = adapters
+        if adapters is not None:
+            a = adapters
+            self.sets = mcs.adapters_desc(a.down_qkv.shape[0], a.down_qkv.shape[1], a.which.shape[0])
+            sizes = [mcs.linear_adapters_workspace(p, self.sets, device=dev) for p in (self.proj_in, self.proj_out)]
+            self.ws = max(sizes, key=torch.Tensor.numel)
+
+    def _project(self, desc, x, w, bias, gate, residual, y, down, up):
+        a = self.adapters
+        if a is None:
+            mcs.mcs_linear(desc, x, w, bias, gate, residual, y)
+        else:
+            mcs.mcs_linear_adapters(desc, self.sets, x, w, bias, gate, residual, getattr(a, down), getattr(a, up), a.scale,
+                                    a.start, a.which, y, self.ws)
 
     def inputs(self, x):
         """(q, k, v) [B, H, N, d] of the hidden states x."""
         d = self.layer.desc
-        mcs.mcs_linear(self.proj_in, x, self.w_qkv, self.b_qkv, None, None, self.qkv)
+        self._project(self.proj_in, x, self.w_qkv, self.b_qkv, None, None, self.qkv, "down_qkv", "up_qkv")
         q, k, v = self.qkv.view(d.B, d.N, 3, d.H, d.d).permute(2, 0, 3, 1, 4)
         mcs.mcs_qk_norm_rope(d, self.rope, self.table, None, q, k, v, self.wq, self.wk, self.eps, self.q, self.k, self.v)
         return self.q, self.k, self.v
 
     def output(self, o, x, gate, y):
         """y = x + gate * (o w_out^T + b_out) for an attention output o; y may be x."""
-        mcs.mcs_linear(self.proj_out, o, self.w_out, self.b_out, gate, x, y)
+        self._project(self.proj_out, o, self.w_out, self.b_out, gate, x, y, "down_out", "up_out")
         return y
 
 

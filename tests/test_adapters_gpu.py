@@ -11,6 +11,15 @@ pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
+def projection_bound(dtype, din, R, size, extra):
+    """The documented bounds of the sums: of the product with R more columns in two parts, of h, of its rounding. size and
+    extra: sums of absolute products (oracle)."""
+    if dtype == "bf16":
+        tol = ((504 + 5.25 * 2 * (R / 16 + 1)) * 2.0 ** -23 + (din / 1024 + 9) * 2.0 ** -24) * (size + extra)
+        return tol + extra * (2.0 ** -16 + (din / 16 + 2) * 5.25 * 2.0 ** -23)
+    return (12 * 2.0 ** -23 + (din / 32 + 11) * 2.0 ** -24) * size + extra * (din + R + 8) * 2.0 ** -24 + (size + extra) * 2.0 ** -23
+
+
 class Case:
     def __init__(self, dtype, B, N, din, dout, rank, start, which, count=3, act="none", heads=0, gated=False, bias=True, seed=0):
         g = torch.Generator(device="cuda").manual_seed(seed + 31 * rank + N)
@@ -47,12 +56,7 @@ class Case:
         z, size, extra = orc.adapted_projection(x, f(self.w), f(self.bias), self.start, self.which, f(self.down), f(self.up), f(self.scale))
         if self.bias is not None:
             size = size + np.abs(f(self.bias))
-        # the documented bounds: of the product with R more columns in two parts, of h, of its rounding
-        if self.dtype == "bf16":
-            tol = ((504 + 5.25 * 2 * (R / 16 + 1)) * 2.0 ** -23 + (din / 1024 + 9) * 2.0 ** -24) * (size + extra)
-            tol += extra * (2.0 ** -16 + (din / 16 + 2) * 5.25 * 2.0 ** -23)
-        else:
-            tol = (12 * 2.0 ** -23 + (din / 32 + 11) * 2.0 ** -24) * size + extra * (din + R + 8) * 2.0 ** -24 + (size + extra) * 2.0 ** -23
+        tol = projection_bound(self.dtype, din, R, size, extra)
         if self.act == "silu":
             v = z / (1 + np.exp(-z))
         elif self.act == "gelu_tanh":
