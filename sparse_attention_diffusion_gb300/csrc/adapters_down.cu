@@ -286,9 +286,10 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 }  // namespace
 
 // bf16: slabs, masks and the bytes of `up`'s shares, for row tiles of any height up to 256 (h and the rows' adapters are
-// smaller). fp32: h and the adapters' part of the sums.
+// smaller). fp32: h, the adapters' part of the sums and the
+// rows' adapters.
 size_t adapters_workspace_bytes(const LinearParams& p, const AdapterParams& a, bool bf16) {
-  if (!bf16) return align256(size_t(p.M) * a.R * 4) + align256(size_t(p.M) * p.O * 4);
+  if (!bf16) return align256(size_t(p.M) * a.R * 4) + align256(size_t(p.M) * p.O * 4) + align256(size_t(p.M) * 4);
   const size_t sections = p.heads > 0 ? p.B : 1;
   const size_t rows = size_t(p.M) + (sections + a.S) * 256;  // of all slabs
   return align256(rows * 2 * a.R * 2) + align256(rows * 8 * 2) + align256(size_t(a.S) * kAdapterPieces);

@@ -71,14 +71,40 @@ __global__ void __launch_bounds__(256) adapters_f32_up_kernel(const LinearParams
   }
 }
 
+// The same where few rows share an adapter: a block takes a row and 256 outputs, a thread an output, whose row of `up`
+// it reads by itself.
+__global__ void __launch_bounds__(256) adapters_f32_up_rows_kernel(const LinearParams p, const AdapterParams a, const float* h, const int32_t* of_row, float* z) {
+  const int o = blockIdx.y * 256 + threadIdx.x, m = blockIdx.x;
+  grid_inputs_ready();
+  grid_let_next_start();
+  if (o >= p.O) return;
+  const int ad = of_row[m];
+  float acc = 0.f;
+  if (ad >= 0) {
+    const float4* x = reinterpret_cast<const float4*>(h + static_cast<size_t>(m) * a.R);
+    const float4* u = reinterpret_cast<const float4*>(static_cast<const float*>(a.up) + (static_cast<size_t>(ad) * p.O + o) * a.R);
+#pragma unroll 4
+    for (int r = 0; r < a.R / 4; ++r) {
+      const float4 v = x[r], w = __ldg(u + r);
+      acc = fmaf(v.w, w.w, fmaf(v.z, w.z, fmaf(v.y, w.y, fmaf(v.x, w.x, acc))));
+    }
+  }
+  z[static_cast<size_t>(m) * p.O + o] = acc;
+}
+
 }  // namespace
 
 cudaError_t linear_adapters_f32(const LinearParams& p, const AdapterParams& a, int num_sms, cudaStream_t s) {
   float* h = static_cast<float*>(a.ws);
   float* z = h + (size_t(p.M) * a.R + 63) / 64 * 64;
-  const dim3 up((unsigned(p.M) + kTile - 1) / kTile, (p.O + kTile - 1) / kTile);
-  cudaError_t e = adapters_down_rows(p, a, false, h, nullptr, s);
-  if (e == cudaSuccess) e = launch_overlapped(adapters_f32_up_kernel, up, 256, 0, s, 0, p, a, h, z);
+  int32_t* of_row = reinterpret_cast<int32_t*>(z + (size_t(p.M) * p.O + 63) / 64 * 64);
+  cudaError_t e = adapters_down_rows(p, a, false, h, of_row, s);
+  if (e != cudaSuccess) return e;
+  // a tile of 64 rows goes through its segments one by one (70 rows with adapters of their own: 88 us in all, 25 row by row)
+  if (p.M <= 4ll * a.S)
+    e = launch_overlapped(adapters_f32_up_rows_kernel, dim3(unsigned(p.M), (p.O + 255) / 256), 256, 0, s, 0, p, a, h, of_row, z);
+  else
+    e = launch_overlapped(adapters_f32_up_kernel, dim3((unsigned(p.M) + kTile - 1) / kTile, (p.O + kTile - 1) / kTile), 256, 0, s, 0, p, a, h, z);
   if (e != cudaSuccess) return e;
   LinearParams with = p;
   with.add = z;

@@ -493,13 +493,21 @@ cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Tiles and chunks. A tile takes as many tokens as fit in 128 rows (64 on the CUDA cores). Sequences are cut where the
-// tiles alone do not fill the GPU twice over and a sequence has more than a thousand keys on average: into pieces of
-// which every SM gets about eight, of 256 keys at least. Whole sequences of more than one tile go two tiles at a time.
+// Tiles and chunks. A tile takes as many tokens as fit in 128 rows; on the CUDA cores in 64, or in 16 where a sequence has
+// no more or the tiles of 64 are fewer than the SMs (77 tokens of 2 x 2 heads 13.9 us with 64 rows, 7.9 with 16).
+// Sequences are cut where the tiles alone do not fill the GPU and a sequence has many keys: into pieces of which
+// every SM gets eight where a sequence is one tile (64 tokens over 16,384 keys and less: 294 us with four, 280 with eight,
+// 284 with sixteen), otherwise four, as every tile of a sequence leaves its sums (seven chunks of 300 tokens and less: 62
+// us with two, 64 with four, 77 with eight). Whole sequences of more than one tile go two tiles at a time.
 bool plan_packed(PackedParams* p, bool bf16) {
   constexpr int kSms = 152;
   p->g = p->H / p->Hk;
-  p->tq = (bf16 ? 128 : 64) / p->g;
+  int rows = bf16 ? 128 : 64;
+  if (!bf16 && p->g <= 16) {
+    const long long tiles64 = static_cast<long long>(p->Tq) / (64 / p->g) + p->S;
+    if (static_cast<long long>(p->max_q) * p->g <= 16 || tiles64 * p->Hk < kSms) rows = 16;
+  }
+  p->tq = rows / p->g;
   p->by_group = Divisor(p->g);
   p->by_heads = Divisor(p->Hk);
   const long long tiles = (static_cast<long long>(p->max_q) + p->tq - 1) / p->tq;

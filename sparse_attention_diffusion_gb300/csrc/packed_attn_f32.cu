@@ -1,8 +1,8 @@
 // Softmax attention over packed sequences on the CUDA cores, fp32: fp32 inputs have to match the
 // 64-bit result to 1e-5, which products of shorter numbers do not. The items of packed.h with 64 rows a tile,
-// a block each.
+// a block each; 16 rows where those are too few for the GPU.
 //
-// 256 threads as 16 x 16: a thread has 4 rows x 4 keys of the scores and 4 rows x D / 16 columns of the sums, in packed
+// 256 threads as 16 x 16: a thread has 4 rows (or one) x 4 keys of the scores and as many x D / 16 columns of the sums, in packed
 // pairs (scores: two columns of the head side by side; sums: two outputs). Keys and values take turns in one buffer of
 // 64 rows, so that two blocks share an SM and one loads while the other multiplies. A step of four head columns
 // reads 12 shared-memory wavefronts for 64 multiplications a lane (16 clocks); the multiplications bound it.
@@ -16,9 +16,10 @@
 namespace mcs {
 namespace {
 
-constexpr int kRowsTile = 64, kKeys = 64, kThreads = 256;
-template <int D>
+constexpr int kKeys = 64, kThreads = 256;
+template <int D, int kR>  // kR: rows of a thread
 struct Cfg {
+  static constexpr int kRowsTile = 16 * kR;
   static constexpr int kLd = D + 4;     // floats of a row: 16 rows' 16-byte pieces lie in different banks
   static constexpr int kLdP = kKeys + 4;
   static constexpr int kBytes = (kRowsTile * kLd + kKeys * kLd + kRowsTile * kLdP) * 4;
@@ -27,9 +28,10 @@ struct Walk {
   Divisor by_tq, by_chunk;
 };
 
-template <int D>
+template <int D, int kR>
 __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const PackedParams p, const Walk wk) {
-  using L = Cfg<D>;
+  using L = Cfg<D, kR>;
+  constexpr int kRowsTile = L::kRowsTile;
   constexpr int kC = D / 64;  // 16-byte pieces of a row of sums a thread has
   extern __shared__ __align__(16) float sm[];
   float* qs = sm;
@@ -62,12 +64,12 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
       w = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + h * p.qs.head + (it.q0 + t) * p.qs.token)[c];
     *reinterpret_cast<float4*>(qs + r * L::kLd + c * 4) = w;
   }
-  int lim[4];
-  float m[4], l[4];
-  uint64_t o[4][kC * 2];
+  int lim[kR];
+  float m[kR], l[kR];
+  uint64_t o[kR][kC * 2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty * 4 + i, t = p.by_group.div(r);
+  for (int i = 0; i < kR; ++i) {
+    const int r = ty * kR + i, t = p.by_group.div(r);
     lim[i] = r < p.rows && t < it.ntok ? visible_keys(it, p.causal, t) : 0;
     m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
@@ -84,20 +86,20 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
       *reinterpret_cast<float4*>(kv + r * L::kLd + c * 4) = w;
     }
     __syncthreads();
-    uint64_t s2[4][4];
+    uint64_t s2[kR][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int n = 0; n < 4; ++n) s2[i][n] = f2_pack(0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < D; k += 4) {
-      ulonglong2 a[4], b[4];
+      ulonglong2 a[kR], b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(qs + (ty * 4 + i) * L::kLd + k);
+      for (int i = 0; i < kR; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(qs + (ty * kR + i) * L::kLd + k);
 #pragma unroll
       for (int n = 0; n < 4; ++n) b[n] = *reinterpret_cast<const ulonglong2*>(kv + (tx + 16 * n) * L::kLd + k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kR; ++i)
 #pragma unroll
         for (int n = 0; n < 4; ++n) s2[i][n] = f2_fma(a[i].y, b[n].y, f2_fma(a[i].x, b[n].x, s2[i][n]));
     }
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
     }
     if (found) odd = 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR; ++i) {
       float s[4], top = -INFINITY;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
       for (int n = 0; n < 4; ++n) {
         const float e = exp2f(s[n] - base);
         sum += e;
-        ps[(ty * 4 + i) * L::kLdP + tx + 16 * n] = e;
+        ps[(ty * kR + i) * L::kLdP + tx + 16 * n] = e;
       }
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -146,16 +148,16 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
     __syncthreads();
 #pragma unroll 2
     for (int j = 0; j < kKeys; j += 4) {
-      float4 w[4];
+      float4 w[kR];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(ps + (ty * 4 + i) * L::kLdP + j);
+      for (int i = 0; i < kR; ++i) w[i] = *reinterpret_cast<const float4*>(ps + (ty * kR + i) * L::kLdP + j);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
         ulonglong2 v[kC];
 #pragma unroll
         for (int c = 0; c < kC; ++c) v[c] = *reinterpret_cast<const ulonglong2*>(kv + (j + jj) * L::kLd + tx * 4 + 64 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kR; ++i) {
           const float e = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
           const uint64_t e2 = f2_pack(e, e);
 #pragma unroll
@@ -170,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
   __syncthreads();
   const bool extra = odd != 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty * 4 + i, t = p.by_group.div(r), h = it.hk * p.g + r - t * p.g;
+  for (int i = 0; i < kR; ++i) {
+    const int r = ty * kR + i, t = p.by_group.div(r), h = it.hk * p.g + r - t * p.g;
     if (r >= p.rows || t >= it.ntok) continue;
     const bool cut = p.chunk > 0;
     const float inv = cut ? 1.f : 1.f / l[i];
@@ -199,18 +201,19 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
   }
 }
 
-template <int D>
+template <int D, int kR>
 cudaError_t launch_f32(const PackedParams& p, cudaStream_t s) {
-  const cudaError_t e = allow_smem<packed_attn_f32_kernel<D>>(Cfg<D>::kBytes);
+  const cudaError_t e = allow_smem<packed_attn_f32_kernel<D, kR>>(Cfg<D, kR>::kBytes);
   if (e != cudaSuccess) return e;
   const Walk wk{Divisor(p.tq), Divisor(p.chunk > 0 ? p.chunk : 1)};
-  return launch_overlapped(packed_attn_f32_kernel<D>, dim3(unsigned(p.items)), kThreads, Cfg<D>::kBytes, s, 0, p, wk);
+  return launch_overlapped(packed_attn_f32_kernel<D, kR>, dim3(unsigned(p.items)), kThreads, Cfg<D, kR>::kBytes, s, 0, p, wk);
 }
 
 }  // namespace
 
 cudaError_t packed_attn_f32(const PackedParams& p, cudaStream_t s) {
-  const cudaError_t e = p.d == 128 ? launch_f32<128>(p, s) : launch_f32<64>(p, s);
+  const cudaError_t e = p.rows > 16 ? (p.d == 128 ? launch_f32<128, 4>(p, s) : launch_f32<64, 4>(p, s))
+                                    : (p.d == 128 ? launch_f32<128, 1>(p, s) : launch_f32<64, 1>(p, s));
   return e != cudaSuccess || p.chunk == 0 ? e : packed_join(p, false, s);
 }
 
