@@ -497,8 +497,8 @@ cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
 // no more or the tiles of 64 are fewer than the SMs (77 tokens of 2 x 2 heads 13.9 us with 64 rows, 7.9 with 16).
 // Sequences are cut where the tiles alone do not fill the GPU and a sequence has many keys: into pieces of which
 // every SM gets eight where a sequence is one tile (64 tokens over 16,384 keys and less: 294 us with four, 280 with eight,
-// 284 with sixteen), otherwise four, as every tile of a sequence leaves its sums (seven chunks of 300 tokens and less: 62
-// us with two, 64 with four, 77 with eight). Whole sequences of more than one tile go two tiles at a time.
+// 284 with sixteen), otherwise two, as every tile of a sequence leaves its sums (seven chunks of 300 tokens and less: 61
+// us with one, 57 with two or four, 70 with eight). Sequences of more than one tile go two tiles at a time.
 bool plan_packed(PackedParams* p, bool bf16) {
   constexpr int kSms = 152;
   p->g = p->H / p->Hk;
@@ -508,6 +508,8 @@ bool plan_packed(PackedParams* p, bool bf16) {
     if (static_cast<long long>(p->max_q) * p->g <= 16 || tiles64 * p->Hk < kSms) rows = 16;
   }
   p->tq = rows / p->g;
+  p->pair = bf16 && p->max_q > p->tq;
+  if (p->pair) p->tq *= 2;
   p->by_group = Divisor(p->g);
   p->by_heads = Divisor(p->Hk);
   const long long tiles = (static_cast<long long>(p->max_q) + p->tq - 1) / p->tq;
@@ -519,18 +521,13 @@ bool plan_packed(PackedParams* p, bool bf16) {
   p->tiles = 1;
   const int piece = bf16 ? 128 : 64;
   if (keys >= 4 * piece && tiles <= 64 && (most * p->Hk < 2 * kSms || (tiles == 1 && most * p->Hk < 8 * kSms))) {
-    const long long work = most * keys * p->Hk, each = tiles == 1 ? 8 : 4;
+    const long long work = most * keys * p->Hk, each = tiles == 1 ? 8 : 2;
     long long chunk = (work / (each * kSms) + piece - 1) / piece * piece;
     if (chunk < 2 * piece) chunk = 2 * piece;
     p->chunk = int(chunk < (1 << 30) ? chunk : (1 << 30));
     p->tiles = int(tiles);
     slots = p->Tk / p->chunk + p->S;
     p->by_tiles = Divisor(p->tiles);
-  }
-  p->pair = bf16 && p->chunk == 0 && p->max_q > p->tq;
-  if (p->pair) {
-    p->tq *= 2;
-    slots = static_cast<long long>(p->Tq) / p->tq + p->S;
   }
   p->rows = p->tq * p->g;
   p->items = slots * p->tiles * p->Hk;

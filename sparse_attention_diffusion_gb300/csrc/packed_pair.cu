@@ -1,5 +1,5 @@
-// Softmax attention over packed sequences, bf16, two tiles of 128 query rows at a time: prompts of more than one tile,
-// whose keys are not cut. Formula, items, masks and what lies in masked places as in packed_attn.cu.
+// Softmax attention over packed sequences, bf16, two tiles of 128 query rows at a time: sequences of more than one tile.
+// Formula, items, masks and what lies in masked places as in packed_attn.cu.
 //
 // One tile alone leaves the tensor core idle while its softmax runs, and the other way round: 1,850 clocks a tile of 128 x
 // 128 scores of which the products take 1,024. Here two tiles, A and B, share every K and V tile and take turns: while
@@ -57,7 +57,8 @@ struct Cfg {
 };
 static_assert(Cfg<128>::kAlloc <= 227 * 1024 && Cfg<64>::kAlloc <= 227 * 1024, "shared memory");
 
-template <int D>
+// kCut: an item's keys are one piece of its sequence's, its sums leave in fp32 for packed_join.
+template <int D, bool kCut>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const PackedParams p, const PackedWalk wk) {
@@ -319,20 +320,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = tt < ntok;
         const int rows = min(32, ntok * p.g - w4 * 32);  // of this warp
         if (rows > 0) {
-          const float l = ml.y, inv = l == 0.f ? 0.f : 1.f / l;  // rows that see nothing give 0
+          const float l = ml.y, inv = kCut ? 1.f : l == 0.f ? 0.f : 1.f / l;  // rows that see nothing give 0
           // elements of V that are not finite and that only some rows see (left out of the products)
           const bool extra = some && all_see < it.nkeys && (odd[n % kFlags * 2] | odd[n % kFlags * 2 + 1]) != 0;
           const int lim = visible_keys(it, p.causal, c * half + tt);
+          constexpr int kPass = kCut ? 32 : 64;  // columns of 128 bytes of a row
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + static_cast<long long>(it.hk) * p.g * p.os.head +
                                static_cast<long long>(it.q0 + c * half) * p.os.token;
+          const long long part = it.part + c * half * p.g + w4 * 32;  // this warp's first row of the partial sums
 #pragma unroll 1
-          for (int q = 0; q < D / 64; ++q) {  // 64 columns: 128 bytes a row
+          for (int q = 0; q < D / kPass; ++q) {
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {  // 16 columns
+            for (int x = 0; x < kPass / 16; ++x) {  // 16 columns
               float o[16];
               if (some) {
                 uint32_t u[16];
-                tmem_ld16(tO + q * 64 + x * 16, u);
+                tmem_ld16(tO + q * kPass + x * 16, u);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(u[i]) * inv;
               } else {
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 16; ++i) o[i] = 0.f;
               }
               if (extra && mine) {
-                const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(p.v) + static_cast<long long>(it.hk) * p.vs.head + q * 64 + x * 16;
+                const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(p.v) + static_cast<long long>(it.hk) * p.vs.head + q * kPass + x * 16;
 #pragma unroll 1
                 for (int j = all_see; j < lim; ++j) {
                   const __nv_bfloat16* vr = vb + static_cast<long long>(it.k0 + j) * p.vs.token;
@@ -351,14 +354,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
               }
+              if constexpr (kCut) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + (((x * 2 + i) ^ (lane & 7)) << 4)),
-                             "r"(pack_bf16x2(o[8 * i], o[8 * i + 1])), "r"(pack_bf16x2(o[8 * i + 2], o[8 * i + 3])),
-                             "r"(pack_bf16x2(o[8 * i + 4], o[8 * i + 5])), "r"(pack_bf16x2(o[8 * i + 6], o[8 * i + 7]))
-                             : "memory");
+                for (int i = 0; i < 4; ++i)
+                  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + (((x * 4 + i) ^ (lane & 7)) << 4)),
+                               "f"(o[4 * i]), "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3])
+                               : "memory");
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + (((x * 2 + i) ^ (lane & 7)) << 4)),
+                               "r"(pack_bf16x2(o[8 * i], o[8 * i + 1])), "r"(pack_bf16x2(o[8 * i + 2], o[8 * i + 3])),
+                               "r"(pack_bf16x2(o[8 * i + 4], o[8 * i + 5])), "r"(pack_bf16x2(o[8 * i + 6], o[8 * i + 7]))
+                               : "memory");
+              }
             }
-            if (q == D / 64 - 1 && some) {  // the sums have been read
+            if (q == D / kPass - 1 && some) {  // the sums have been read
               tc_fence_before();
               mbar_arrive(o_free + c);
             }
@@ -373,13 +384,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                              : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                              : "r"(patch + r * 128 + ((ch ^ (r & 7)) << 4))
                              : "memory");
-                const int rr = w4 * 32 + r, rt = p.by_group.div(rr), rh = rr - rt * p.g;
-                *reinterpret_cast<uint4*>(out + rh * p.os.head + rt * p.os.token + q * 64 + ch * 8) = w;
+                if constexpr (kCut) {
+                  *reinterpret_cast<uint4*>(p.part_o + (part + r) * D + q * kPass + ch * 4) = w;
+                } else {
+                  const int rr = w4 * 32 + r, rt = p.by_group.div(rr), rh = rr - rt * p.g;
+                  *reinterpret_cast<uint4*>(out + rh * p.os.head + rt * p.os.token + q * kPass + ch * 8) = w;
+                }
               }
             }
             __syncwarp();
           }
-          if (mine && p.lse != nullptr)
+          if (kCut && mine) p.part_ml[part + lane] = ml;
+          if (!kCut && mine && p.lse != nullptr)
             p.lse[static_cast<long long>(it.hk * p.g + hh) * p.Tq + it.q0 + c * half + tt] = l == 0.f ? -INFINITY : (ml.x + __log2f(l)) * kLn2;
         } else if (some) {
           tc_fence_before();
@@ -482,21 +498,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kCut>
 cudaError_t launch_two(const PackedParams& p, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   if (!(make_view_map(&mq, p.q, p.H, p.Tq, D, p.qs, p.g, p.tq / 2) && make_view_map(&mk, p.k, p.Hk, p.Tk, D, p.ks, 1, 128) &&
         make_view_map(&mv, p.v, p.Hk, p.Tk, D, p.vs, 1, 128)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem_and_regs<packed_pair_kernel<D>>(Cfg<D>::kAlloc, kLaunchRegs);
+  const cudaError_t e = allow_smem_and_regs<packed_pair_kernel<D, kCut>>(Cfg<D>::kAlloc, kLaunchRegs);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(packed_pair_kernel<D>, dim3(unsigned(p.items)), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
+  return launch_overlapped(packed_pair_kernel<D, kCut>, dim3(unsigned(p.items)), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
 }
 
 }  // namespace
 
 cudaError_t packed_attn_pair(const PackedParams& p, cudaStream_t s) {
-  return p.d == 128 ? launch_two<128>(p, s) : launch_two<64>(p, s);
+  if (p.chunk == 0) return p.d == 128 ? launch_two<128, false>(p, s) : launch_two<64, false>(p, s);
+  const cudaError_t e = p.d == 128 ? launch_two<128, true>(p, s) : launch_two<64, true>(p, s);
+  return e != cudaSuccess ? e : packed_join(p, true, s);
 }
 
 }  // namespace mcs
