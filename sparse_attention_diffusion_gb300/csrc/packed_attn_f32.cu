@@ -49,7 +49,8 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
     }
     __syncwarp();
     PackedItem it{};
-    const bool found = packed_item(p, wk.by_tq, wk.by_chunk, blockIdx.x, lane, &it);
+    const PackedLane sequence = p.S <= 32 ? packed_lane(p, wk.by_tq, wk.by_chunk, lane) : PackedLane{};
+    const bool found = packed_item(p, wk.by_tq, wk.by_chunk, sequence, blockIdx.x, lane, &it);
     if (lane == 0) item = it, go = found, odd = 0;
   }
   __syncthreads();

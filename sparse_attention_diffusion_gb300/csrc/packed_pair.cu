@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++cnt;
         return true;
       };
-      PackedBlocks blocks(steal, steal_slot);
+      PackedBlocks blocks(p, wk, lane, steal, steal_slot);
       PackedItem it{}, following{};  // the first turn finds an item and loads nothing
       for (bool begun = false;; it = following, begun = true) {
         if (begun) {

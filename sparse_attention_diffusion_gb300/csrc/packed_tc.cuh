@@ -76,7 +76,11 @@ struct PackedBlocks {
   uint64_t* bar;
   uint32_t slot, answers = 0;
   bool own = true;
-  __device__ __forceinline__ PackedBlocks(uint64_t* b, uint32_t s) : bar(b), slot(s) { ask(); }
+  PackedLane sequence;
+  __device__ __forceinline__ PackedBlocks(const PackedParams& p, const PackedWalk& wk, int lane, uint64_t* b, uint32_t s) : bar(b), slot(s) {
+    ask();
+    if (p.S <= 32) sequence = packed_lane(p, wk.by_tq, wk.by_chunk, lane);
+  }
   __device__ __forceinline__ void ask() {
     if (elect_one()) {
       mbar_arrive_expect_tx(bar, 16);
@@ -105,7 +109,7 @@ struct PackedBlocks {
         if (!packed_sequence(p, int(s), a, b, c, d)) raise_status(p.status, kStatusBounds);
       }
       __syncwarp();
-      if (packed_item(p, wk.by_tq, wk.by_chunk, i, lane, &it)) return true;
+      if (packed_item(p, wk.by_tq, wk.by_chunk, sequence, i, lane, &it)) return true;
     }
   }
 };
