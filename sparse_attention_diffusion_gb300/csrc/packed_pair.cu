@@ -47,10 +47,10 @@ struct Cfg {
   static constexpr int kOut = kRing + kStages * kTile;
   static constexpr int kStats = kOut + 4 * kPatch;    // (maximum, sum) of A's and B's rows
   static constexpr int kBar = kStats + 2 * 128 * 8;
-  static constexpr int kNumBars = 2 * kStages + 2 * 7 + 2 * kItems + 2;
+  static constexpr int kNumBars = 2 * kStages + 2 * 7 + 2 * kItems + 5;
   static constexpr int kSteal = (kBar + kNumBars * 8 + 15) / 16 * 16;  // the answer to a request for a block
   static constexpr int kMisc = kSteal + 16;
-  static constexpr int kItem = (kMisc + 16 + kFlags * 8 + 15) / 16 * 16;
+  static constexpr int kItem = (kMisc + 16 + kFlags * 4 + 15) / 16 * 16;
   static constexpr int kBytes = kItem + kItems * int(sizeof(PackedItem));
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kColS = 0, kColO = 256;  // of A; B's lie 128 behind
@@ -78,23 +78,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_free = o_full + 2;
   uint64_t* it_full = o_free + 2;     // [kItems]
   uint64_t* it_empty = it_full + kItems;
-  uint64_t* drain = it_empty + kItems;
-  uint64_t* steal = drain + 1;
+  uint64_t* turn = it_empty + kItems;  // [2] products of a tile issued, or left out
+  uint64_t* drain = turn + 2;          // [2]
+  uint64_t* steal = drain + 2;
   const uint32_t steal_slot = sbase + L::kSteal;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
-  volatile uint32_t* odd = tmem_slot + 4;  // [kFlags][2] the item's V held something that is not finite and not seen by all
+  volatile uint32_t* odd = tmem_slot + 4;  // [kFlags] the item's V held something that is not finite and not seen by all
   float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
   PackedItem* items = reinterpret_cast<PackedItem*>(smem + L::kItem);
 
   const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
   uint32_t* st = p.status;
   if (tid == 0) {
-    for (int s = 0; s < R; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    for (int s = 0; s < R; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 2);
     for (int c = 0; c < 2; ++c) {
-      mbar_init(q_full + c, 1), mbar_init(q_empty + c, 1), mbar_init(s_go + c, 2), mbar_init(s_full + c, 1);
-      mbar_init(p_full + c, 130), mbar_init(o_full + c, 130), mbar_init(o_free + c, 128);
+      mbar_init(q_full + c, 1), mbar_init(q_empty + c, 1), mbar_init(s_go + c, 1), mbar_init(turn + c, 1), mbar_init(drain + c, 1), mbar_init(s_full + c, 1);
+      mbar_init(p_full + c, 129), mbar_init(o_full + c, 130), mbar_init(o_free + c, 128);
     }
-    mbar_init(drain, 1), mbar_init(steal, 1);
+    mbar_init(steal, 1);
     for (int b = 0; b < kItems; ++b) mbar_init(it_full + b, 1), mbar_init(it_empty + b, 8 + 4 + 3);
     fence_mbar_init();
   }
@@ -187,63 +188,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         settle_copies();  // normally the products have consumed every copy before the CTA exits
       }
       __syncwarp();
-    } else if (warp == 13) {
-      // ---------------------------------------------------------- products, of A and B in turn
+    } else if (warp <= 14) {
+      // ---------------------------------------------------------- products of A (warp 13) and of B (warp 14)
+      const int c = warp - 13;
       constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
+      const uint32_t tO = tmem + L::kColO + c * 128, tS = tmem + L::kColS + c * 128;
+      const uint32_t qlo = desc_lo_kmajor(sbase + L::kQ + c * L::kTile);
       bool ok = true, issued = false;
-      int tile = 0, done0 = 0, done1 = 0, live0 = 0, live1 = 0;  // K/V tiles so far, those of each chain, its items
+      uint32_t tile = 0, done = 0, live = 0;  // K/V tiles so far, those of this chain, its items
       for (int n = 0; ok; ++n) {
         PackedItem it;
         if (!(ok = take(n, it))) break;
         if (it.tiles < 0) break;
-        const int T0 = tiles_of(it, 0), T1 = tiles_of(it, 1);  // A's are not more than B's, unless B has none
-        // S_0 of both; then P_j V_j and S_{j+1}. The last chain that takes a tile lets its stage go.
-        for (int j = -1; j < it.tiles && ok; ++j) {
-          const uint32_t sv = uint32_t(2 * (tile + j) + 1) % R, sk = (sv + 1) % R;
+        const int T = tiles_of(it, c);
+        // S_0; then P_j V_j and S_{j+1}
+        for (int j = -1; j < it.tiles; ++j) {
+          if (j < 0 && T == 0) continue;
+          const uint32_t xv = 2 * (tile + j) + 1, sv = xv % R, xk = xv + 1, sk = xk % R;
+          if (j >= 0) {
+            // the other one's products of the tile before (A: of B; B: of A, this tile) have been issued
+            if (!(ok = warp_all(mbar_wait_short(turn + (c ^ 1), (tile + j + (c ^ 1)) & 1)))) break;
+            if (j >= T) {  // a tile that only B takes: its keys and values are let go when they have come
+              ok = warp_all(mbar_wait_short(full + (xv - 1) % R, ((xv - 1) / R) & 1)) && warp_all(mbar_wait_short(full + sv, (xv / R) & 1));
+              if (!ok) break;
+              if (lane == 0) mbar_arrive(empty + (xv - 1) % R), mbar_arrive(empty + sv), mbar_arrive(turn + c);
+              __syncwarp();
+              continue;
+            }
+          }
+          if (!(ok = warp_all(mbar_wait_short((j < 0 ? s_go : p_full) + c, j < 0 ? live & 1 : (done + j) & 1)))) break;
+          tc_fence_after();
+          issued = true;
           const uint32_t vlo = desc_lo_mnmajor(sbase + L::kRing + sv * L::kTile), klo = desc_lo_kmajor(sbase + L::kRing + sk * L::kTile);
+          if (elect_one()) {
+            if (j >= 0) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int T = c ? T1 : T0;
-            if (j >= T || T == 0) continue;
-            if (!(ok = warp_all(mbar_wait_short((j < 0 ? s_go : p_full) + c, j < 0 ? uint32_t(c ? live1 : live0) & 1 : uint32_t((c ? done1 : done0) + j) & 1)))) break;
-            tc_fence_after();
-            issued = true;
-            const uint32_t tO = tmem + L::kColO + c * 128, tS = tmem + L::kColS + c * 128;
-            if (elect_one()) {
-              if (j >= 0) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                  tc_mma_ts_lo(tO, tS + ks * 8, vlo + kstep_mnmajor(ks), kIdescPV, (j > 0 || ks > 0) ? 1u : 0u);
-                if (c == 1 || j >= T1) tc_commit(empty + sv);
-                if (j == T - 1) {
-                  tc_commit(o_full + c);
-                  mbar_arrive(o_full + c);  // passes on the flags of V
-                }
-              }
-              if (j + 1 < T) {
-                const uint32_t qlo = desc_lo_kmajor(sbase + L::kQ + c * L::kTile);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                  tc_mma_ss_lo(tS, qlo + kstep_kmajor(ks), klo + kstep_kmajor(ks), kIdescQK, ks > 0 ? 1u : 0u);
-                tc_commit(s_full + c);
-                if (c == 1 || j + 1 >= T1) tc_commit(empty + sk);
-                if (j + 2 == T) tc_commit(q_empty + c);
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma_ts_lo(tO, tS + ks * 8, vlo + kstep_mnmajor(ks), kIdescPV, (j > 0 || ks > 0) ? 1u : 0u);
+              tc_commit(empty + sv);
+              // The other one's turn: it takes 300 clocks to begin, two S products are in the queue by then (with all
+              // of them 345 us instead of 344 for three clips, from P V on 345).
+              if (j + 1 >= T) mbar_arrive(turn + c);
+              if (j == T - 1) {
+                tc_commit(o_full + c);
+                mbar_arrive(o_full + c);  // passes on the flag of V
               }
             }
-            __syncwarp();
+            if (j + 1 < T) {
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                tc_mma_ss_lo(tS, qlo + kstep_kmajor(ks), klo + kstep_kmajor(ks), kIdescQK, ks > 0 ? 1u : 0u);
+                if (j >= 0 && ks == 1) mbar_arrive(turn + c);
+              }
+              tc_commit(s_full + c);
+              tc_commit(empty + sk);
+              if (j + 2 == T) tc_commit(q_empty + c);
+            }
           }
+          __syncwarp();
         }
         if (!ok) break;
         tile += it.tiles;
-        done0 += T0, done1 += T1, live0 += T0 > 0, live1 += T1 > 0;
+        done += T, live += T > 0;
       }
       if (!ok) {
         if (lane == 0) raise_status(st, kStatusTimeout);
         if (issued) {
-          if (elect_one()) tc_commit(drain);
+          if (elect_one()) tc_commit(drain + c);
           __syncwarp();
-          mbar_drain(drain, 0);
+          mbar_drain(drain + c, 0);
         }
       }
       __syncwarp();
@@ -259,8 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int T0 = tiles_of(it, 0), T1 = tiles_of(it, 1);
         const int all_see = visible_keys(it, p.causal, 0);
         bool found = false;
-        const int part = warp - 14;
-        if (lane == 0) odd[n % kFlags * 2 + part] = 0;
+        if (lane == 0) odd[n % kFlags] = 0;
         if (it.tiles > 0 && !(ok = landed(2 * tile))) break;
 #pragma unroll 1
         for (int x = -2; x < 2 * it.tiles && ok; ++x) {
@@ -269,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int v = 2 * (tile + j) + 1;
             if (!(ok = landed(v))) break;
             if ((j + 1) * 128 > all_see) {
-              found |= settle_v<D, 2>(sbase + L::kRing + v % R * L::kTile, max(0, all_see - j * 128), min(128, it.nkeys - j * 128), part, lane);
+              found |= settle_v<D>(sbase + L::kRing + v % R * L::kTile, max(0, all_see - j * 128), min(128, it.nkeys - j * 128), 0, lane);
               fence_proxy_async_smem();
-              if (__any_sync(0xffffffffu, found) && lane == 0) odd[n % kFlags * 2 + part] = 1;
+              if (__any_sync(0xffffffffu, found) && lane == 0) odd[n % kFlags] = 1;
               __syncwarp();
             }
             if (j + 1 < it.tiles && !(ok = landed(v + 1))) break;
@@ -281,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_all(mbar_wait_short(q_full + c, uint32_t(live) & 1));
           } else {
             if (j == 0) ok = warp_all(mbar_wait_short(o_free + c, (uint32_t(live) & 1) ^ 1));
-            // one arrival of each warp a phase: the last tile's has to be complete
+            // one arrival a phase: the last tile's has to be complete
             if (ok) ok = warp_all(mbar_wait_short(p_full + c, (uint32_t((c ? done1 : done0) + j) & 1) ^ 1));
           }
           if (ok && lane == 0) mbar_arrive((j < 0 ? s_go : p_full) + c);
@@ -322,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rows > 0) {
           const float l = ml.y, inv = kCut ? 1.f : l == 0.f ? 0.f : 1.f / l;  // rows that see nothing give 0
           // elements of V that are not finite and that only some rows see (left out of the products)
-          const bool extra = some && all_see < it.nkeys && (odd[n % kFlags * 2] | odd[n % kFlags * 2 + 1]) != 0;
+          const bool extra = some && all_see < it.nkeys && odd[n % kFlags] != 0;
           const int lim = visible_keys(it, p.causal, c * half + tt);
           constexpr int kPass = kCut ? 32 : 64;  // columns of 128 bytes of a row
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + static_cast<long long>(it.hk) * p.g * p.os.head +

@@ -50,7 +50,7 @@ __device__ __forceinline__ bool settle_v(uint32_t v, int some, int none, int par
                    : "memory");
     }
   }
-#pragma unroll 1
+#pragma unroll 4
   for (int r = none + row0; r < 128; r += kRows)
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + sw128_off(r, ch)), "r"(0) : "memory");
   return found;
