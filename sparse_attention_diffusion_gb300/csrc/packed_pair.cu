@@ -2,23 +2,30 @@
 // Formula, items, masks and what lies in masked places as in packed_attn.cu.
 //
 // One tile alone leaves the tensor core idle while its softmax runs, and the other way round: 1,850 clocks a tile of 128 x
-// 128 scores of which the products take 1,024. Here two tiles, A and B, share every K and V tile and take turns: while
-// A's softmax runs, B's P V and next S do. A block an item, of which one an SM runs and takes over the items of blocks that have not started (cluster launch
-// control), so that items of unlike length spread by themselves; 512 threads:
+// 128 scores of which the products take 1,024. Here two tiles, A and B, share every K and V tile and take turns: while A's
+// softmax runs, B's P V and next S do. A block an item, of which one an SM runs and takes over the items of blocks that
+// have not started (cluster launch control), so that items of unlike length spread by themselves; 512 threads:
 //   warps 0-3, 4-7  softmax of A and of B, a thread per row
 //   warps 8-11      the rows' way out, of A and then of B, while the softmax is at the next item
 //   warp 12         finds the items and loads by TMA: the queries of A and of B, and one ring of K_0, V_0, K_1, V_1, ...
-//   warp 13         the products: S_0 of both; then for every tile P_j V_j and S_{j+1} of A, the same of B. In turn from
-//                   one warp: A and B issued by a warp each fell into step, both softmaxes and then both products
-//                   (3,200 clocks a pair of tiles at d = 128)
-//   warps 14, 15    make V tiles that hold masked keys harmless, half of the rows each, and let the products go
-// The product warp waits on one barrier a step: a wait that is satisfied already takes it 200 clocks beside eight
-// softmax warps, and about as much is hidden by the products that are still queued. So warps 14 and 15 look after everything
-// else that a step needs (keys, values, a free O) and arrive together with the softmax's threads.
+//   warps 13, 14    the products of A and of B: S_0; then for every tile P_j V_j and S_{j+1}, in strict turns: without
+//                   them A and B fall into step, both softmaxes and then both products (3,200 clocks a pair of tiles)
+//   warp 15         makes V tiles that hold masked keys harmless and lets the products go
+// A wait takes a product warp 200 to 300 clocks beside eight softmax warps even where nothing is to be waited for, as much
+// as the products in the queue hide. So warp 15 looks after everything that a step needs (keys, values, a free O) and
+// arrives together with the softmax's threads, and the turn is handed over before the last products are taken in. From one
+// warp, A's step and then B's, a pair of tiles took 3,170 clocks, now 2,900, of which the products take 2,048. P handed over
+// in two halves was slower (2,450 us instead of 2,260 for 32,768 causal tokens), and the last tile's maximum as a first
+// guess, checked afterwards, no faster.
 // Tensor memory: S_A, S_B, O_A, O_B of 128 columns each, P_j written over S_j (a row per lane, so a thread overwrites only
 // what it has read); the products of one warp run in order, so S_{j+1} cannot meet P_j.
 // A sees fewer keys than B under a causal mask and leaves its last tiles out. Softmax warps take the registers that the
 // others hand over (128 at launch; 184, 88 on the way out, 56).
+//
+// Measured: 32,768 causal tokens of 12 heads on 4, d = 128: 2,167 us, 1,523 TFLOP/s at 1,910 MHz (0.87 of the sustained
+// rate of plain products); three full sequences of 7,716, 4,031 and 1,626 tokens, 12 heads: 342 us, 1,410 TFLOP/s; 16 causal
+// prompts of 6 to 839 tokens, 32 heads on 8: 54 us. There the instructions count: with 62 KB of them, unrolled masks and
+// 40 for every wait, a quarter of the fetches missed the instruction cache and the same prompts took 99 us.
 #include "attn_common.cuh"
 #include "common.cuh"
 #include "launch.cuh"
@@ -35,7 +42,7 @@ constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 128, kControlRegs = 56, kOutRegs = 88, kSoftmaxRegs = 184;
 static_assert(128 * kControlRegs + 128 * kOutRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "an increase would wait forever");
 constexpr int kItems = 4;   // items found ahead
-constexpr int kFlags = 8;   // items whose V flags are kept (warps 14, 15 are at most kItems ahead of the way out)
+constexpr int kFlags = 8;   // items whose V flags are kept (warp 15 is at most kItems ahead of the way out)
 constexpr int kPatch = 32 * 128;  // a warp's rows x 128 bytes on their way out
 
 template <int D>
@@ -73,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_go = q_empty + 2;       // queries and first keys are there
   uint64_t* s_full = s_go + 2;
-  uint64_t* p_full = s_full + 2;      // P written (128 threads), and all else that P V and the next S need (warps 14, 15)
+  uint64_t* p_full = s_full + 2;      // P written (128 threads), and all else that P V and the next S need (warp 15)
   uint64_t* o_full = p_full + 2;
   uint64_t* o_free = o_full + 2;
   uint64_t* it_full = o_free + 2;     // [kItems]
