@@ -20,7 +20,7 @@
 // Tensor memory: S_A, S_B, O_A, O_B of 128 columns each, P_j written over S_j (a row per lane, so a thread overwrites only
 // what it has read); the products of one warp run in order, so S_{j+1} cannot meet P_j.
 // A sees fewer keys than B under a causal mask and leaves its last tiles out. Softmax warps take the registers that the
-// others hand over (128 at launch; 184, 88 on the way out, 56).
+// others hand over (128 at launch; 184, 96 on the way out, 48).
 //
 // Measured: 32,768 causal tokens of 12 heads on 4, d = 128: 2,167 us, 1,523 TFLOP/s at 1,910 MHz (0.87 of the sustained
 // rate of plain products); three full sequences of 7,716, 4,031 and 1,626 tokens, 12 heads: 342 us, 1,410 TFLOP/s; 16 causal
@@ -39,7 +39,7 @@ namespace mcs {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kLaunchRegs = 128, kControlRegs = 56, kOutRegs = 88, kSoftmaxRegs = 184;
+constexpr int kLaunchRegs = 128, kControlRegs = 48, kOutRegs = 96, kSoftmaxRegs = 184;
 static_assert(128 * kControlRegs + 128 * kOutRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "an increase would wait forever");
 constexpr int kItems = 4;   // items found ahead
 constexpr int kFlags = 8;   // items whose V flags are kept (warp 15 is at most kItems ahead of the way out)
@@ -320,6 +320,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int live0 = 0, live1 = 0;
     const uint32_t patch = sbase + L::kOut + w4 * kPatch;
+    // where this lane's pieces of a tile's rows go: made once, an address is some 30 instructions
+    [[maybe_unused]] long long row_at[8];
+    if constexpr (!kCut) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = w4 * 32 + i * 4 + (lane >> 3), rt = p.by_group.div(r);
+        row_at[i] = (r - rt * p.g) * p.os.head + rt * p.os.token + (lane & 7) * 8;
+      }
+    }
     for (int n = 0; ok; ++n) {
       PackedItem it;
       if (!(ok = take(n, it))) break;
@@ -351,64 +360,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int q = 0; q < D / kPass; ++q) {
 #pragma unroll 1
-            for (int x = 0; x < kPass / 16; ++x) {  // 16 columns
-              float o[16];
-              if (some) {
-                uint32_t u[16];
-                tmem_ld16(tO + q * kPass + x * 16, u);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(u[i]) * inv;
+            for (int x = 0; x < kPass / 32; ++x) {  // 32 columns
+              uint32_t u[32];
+              if (some) {  // rows that see nothing have sums of 0
+                tmem_ld32(tO + q * kPass + x * 32, u);
               } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                for (int i = 0; i < 32; ++i) u[i] = 0;
               }
-              if (extra && mine) {
-                const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(p.v) + static_cast<long long>(it.hk) * p.vs.head + q * kPass + x * 16;
-#pragma unroll 1
-                for (int j = all_see; j < lim; ++j) {
-                  const __nv_bfloat16* vr = vb + static_cast<long long>(it.k0 + j) * p.vs.token;
+              if constexpr (!kCut) {
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const float f = __bfloat162float(vr[i]);
-                    if (!isfinite(f)) o[i] += f;
-                  }
-                }
+                for (int i = 0; i < 16; ++i) u[i] = pack_bf16x2(__uint_as_float(u[2 * i]) * inv, __uint_as_float(u[2 * i + 1]) * inv);
               }
-              if constexpr (kCut) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + (((x * 4 + i) ^ (lane & 7)) << 4)),
-                               "f"(o[4 * i]), "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3])
-                               : "memory");
-              } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + (((x * 2 + i) ^ (lane & 7)) << 4)),
-                               "r"(pack_bf16x2(o[8 * i], o[8 * i + 1])), "r"(pack_bf16x2(o[8 * i + 2], o[8 * i + 3])),
-                               "r"(pack_bf16x2(o[8 * i + 4], o[8 * i + 5])), "r"(pack_bf16x2(o[8 * i + 6], o[8 * i + 7]))
-                               : "memory");
-              }
+              for (int i = 0; i < (kCut ? 8 : 4); ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * 128 + (((x * 4 + i) ^ (lane & 7)) << 4)),
+                             "r"(u[4 * i]), "r"(u[4 * i + 1]), "r"(u[4 * i + 2]), "r"(u[4 * i + 3])
+                             : "memory");
             }
             if (q == D / kPass - 1 && some) {  // the sums have been read
               tc_fence_before();
               mbar_arrive(o_free + c);
             }
+            if (extra && mine) add_unseen<kCut>(patch + lane * 128, lane, p, it, q * kPass, all_see, lim);
             __syncwarp();
-            // along rows: eight lanes a row
-#pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
-              const int r = i * 4 + (lane >> 3), ch = lane & 7;
-              if (r < rows) {
-                uint4 w;
+            // along rows: eight lanes a row, four rows in flight
+#pragma unroll
+            for (int i0 = 0; i0 < 8; i0 += 4) {
+              uint4 w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = (i0 + i) * 4 + (lane >> 3);
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                             : "r"(patch + r * 128 + ((ch ^ (r & 7)) << 4))
+                             : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                             : "r"(patch + r * 128 + (((lane & 7) ^ (r & 7)) << 4))
                              : "memory");
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = (i0 + i) * 4 + (lane >> 3);
+                if (r >= rows) break;
                 if constexpr (kCut) {
-                  *reinterpret_cast<uint4*>(p.part_o + (part + r) * D + q * kPass + ch * 4) = w;
+                  *reinterpret_cast<uint4*>(p.part_o + (part + r) * D + q * kPass + (lane & 7) * 4) = w[i];
                 } else {
-                  const int rr = w4 * 32 + r, rt = p.by_group.div(rr), rh = rr - rt * p.g;
-                  *reinterpret_cast<uint4*>(out + rh * p.os.head + rt * p.os.token + q * kPass + ch * 8) = w;
+                  *reinterpret_cast<uint4*>(out + row_at[i0 + i] + q * kPass) = w[i];
                 }
               }
             }

@@ -70,6 +70,35 @@ __device__ __forceinline__ void mask_scores(uint32_t tS, int nvalid) {
   }
 }
 
+// Adds to the outputs of a row that lie in a patch row (128 bytes, 16-byte pieces swizzled by `sw`: 32 fp32 sums or 64 bf16
+// outputs, of the columns from `col` on) the elements of V that were left out of the products because they are not finite
+// and not all rows see them: of the keys all_see .. lim - 1 of the item. An infinity or a NaN stays one, whatever finite numbers
+// are added, divided or rounded.
+template <bool kF32>
+__device__ __forceinline__ void add_unseen(uint32_t patch_row, int sw, const PackedParams& p, const PackedItem& it, int col, int all_see, int lim) {
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + static_cast<long long>(it.hk) * p.vs.head + col;
+#pragma unroll 1
+  for (int j = all_see; j < lim; ++j) {
+#pragma unroll 1
+    for (int i = 0; i < (kF32 ? 32 : 64); ++i) {
+      const float f = __bfloat162float(v[static_cast<long long>(it.k0 + j) * p.vs.token + i]);
+      if (isfinite(f)) continue;
+      const int byte = i * (kF32 ? 4 : 2);
+      const uint32_t at = patch_row + (((byte >> 4) ^ (sw & 7)) << 4) + (byte & 15);
+      if constexpr (kF32) {
+        float o;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(o) : "r"(at) : "memory");
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(o + f) : "memory");
+      } else {
+        uint16_t o;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(o) : "r"(at) : "memory");
+        const __nv_bfloat16 sum = __float2bfloat16_rn(__bfloat162float(__ushort_as_bfloat16(o)) + f);
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__bfloat16_as_ushort(sum)) : "memory");
+      }
+    }
+  }
+}
+
 // The items of one block: its own, then those of blocks that have not started yet, which it asks the hardware for, one
 // request ahead. One warp; `bar` has a count of one, `slot` is 16 aligned bytes of shared memory.
 struct PackedBlocks {
