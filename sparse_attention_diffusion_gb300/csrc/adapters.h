@@ -88,8 +88,9 @@ struct AdapterArgs<kAdapterRows> {
 
 size_t adapters_workspace_bytes(const LinearParams& p, const AdapterParams& a, bool bf16);
 // First step, bf16: slabs for `t`'s tiles; fills the view and the maps (boxes of `box` slab rows and `wbox` rows of up).
+// free_sms: those that the product leaves, which runs beside it.
 cudaError_t adapters_down_tc(const LinearParams& p, const AdapterParams& a, const RowTiles& t, int box, int wbox, int num_sms,
-                             AdapterArgs<kAdapterSteps>* args, cudaStream_t s);
+                             int free_sms, AdapterArgs<kAdapterSteps>* args, cudaStream_t s);
 // First step with rows of their own: h and every row's adapter (of_row may be null).
 cudaError_t adapters_down_rows(const LinearParams& p, const AdapterParams& a, bool bf16, float* h, int32_t* of_row, cudaStream_t s);
 cudaError_t linear_adapters_tc(const LinearParams& p, const AdapterParams& a, int num_sms, cudaStream_t s);

@@ -438,7 +438,7 @@ cudaError_t launch_few(const LinearParams& p, const FewPlan& plan, const Adapter
   const size_t smem = size_t(a.stages) * stage + kBarBytes<kAdapt> + 1024;
   AdapterArgs<kAdapt> ad{};
   if constexpr (kAdapt == kAdapterSteps) {
-    const cudaError_t e = adapters_down_tc(p, *adapters, RowTiles(a.rows, a.sections, a.bn), a.bn, 128, num_sms, &ad, s);
+    const cudaError_t e = adapters_down_tc(p, *adapters, RowTiles(a.rows, a.sections, a.bn), a.bn, 128, num_sms, int(ctas < num_sms ? num_sms - ctas : 0), &ad, s);
     if (e != cudaSuccess) return e;
   }
   if constexpr (kAdapt == kAdapterRows) {

@@ -598,12 +598,12 @@ cudaError_t launch_pair(const LinearParams& p, int bn, const AdapterParams* adap
     if (p.residual) ok = ok && make_patch_map(&mr, p.residual, t.sections, t.rows, p.O);
   }
   if (!ok) return cudaErrorInvalidValue;
+  const int pairs = t.total < num_sms / 2 ? t.total : num_sms / 2;
   AdapterArgs<kAdapt> ad{};
   if constexpr (kAdapt) {
-    const cudaError_t e = adapters_down_tc(p, *adapters, RowTiles(t.rows, t.sections, 256), 128, t.bn / 2, num_sms, &ad, s);
+    const cudaError_t e = adapters_down_tc(p, *adapters, RowTiles(t.rows, t.sections, 256), 128, t.bn / 2, num_sms, num_sms - 2 * pairs, &ad, s);
     if (e != cudaSuccess) return e;
   }
-  const int pairs = t.total < num_sms / 2 ? t.total : num_sms / 2;
   switch (p.act) {
     case MCS_ACT_GELU_TANH: return start_pair<MCS_ACT_GELU_TANH>(mx, mw, my, mr, ad, p, t, pairs, s);
     case MCS_ACT_GELU_ERF: return start_pair<MCS_ACT_GELU_ERF>(mx, mw, my, mr, ad, p, t, pairs, s);
