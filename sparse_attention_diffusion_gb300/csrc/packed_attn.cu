@@ -418,12 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
 template <int D, typename T>
 __global__ void __launch_bounds__(256, 4) packed_join_kernel(const PackedParams p, const PackedWalk wk) {
-  grid_inputs_ready();
-  grid_let_next_start();
+  // The lengths are read before the wait for the pieces: the first kernel has waited for its own predecessor before it let
+  // this one start, so they are there. Every block waits, those without work too, as the next call may overwrite the
+  // workspace once this grid is done.
   const int lane = threadIdx.x & 31, tok = blockIdx.x;
   const int s = packed_find(p.q_start, p.S, wk.by_one, 0, tok, lane);
-  int q0, nq, k0, nk;
-  if (s < 0 || !packed_sequence(p, s, q0, nq, k0, nk) || tok < q0 || tok >= q0 + nq) return;
+  int q0 = 0, nq = 0, k0 = 0, nk = 0;
+  const bool mine = s >= 0 && packed_sequence(p, s, q0, nq, k0, nk) && tok >= q0 && tok < q0 + nq;
+  grid_inputs_ready();
+  grid_let_next_start();
+  if (!mine) return;
   const int i = tok - q0, iq = wk.by_tq.div(i), last = min((iq + 1) * p.tq, nq);
   const int seen = p.causal ? max(0, min(nk, last + nk - nq)) : nk;
   const int chunks = wk.by_chunk.div(seen + p.chunk - 1), slot = wk.by_chunk.div(k0) + s;

@@ -220,3 +220,19 @@ def test_many_segments():
     start = [i * rows // 2000 for i in range(2001)]
     Case("bf16", 1, rows, 128, 96, 16, start, [i % 6 - 2 for i in range(2000)], count=4).check()
     Case("f32", 1, rows, 128, 96, 16, start, [i % 6 - 2 for i in range(2000)], count=4).check()
+
+
+def test_two_streams_at_once():
+    """Calls that may run side by side, each with a workspace of its own."""
+    cases = [Case("bf16", 1, n, 512, 384, 32, [0, n // 2, n], [0, 2], seed=n) for n in (6000, 300)]
+    cases.append(Case("bf16", 1, 64, 512, 384, 16, list(range(65)), [i % 3 for i in range(64)], seed=64))
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cases], [[] for _ in cases]
+    for _ in range(20):
+        for c, s, out in zip(cases, streams, got):
+            with torch.cuda.stream(s):
+                out.append(c.run())
+    torch.cuda.synchronize()
+    for w, out in zip(want, got):
+        assert all(torch.equal(w, y) for y in out)

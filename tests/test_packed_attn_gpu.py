@@ -282,3 +282,82 @@ def test_other_device_is_refused():
     st = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         mcs.mcs_packed_attn(desc, q, q, q, st, st, torch.empty_like(q), None, mcs.packed_attn_workspace(desc))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+def test_masked_values_have_no_effect_in_cut_prompts(d, poison):
+    """The same where sequences of several tiles are cut along their keys."""
+    g = torch.Generator(device="cuda").manual_seed(20)
+    nq, nk = [70, 90, 80], [1100, 1300, 900]
+    qs, ks = starts(nq), starts(nk)
+    Tk = ks[-1] + 9
+    q, k, v = (view(g, h, n, d, torch.bfloat16, "heads", 2.0) for h, n in ((4, qs[-1]), (2, Tk), (2, Tk)))
+    desc = mcs.packed_desc(3, qs[-1], Tk, 4, 2, d, q.dtype, True, max(nq))
+    assert mcs.packed_attn_workspace(desc).numel() > 16  # the plan cuts
+    a = call(q, k, v, qs, ks, True, max(nq))
+    kp, vp = k.clone(), v.clone()
+    for x in (kp, vp):
+        x[:, ks[1]:ks[2]] = poison
+        x[:, ks[3]:] = poison
+        x[:, ks[3] - 1] = poison            # only the last query sees it
+    b = call(q, kp, vp, qs, ks, True, max(nq))
+    mcs.mcs_check_status()
+    keep = torch.ones(qs[-1], dtype=torch.bool, device="cuda")
+    keep[qs[1]:qs[2]] = False
+    keep[-1] = False
+    for x, y in zip(a, b):
+        assert torch.equal(x[:, keep], y[:, keep])
+        assert not torch.isfinite(y[:, ~keep].float()).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_values_that_some_rows_see_in_cut_prompts(d):
+    """100 queries behind 1,100 kept keys: query i sees the keys up to 1,100 + i."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    q, k, v = (view(g, 2, n, d, torch.bfloat16, "heads", 1.0) for n in (100, 1200, 1200))
+    q = torch.cat([q, q])  # two query heads a key head
+    desc = mcs.packed_desc(1, 100, 1200, 4, 2, d, q.dtype, True, 100)
+    assert mcs.packed_attn_workspace(desc).numel() > 16
+    v[0, 1150, 5], v[1, 1199, 63], v[1, 10, 0] = float("inf"), float("-inf"), float("nan")
+    o, _ = call(q, k, v, [0, 100], [0, 1200], True, 100)
+    want = torch.zeros((4, 100, d), device="cuda")
+    want[:2, 50:, 5], want[2:, 99:, 63], want[2:, :, 0] = float("inf"), float("-inf"), float("nan")
+    o = o.float()
+    assert torch.equal(torch.isfinite(o), torch.isfinite(want))
+    assert torch.equal(o[torch.isinf(want)], want[torch.isinf(want)])
+    assert torch.isnan(o[torch.isnan(want)]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_single_tokens_over_cut_keys(dtype):
+    """More sequences than a warp has lanes, a token each or none, over keys that are cut."""
+    g = torch.Generator(device="cuda").manual_seed(22)
+    nq = [0 if i % 11 == 5 else 1 for i in range(48)]
+    nk = [(137 * i * i) % 1900 if i % 7 else 0 for i in range(48)]
+    qs, ks = starts(nq), starts(nk)
+    q, k, v = view(g, 8, qs[-1], 128, DT[dtype], "tokens", 2.0), view(g, 2, ks[-1], 128, DT[dtype], "tokens"), view(g, 2, ks[-1], 128, DT[dtype], "heads")
+    desc = mcs.packed_desc(48, qs[-1], ks[-1], 8, 2, 128, DT[dtype], True, 1)
+    assert mcs.packed_attn_workspace(desc).numel() > 16
+    check(q, k, v, qs, ks, True, max_q=1)
+
+
+def test_two_streams_at_once():
+    """Calls that may run side by side, each with a workspace of its own."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+    calls = []
+    for nq, nk in (([1] * 6, [2000, 300, 1500, 40, 900, 1111]), ([300, 5, 200], [300, 5, 200])):
+        qs, ks = starts(nq), starts(nk)
+        q, k, v = view(g, 8, qs[-1], 128, torch.bfloat16, "tokens", 2.0), *(view(g, 2, ks[-1], 128, torch.bfloat16, "tokens") for _ in range(2))
+        calls.append((q, k, v, qs, ks, True, max(nq)))
+    want = [call(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(20):
+        for c, s, out in zip(calls, streams, got):
+            with torch.cuda.stream(s):
+                out.append(call(*c))
+    torch.cuda.synchronize()
+    for w, out in zip(want, got):
+        assert all(torch.equal(w[0], o) and torch.equal(w[1], l) for o, l in out)
