@@ -437,8 +437,23 @@ __global__ void __launch_bounds__(256, 4) packed_join_kernel(const PackedParams 
     auto at = [&](int c) { return ((static_cast<long long>(slot + c) * p.tiles + iq) * p.Hk + hk) * p.rows + row; };
     constexpr int kE = D / 32;
     float M = -INFINITY, l = 0.f, o[kE] = {};
+    auto read = [&](int c, float (&v)[kE]) {
+      const float* po = p.part_o + at(c) * D + lane * kE;
+      if constexpr (kE == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(po);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(po);
+        v[0] = x.x, v[1] = x.y;
+      }
+    };
     for (int c0 = 0; c0 < chunks; c0 += 32) {
       const float2 ml = c0 + lane < chunks ? p.part_ml[at(c0 + lane)] : make_float2(-INFINITY, 0.f);
+      constexpr int kFirst = 4;  // sums that are on their way while the maxima are compared
+      float first[kFirst][kE];
+  #pragma unroll
+      for (int c = 0; c < kFirst; ++c)
+        if (c0 + c < chunks) read(c0 + c, first[c]);
       float top = ml.x;
   #pragma unroll
       for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -452,23 +467,22 @@ __global__ void __launch_bounds__(256, 4) packed_join_kernel(const PackedParams 
       l = l * keep + sum;
   #pragma unroll
       for (int e = 0; e < kE; ++e) o[e] *= keep;
-      const int n = min(32, chunks - c0);
-  #pragma unroll 8
-      for (int c = 0; c < n; ++c) {
+      auto add = [&](int c, const float (&v)[kE]) {
         const float fc = __shfl_sync(0xffffffffu, f, c);
-        const float* po = p.part_o + at(c0 + c) * D + lane * kE;
-        float v[kE];
-        if constexpr (kE == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(po);
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(po);
-          v[0] = x.x, v[1] = x.y;
-        }
         if (fc != 0.f) {
   #pragma unroll
           for (int e = 0; e < kE; ++e) o[e] = fmaf(fc, v[e], o[e]);
         }
+      };
+      const int n = min(32, chunks - c0);
+  #pragma unroll
+      for (int c = 0; c < kFirst; ++c)
+        if (c < n) add(c, first[c]);
+  #pragma unroll 8
+      for (int c = kFirst; c < n; ++c) {
+        float v[kE];
+        read(c0 + c, v);
+        add(c, v);
       }
       M = Mn;
     }
