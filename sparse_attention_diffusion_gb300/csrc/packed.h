@@ -35,6 +35,7 @@ struct PackedParams {
   float scale_log2;       // scale * log2(e)
   int tq, rows;           // tokens and rows (tq * g) of a tile (of two tiles: pair)
   int pair;               // bf16, two tiles of 128 rows an item
+  int quarters;           // bf16, d = 64, items of 32 rows at most: every softmax warp a quarter of the keys
   int chunk;              // keys of a piece of a sequence, 0: sequences are not cut
   int tiles;              // with chunk > 0: query tiles of the longest sequence
   long long items;        // slots of all heads (and tiles)

@@ -43,7 +43,7 @@ constexpr int kThreads = 224;
 constexpr int kItems = 4;   // items found ahead
 constexpr int kFlags = 2;   // items whose V flags are kept: warp 6 is one item ahead of the way out at most
 
-template <int D>
+template <int D, bool kQuarters>
 struct Cfg {
   static constexpr int kStages = (D == 128) ? 3 : 6;
   static constexpr int kTile = (D / 64) * kRegion;
@@ -51,21 +51,28 @@ struct Cfg {
   static constexpr int kK = kQ + kTile;
   static constexpr int kV = kK + kStages * kTile;
   static constexpr int kBar = kV + kStages * kTile;
-  static constexpr int kNumBars = 4 * kStages + 2 + 2 + 2 + 2 + 2 + 2 * kItems + 2 + 1;
+  static constexpr int kNumBars = 4 * kStages + 2 + 2 + 2 + 2 + 2 + 2 * kItems + 2 + 1 + 1;
   static constexpr int kSteal = (kBar + kNumBars * 8 + 15) / 16 * 16;  // the answer to a request for a block
   static constexpr int kMisc = kSteal + 16;  // tensor-memory slot, flags, items
   static constexpr int kItem = (kMisc + 16 + kFlags * 4 + 15) / 16 * 16;
-  static constexpr int kBytes = kItem + kItems * int(sizeof(PackedItem));
+  static constexpr int kJoin = (kItem + kItems * int(sizeof(PackedItem)) + 127) / 128 * 128;  // 32 columns of four warps' sums,
+  static constexpr int kJoinMl = kJoin + 4 * 32 * 128;                                         // their maxima and sums of weights
+  static constexpr int kBytes = kQuarters ? kJoinMl + 4 * 32 * 8 : kJoin;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kColS = 0, kColO = 256, kColP = 384;
 };
-static_assert(Cfg<128>::kAlloc <= 227 * 1024 && Cfg<64>::kAlloc <= 227 * 1024, "shared memory");
+static_assert(Cfg<128, false>::kAlloc <= 227 * 1024 && Cfg<64, true>::kAlloc <= 227 * 1024, "shared memory");
 
-template <int D>
+// kQuarters: items of 32 rows at most, which lie four times in the tile, 32 rows apart: every softmax warp has all of them
+// and takes a quarter of a tile's keys, P being 0 for the others', and the four sums meet on the way out. One warp's softmax
+// of 128 keys (2,100 clocks a tile with its waits) bounded tokens of d = 64, whose tiles take 1,500 from HBM: 64 over
+// 16,384 keys and less of 8 heads 189 us with a softmax warp for all keys, 141 with four (0.94 of the copy bandwidth). With d = 128
+// a tile takes twice as long, and there is no shared memory for the sums.
+template <int D, bool kQuarters>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const PackedParams p, const PackedWalk wk) {
-  using L = Cfg<D>;
+  using L = Cfg<D, kQuarters>;
   constexpr int S = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -86,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* it_empty = it_full + kItems;
   uint64_t* drain = it_empty + kItems;  // [2]
   uint64_t* steal = drain + 2;
+  uint64_t* join = steal + 1;           // the softmax warps meet (kQuarters)
   const uint32_t steal_slot = sbase + L::kSteal;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* odd = tmem_slot + 4;  // [kFlags] the item's V held something that is not finite and not seen by all
@@ -97,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < S; ++s) mbar_init(k_full + s, 1), mbar_init(k_empty + s, 1), mbar_init(v_full + s, 1), mbar_init(v_empty + s, 1);
     for (int b = 0; b < 2; ++b) mbar_init(s_full + b, 1), mbar_init(s_free + b, 128), mbar_init(drain + b, 1);
     mbar_init(p_full, 128), mbar_init(p_empty, 1);
-    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(steal, 1);
+    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(steal, 1), mbar_init(join, 128);
     mbar_init(o_full, 2), mbar_init(o_free, 128);  // o_full: the products and the flag of V
     for (int b = 0; b < kItems; ++b) mbar_init(it_full + b, 1), mbar_init(it_empty + b, 4 + 2);
     fence_mbar_init();
@@ -170,10 +178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x > 0) continue;
         if (!(ok = warp_all(mbar_wait_short(q_empty, (uint32_t(live) & 1) ^ 1)))) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(q_full, uint32_t(p.rows * 128 * (D / 64)));
+          constexpr int kCopies = kQuarters ? 4 : 1;
+          mbar_arrive_expect_tx(q_full, uint32_t(p.rows * 128 * (D / 64) * kCopies));
 #pragma unroll
-          for (int rg = 0; rg < D / 64; ++rg)
-            tma_load_3d(sbase + L::kQ + rg * kRegion, &map_q, rg * 64, it.hk * p.g, it.q0, smem_u32(q_full));
+          for (int rg = 0; rg < D / 64 * kCopies; ++rg)
+            tma_load_3d(sbase + L::kQ + rg / kCopies * kRegion + rg % kCopies * 32 * 128, &map_q, rg / kCopies * 64, it.hk * p.g, it.q0,
+                        smem_u32(q_full));
         }
         __syncwarp();
         ++live;
@@ -262,6 +272,185 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(d, 0);
       }
     }
+    __syncwarp();
+  } else if constexpr (kQuarters) {
+    // ------------------------------------------------------------ softmax of a quarter of the keys, and the way out
+    const int t = p.by_group.div(lane), hh = lane - t * p.g;  // this row's token of the item and head of the group
+    const uint32_t lane_off = uint32_t(warp * 32) << 16;
+    const uint32_t tSw = tS + lane_off + warp * 32, tOw = tO + lane_off;
+    const float sl2 = p.scale_log2;
+    uint8_t* sums = smem + L::kJoin;
+    float2* ml = reinterpret_cast<float2*>(smem + L::kJoinMl);
+    bool ok = true;
+    int tile = 0, live = 0;
+    uint32_t met = 0;
+    auto meet = [&]() -> bool {
+      mbar_arrive(join);
+      return warp_all(mbar_wait_short(join, met++ & 1));
+    };
+    {
+      uint32_t zero[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) zero[c] = 0;
+      tmem_st64(tP + lane_off, zero);  // the other warps' keys, for good
+    }
+    for (int n = 0; ok; ++n) {
+      PackedItem it;
+      if (!(ok = take(n, it))) break;
+      if (it.tiles < 0) break;
+      const bool mine = t < it.ntok && lane < p.rows;
+      const int lim = mine ? visible_keys(it, p.causal, t) : it.nkeys;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < it.tiles; ++j, ++tile) {
+        const int b = tile & 1;
+        if (!(ok = warp_all(mbar_wait_short(s_full + b, uint32_t(tile >> 1) & 1)))) break;
+        tc_fence_after();
+        uint32_t r[32], pk[16];
+        tmem_ld32(tSw + b * 128, r);
+        tc_fence_before();
+        mbar_arrive(s_free + b);
+        const int nvalid = lim - j * 128 - warp * 32;
+        if (__any_sync(0xffffffffu, nvalid < 32)) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = i < nvalid ? r[i] : __float_as_uint(-INFINITY);
+        }
+        float mp[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mp[i] = __uint_as_float(r[i]);
+#pragma unroll
+        for (int c = 4; c < 32; c += 2) mp[(c >> 1) & 3] = fmax3(mp[(c >> 1) & 3], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+        const float m_new = fmaxf(m, fmax3(fmaxf(mp[0], mp[1]), mp[2], mp[3]) * sl2);
+        const bool need = m_new > m + 8.f;  // as below
+        const float m_use = need ? m_new : m;
+        const float alpha = need ? ex2_approx(m - m_new) : 1.f;
+        const float neg_m = m_use == -INFINITY ? 0.f : -m_use;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2), negmx2 = f2_pack(neg_m, neg_m);
+        uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float x0, x1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sl2x2, negmx2), x0, x1);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          ls2[c & 1] = f2_add(ls2[c & 1], f2_pack(p0, p1));
+          pk[c] = pack_bf16x2(p0, p1);
+        }
+        float la, lb;
+        f2_unpack(f2_add(ls2[0], ls2[1]), la, lb);
+        l = l * alpha + (la + lb);
+        m = m_use;
+        if (!(ok = warp_all(mbar_wait_short(p_empty, (uint32_t(tile) & 1) ^ 1)))) break;  // the last tile's P V is done
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, need && j > 0)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tOw + c * 32, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tOw + c * 32, o);
+          }
+        }
+        tmem_st16(tP + lane_off + warp * 16, pk);
+        tc_fence_before();
+        mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      if (it.tiles > 0) {
+        if (!(ok = warp_all(mbar_wait_short(o_full, uint32_t(live) & 1)))) break;
+        ++live;
+        tc_fence_after();
+      }
+      // 32 columns at a time: a warp leaves its sums of them, and adds the four warps' of eight
+      const bool cut = p.chunk > 0, extra = it.tiles > 0 && odd[n % kFlags] != 0;
+      const int h = it.hk * p.g + hh, all_see = visible_keys(it, p.causal, 0);
+      float M = -INFINITY, total = 0.f, f[4] = {};
+      ml[tid] = make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        if (it.tiles > 0) {
+          uint32_t u[32];
+          tmem_ld32(tOw + c * 32, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(sums + tid * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+        }
+        if (!(ok = meet())) break;
+        if (c == 0) {  // weights of the four as in packed_join_kernel
+          float2 x[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            x[w] = ml[w * 32 + lane];
+            M = fmaxf(M, x[w].x);
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            f[w] = x[w].y == 0.f ? 0.f : x[w].x == -INFINITY ? 1.f : fmaxf(ex2_approx(x[w].x - M), FLT_MIN);
+            total += x[w].y * f[w];
+          }
+        }
+        if (mine) {
+          const int col = c * 32 + warp * 8;
+          float o[8] = {};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            if (f[w] == 0.f) continue;  // no key, and what the sums hold then does not count
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float4 v = *reinterpret_cast<const float4*>(sums + (w * 32 + lane) * 128 + (((warp * 2 + i) ^ (lane & 7)) << 4));
+              o[4 * i] = fmaf(f[w], v.x, o[4 * i]), o[4 * i + 1] = fmaf(f[w], v.y, o[4 * i + 1]);
+              o[4 * i + 2] = fmaf(f[w], v.z, o[4 * i + 2]), o[4 * i + 3] = fmaf(f[w], v.w, o[4 * i + 3]);
+            }
+          }
+          const float inv = cut ? 1.f : total == 0.f ? 0.f : 1.f / total;  // rows that see nothing give 0
+          bool lost = false;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[i] *= inv;
+            lost |= !isfinite(o[i]);
+          }
+          // Elements of V that are not finite: those that only some rows see were left out of the products, and those that all
+          // see are NaN in the sums of the warps whose P is 0 there. Their sum is what the row gives, if its weights are numbers.
+          if (isfinite(total) && total != 0.f && (lost || extra)) {
+            const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(p.v) + static_cast<long long>(it.hk) * p.vs.head + col;
+            float e[8] = {};
+#pragma unroll 1
+            for (int j = lost ? 0 : all_see; j < lim; ++j) {
+              const uint4 v = *reinterpret_cast<const uint4*>(vc + static_cast<long long>(it.k0 + j) * p.vs.token);
+              if ((odd_bf16x2(v.x) | odd_bf16x2(v.y) | odd_bf16x2(v.z) | odd_bf16x2(v.w)) == 0) continue;
+              const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float y = __uint_as_float(i & 1 ? w4[i >> 1] & 0xffff0000u : w4[i >> 1] << 16);
+                if (!isfinite(y)) e[i] += y;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (!isfinite(e[i])) o[i] = e[i];
+          }
+          if (cut) {
+            float* prow = p.part_o + (it.part + lane) * D + col;
+            *reinterpret_cast<float4*>(prow) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(prow + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          } else {
+            __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(h) * p.os.head + static_cast<long long>(it.q0 + t) * p.os.token) + col;
+            *reinterpret_cast<uint4*>(orow) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+          }
+        }
+        if (!(ok = meet())) break;  // the place is free again
+      }
+      if (!ok) break;
+      if (mine && warp == 0) {
+        if (cut) p.part_ml[it.part + lane] = make_float2(M, total);
+        else if (p.lse != nullptr)
+          p.lse[static_cast<long long>(h) * p.Tq + it.q0 + t] = total == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + __log2f(total)) * kLn2;
+      }
+      if (it.tiles > 0) {
+        tc_fence_before();
+        mbar_arrive(o_free);
+      }
+    }
+    if (!ok && lane == 0) raise_status(st, kStatusTimeout);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax and the way out
@@ -505,15 +694,15 @@ __global__ void __launch_bounds__(256, 3) packed_join_kernel(const PackedParams 
   }
 }
 
-template <int D>
+template <int D, bool kQuarters>
 cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   if (!(make_view_map(&mq, p.q, p.H, p.Tq, D, p.qs, p.g, p.tq) && make_view_map(&mk, p.k, p.Hk, p.Tk, D, p.ks, 1, 128) &&
         make_view_map(&mv, p.v, p.Hk, p.Tk, D, p.vs, 1, 128)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<packed_attn_kernel<D>>(Cfg<D>::kAlloc);
+  const cudaError_t e = allow_smem<packed_attn_kernel<D, kQuarters>>(Cfg<D, kQuarters>::kAlloc);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(packed_attn_kernel<D>, dim3(unsigned(p.items)), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
+  return launch_overlapped(packed_attn_kernel<D, kQuarters>, dim3(unsigned(p.items)), kThreads, Cfg<D, kQuarters>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
 }
 
 }  // namespace
@@ -532,6 +721,8 @@ bool plan_packed(PackedParams* p, bool bf16) {
     const long long tiles64 = static_cast<long long>(p->Tq) / (64 / p->g) + p->S;
     if (static_cast<long long>(p->max_q) * p->g <= 16 || tiles64 * p->Hk < kSms) rows = 16;
   }
+  p->quarters = bf16 && p->d == 64 && static_cast<long long>(p->max_q) * p->g <= 32;
+  if (p->quarters) rows = 32;
   p->tq = rows / p->g;
   p->pair = bf16 && p->max_q > p->tq;
   if (p->pair) p->tq *= 2;
@@ -569,7 +760,7 @@ size_t packed_workspace_bytes(const PackedParams& p) {
 
 cudaError_t packed_attn_tc(const PackedParams& p, cudaStream_t s) {
   if (p.pair) return packed_attn_pair(p, s);
-  const cudaError_t e = p.d == 128 ? launch_tc<128>(p, s) : launch_tc<64>(p, s);
+  const cudaError_t e = p.d == 128 ? launch_tc<128, false>(p, s) : p.quarters ? launch_tc<64, true>(p, s) : launch_tc<64, false>(p, s);
   return e != cudaSuccess || p.chunk == 0 ? e : packed_join(p, true, s);
 }
 

@@ -361,3 +361,85 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for w, out in zip(want, got):
         assert all(torch.equal(w[0], o) and torch.equal(w[1], l) for o, l in out)
+
+
+@pytest.mark.parametrize("group,nq,nk", [
+    (1, [32, 7, 0, 1], [32, 300, 40, 129]), (5, [6, 1, 3], [700, 900, 640]), (32, [1, 1, 0, 1], [1, 31, 64, 2500]),
+    (8, [4, 4], [127, 3]), (2, [16, 5], [1000, 1030]), (4, [0 if i % 11 == 5 else 1 for i in range(48)], [(137 * i * i) % 1900 if i % 7 else 0 for i in range(48)]),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_rows(group, nq, nk, causal):
+    """Up to 32 rows a sequence with d = 64: four warps share a tile's keys."""
+    g = torch.Generator(device="cuda").manual_seed(24)
+    qs, ks = starts(nq), starts(nk)
+    q, k, v = view(g, 2 * group, qs[-1], 64, torch.bfloat16, "tokens", 2.0), view(g, 2, ks[-1], 64, torch.bfloat16, "tokens"), view(g, 2, ks[-1], 64, torch.bfloat16, "heads")
+    check(q, k, v, qs, ks, causal, max_q=max(nq))
+    check(q, k, v, qs, ks, causal, max_q=max(nq), scale=0.6, out="tokens")
+
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+def test_few_rows_masked_values_have_no_effect(cut, poison):
+    g = torch.Generator(device="cuda").manual_seed(25)
+    nq, nk = [2, 2, 2], [700, 1000, 600] if cut else [90, 70, 150]
+    qs, ks = starts(nq), starts(nk)
+    Tk = ks[-1] + 9
+    q, k, v = (view(g, h, n, 64, torch.bfloat16, "heads", 2.0) for h, n in ((4, qs[-1]), (2, Tk), (2, Tk)))
+    a = call(q, k, v, qs, ks, True, 2)
+    kp, vp = k.clone(), v.clone()
+    for x in (kp, vp):
+        x[:, ks[1]:ks[2]] = poison
+        x[:, ks[3]:] = poison
+        x[:, ks[3] - 1] = poison
+    b = call(q, kp, vp, qs, ks, True, 2)
+    mcs.mcs_check_status()
+    keep = torch.ones(qs[-1], dtype=torch.bool, device="cuda")
+    keep[qs[1]:qs[2]] = False
+    keep[-1] = False
+    for x, y in zip(a, b):
+        assert torch.equal(x[:, keep], y[:, keep])
+        assert not torch.isfinite(y[:, ~keep].float()).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nk", [300, 1200])
+def test_few_rows_infinite_values(d, nk):
+    """4 queries, of which the i-th sees the keys up to nk - 4 + i: values that are not finite reach the rows that see them,
+    in their columns, with their signs; two of unlike sign give NaN."""
+    inf, nan = float("inf"), float("nan")
+    g = torch.Generator(device="cuda").manual_seed(26)
+    q, k, v = (view(g, h, n, d, torch.bfloat16, "heads", 1.0) for h, n in ((4, 4), (2, nk), (2, nk)))
+    clean, lse = call(q, k, v, [0, 4], [0, nk], True, 4)
+    v[0, 200, 5], v[0, 40, 6], v[0, 41, 6], v[1, 10, 0] = inf, inf, -inf, nan
+    v[1, nk - 2, 63], v[1, 7, 31] = -inf, -inf
+    o, l = call(q, k, v, [0, 4], [0, nk], True, 4)
+    want = clean.float().clone()
+    want[:2, :, 5], want[:2, :, 6], want[2:, :, 0], want[2:, 2:, 63], want[2:, :, 31] = inf, nan, nan, -inf, -inf
+    assert torch.equal(torch.nan_to_num(o.float(), 123.0, 1e30, -1e30), torch.nan_to_num(want, 123.0, 1e30, -1e30))
+    assert torch.equal(l, lse)
+
+
+def test_few_rows_captured_graph():
+    """Lengths that change between replays, with and without cuts."""
+    g = torch.Generator(device="cuda").manual_seed(27)
+    for most, cases in ((4000, [([0, 2, 6], [0, 1000, 4000]), ([0, 5, 6], [0, 3900, 3950]), ([0, 0, 3], [0, 0, 2500])]),
+                        (300, [([0, 2, 6], [0, 100, 300]), ([0, 5, 6], [0, 290, 291]), ([0, 0, 3], [0, 0, 129])])):
+        q, k, v = view(g, 8, 6, 64, torch.bfloat16, "tokens", 2.0), *(view(g, 2, most, 64, torch.bfloat16, "tokens") for _ in range(2))
+        want = [call(q, k, v, a, b, True) for a, b in cases]
+        desc = mcs.packed_desc(2, 6, most, 8, 2, 64, q.dtype)
+        ws = mcs.packed_attn_workspace(desc)
+        qs, ks = (torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(2))
+        o, lse = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+        graph = torch.cuda.CUDAGraph()
+        mcs.mcs_packed_attn(desc, q, k, v, qs, ks, o, lse, ws)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            mcs.mcs_packed_attn(desc, q, k, v, qs, ks, o, lse, ws)
+        for (a, b), (wo, wl) in zip(cases, want):
+            qs.copy_(torch.tensor(a)), ks.copy_(torch.tensor(b))
+            o.fill_(7.0), lse.fill_(7.0)
+            ws.fill_(255)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+    mcs.mcs_check_status()
