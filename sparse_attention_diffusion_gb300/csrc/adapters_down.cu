@@ -6,7 +6,7 @@
 // fp32 accumulator [128 rows x R] in tensor memory, whose sums the cluster joins through distributed shared memory,
 // ranks in order. 192 threads: warp 0 copies, warp 1 MMAs, warps 2-5 look over their share of up_a meanwhile and
 // then bring the accumulator out, all six add and write. Reading x once bounds it: 75,600 x 5,120 with rank 32 in 115 us
-// = 6.7 TB/s, 32,768 x 1,536 with rank 64 in 24 us, 452 x 4,096 in 10 us.
+// = 6.7 TB/s, 32,768 x 1,536 with rank 64 in 25 us.
 #include <algorithm>
 
 #include "adapters.h"

@@ -100,7 +100,7 @@ cudaError_t linear_adapters_f32(const LinearParams& p, const AdapterParams& a, i
   int32_t* of_row = reinterpret_cast<int32_t*>(z + (size_t(p.M) * p.O + 63) / 64 * 64);
   cudaError_t e = adapters_down_rows(p, a, false, h, of_row, s);
   if (e != cudaSuccess) return e;
-  // a tile of 64 rows goes through its segments one by one (70 rows with adapters of their own: 88 us in all, 25 row by row)
+  // a tile of 64 rows goes through its segments one by one (70 rows with adapters of their own: 88 us in all, 31 row by row)
   if (p.M <= 4ll * a.S)
     e = launch_overlapped(adapters_f32_up_rows_kernel, dim3(unsigned(p.M), (p.O + 255) / 256), 256, 0, s, 0, p, a, h, of_row, z);
   else

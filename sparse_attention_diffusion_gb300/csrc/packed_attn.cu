@@ -23,8 +23,9 @@
 // maximum and sum, and a second launch joins them.
 //
 // This kernel is for sequences of one tile, single tokens over kept keys above all; longer ones go two tiles at a time
-// (packed_pair.cu). Measured: 64 tokens over 292 to 16,384 keys of 8 heads, d = 128: 268 us = 6.68 TB/s, 0.985 of the measured copy
-// bandwidth (302 us with items dealt out in advance); one token over 4,000 keys 14.7 us, of which the join is half.
+// (packed_pair.cu). Measured: 64 tokens over 292 to 16,384 keys of 8 heads, d = 128: 263 to 266 us = 6.74 to 6.81 TB/s, as fast as
+// the measured copy (302 us with items dealt out in advance, 268 before the join read ahead); one token over 4,000 keys 11.4 us.
+#include <algorithm>
 #include <cfloat>
 
 #include "attn_common.cuh"
@@ -707,12 +708,16 @@ cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Tiles and chunks. A tile takes as many tokens as fit in 128 rows; on the CUDA cores in 64, or in 16 where a sequence has
-// no more or the tiles of 64 are fewer than the SMs (77 tokens of 2 x 2 heads 13.9 us with 64 rows, 7.9 with 16).
-// Sequences are cut where the tiles alone do not fill the GPU and a sequence has many keys: into pieces of which
-// every SM gets eight where a sequence is one tile (64 tokens over 16,384 keys and less: 294 us with four, 280 with eight,
-// 284 with sixteen), otherwise two, as every tile of a sequence leaves its sums (seven chunks of 300 tokens and less: 61
-// us with one, 57 with two or four, 70 with eight). Sequences of more than one tile go two tiles at a time.
+// Tiles and chunks. A tile takes as many tokens as fit in 128 rows (32: see kQuarters); on the CUDA cores in 64, or in 16 where
+// a sequence has no more or the tiles of 64 are fewer than the SMs (77 tokens of 2 x 2 heads 13.9 us with 64 rows, 9.9 with 16).
+// Sequences are cut where the tiles alone do not fill the GPU and a sequence has many keys. Where a sequence is one tile every
+// SM gets eight pieces (64 tokens over 16,384 keys and less 288 us with four, 268 with eight, 265 with sixteen; but 128 over
+// 2,000 keys and less 83 us with eight, 93 with sixteen, eight over 30,000 and less 74 and 101), unless they would be shorter than
+// eight tiles: then one round of pieces, or pieces of eight tiles (16 tokens over 4,000 keys and less of 16 heads, d = 64, 34 us in pieces
+// of two tiles, 24 so; three over 20,000 and less of 8 heads, d = 128, 22 and 17; the CUDA cores
+// rather have the short ones: 32 tokens over 4,000 keys and less of 4 heads 204 us so, 171 without). Otherwise two an SM, as every tile
+// of a sequence leaves its sums (seven chunks of 300 tokens and less: 49 us with one, 45 with two, 53 with four, 65 with eight).
+// Sequences of more than one tile go two tiles at a time.
 bool plan_packed(PackedParams* p, bool bf16) {
   constexpr int kSms = 152;
   p->g = p->H / p->Hk;
@@ -739,6 +744,9 @@ bool plan_packed(PackedParams* p, bool bf16) {
   if (keys >= 4 * piece && tiles <= 64 && (most * p->Hk < 2 * kSms || (tiles == 1 && most * p->Hk < 8 * kSms))) {
     const long long work = most * keys * p->Hk, each = tiles == 1 ? 8 : 2;
     long long chunk = (work / (each * kSms) + piece - 1) / piece * piece;
+    // short pieces: rather one round of the SMs than eight
+    const long long round = (work / kSms + piece - 1) / piece * piece;
+    if (bf16 && tiles == 1) chunk = std::max(chunk, std::min(round, 8ll * piece));
     if (chunk < 2 * piece) chunk = 2 * piece;
     p->chunk = int(chunk < (1 << 30) ? chunk : (1 << 30));
     p->tiles = int(tiles);

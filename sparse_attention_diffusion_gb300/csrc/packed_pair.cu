@@ -14,17 +14,17 @@
 // A wait takes a product warp 200 to 300 clocks beside eight softmax warps even where nothing is to be waited for, as much
 // as the products in the queue hide. So warp 15 looks after everything that a step needs (keys, values, a free O) and
 // arrives together with the softmax's threads, and the turn is handed over before the last products are taken in. From one
-// warp, A's step and then B's, a pair of tiles took 3,170 clocks, now 2,900, of which the products take 2,048. P handed over
-// in two halves was slower (2,450 us instead of 2,260 for 32,768 causal tokens), and the last tile's maximum as a first
-// guess, checked afterwards, no faster.
+// warp, A's step and then B's, 32,768 causal tokens took 2,255 us. P handed over
+// in two halves was slower (2,450 us instead of 2,260), and the last tile's maximum as a first guess, checked
+// afterwards, no faster (2,270).
 // Tensor memory: S_A, S_B, O_A, O_B of 128 columns each, P_j written over S_j (a row per lane, so a thread overwrites only
 // what it has read); the products of one warp run in order, so S_{j+1} cannot meet P_j.
 // A sees fewer keys than B under a causal mask and leaves its last tiles out. Softmax warps take the registers that the
 // others hand over (128 at launch; 184, 96 on the way out, 48).
 //
-// Measured: 32,768 causal tokens of 12 heads on 4, d = 128: 2,167 us, 1,523 TFLOP/s at 1,910 MHz (0.87 of the sustained
-// rate of plain products); three full sequences of 7,716, 4,031 and 1,626 tokens, 12 heads: 342 us, 1,410 TFLOP/s; 16 causal
-// prompts of 6 to 839 tokens, 32 heads on 8: 54 us. There the instructions count: with 62 KB of them, unrolled masks and
+// Measured: 32,768 causal tokens of 12 heads on 4, d = 128: 2,160 to 2,180 us, 1,510 to 1,525 TFLOP/s at 1,910 to 1,940 MHz
+// (0.86 to 0.87 of the sustained rate of plain products); three full sequences of 7,716, 4,031 and 1,626 tokens, 12 heads: 338
+// us, 1,426 TFLOP/s, tensor pipe 64 % active; 16 causal prompts of 6 to 839 tokens, 32 heads on 8: 50 us, pipe 26 %. There the instructions count: with 62 KB of them, unrolled masks and
 // 40 for every wait, a quarter of the fetches missed the instruction cache and the same prompts took 99 us.
 #include "attn_common.cuh"
 #include "common.cuh"
