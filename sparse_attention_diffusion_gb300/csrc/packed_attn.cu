@@ -23,8 +23,8 @@
 // maximum and sum, and a second launch joins them.
 //
 // This kernel is for sequences of one tile, single tokens over kept keys above all; longer ones go two tiles at a time
-// (packed_pair.cu). Measured: 64 tokens over 292 to 16,384 keys of 8 heads, d = 128: 263 to 266 us = 6.74 to 6.81 TB/s, as fast as
-// the measured copy (302 us with items dealt out in advance, 268 before the join read ahead); one token over 4,000 keys 11.4 us.
+// (packed_pair.cu). Measured: 64 tokens over 88 to 16,343 keys of 8 heads, d = 128: 263 to 266 us = 6.74 to 6.81 TB/s, as fast as
+// the measured copy (302 us with items dealt out in advance and larger pieces); one token over 4,000 keys 11.4 us.
 #include <algorithm>
 #include <cfloat>
 
