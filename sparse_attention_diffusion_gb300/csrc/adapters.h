@@ -63,6 +63,7 @@ struct AdapterView {
   const uint8_t* odd;     // [S][kAdapterPieces] share of `up` that is not finite
   int count, R, S, M;
   int halves_splits;      // blocks of the first kernel a slab (each takes a share of `up`)
+  int more_shares;        // blocks a segment that take nothing else
   RowTiles tiles;
   Divisor by_one;
 };
@@ -118,7 +119,7 @@ __device__ __forceinline__ bool segment_rows(const int32_t* start, int s, int M,
 }
 // Shares in which the `up` of a segment over rows a .. b - 1 (not none) is looked over.
 __device__ __forceinline__ int up_shares(const AdapterView& v, int a, int b) {
-  return min(kAdapterPieces, (v.tiles.of(b - 1) - v.tiles.of(a) + 1) * v.halves_splits);
+  return min(kAdapterPieces, (v.tiles.of(b - 1) - v.tiles.of(a) + 1) * v.halves_splits + v.more_shares);
 }
 // Calls f(segment, adapter, odd) for every segment with an adapter in rows row0 .. row1 - 1; one warp, all lanes.
 template <typename F>

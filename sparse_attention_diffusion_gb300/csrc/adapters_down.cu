@@ -36,6 +36,7 @@ struct DownArgs {
   long long up_elems;     // of one adapter
   int K, heads, col_mask, head_shift;
   int halves, splits, rn; // 128-row halves of a slab; R rounded up to the MMA's 16 columns
+  int units;              // halves of all slabs; the clusters behind them only look over `up`
   int stages;
   uint32_t tmem_cols;
   uint32_t* status;
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   // The segment of this slot: the last whose first slot is not above it; every warp finds it for itself.
   int seg = -1, ad = -1, rt = 0, ra = 0, rb = 0, r0 = 0, r1 = 0;
-  {
+  if (unit < a.units) {
     int lo = 0, n = v.S;
     while (true) {
       const int jump = (n + 31) >> 5, at = lane * jump;
@@ -114,6 +115,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     live = rt >= v.tiles.of(ra) && rt <= v.tiles.of(rb - 1);
     ad = v.which[seg];
     live = live && ad >= 0 && ad < v.count;
+  }
+  int share = live ? ((rt - v.tiles.of(ra)) * a.halves + half) * a.splits + rank : -1;  // of the adapter's `up`
+  if (unit >= a.units) {
+    const int more = v.more_shares / a.splits;  // clusters a segment
+    seg = (unit - a.units) / more;
+    if (segment_rows(v.start, seg, v.M, ra, rb) && ra < rb) {
+      ad = v.which[seg];
+      if (ad >= 0 && ad < v.count)
+        share = (v.tiles.of(rb - 1) - v.tiles.of(ra) + 1) * v.halves_splits + (unit - a.units - seg * more) * a.splits + rank;
+    }
   }
   // rows of this half of the slab that are the segment's, counted from the half's first row
   const int height = min(128, v.tiles.height - half * 128);
@@ -188,23 +199,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
   } else if (warp >= 2) {
-    if (live) {  // this block's share of the adapter's `up`
-      const int shares = up_shares(v, ra, rb), mine = ((rt - v.tiles.of(ra)) * a.halves + half) * a.splits + rank;
-      if (mine < shares) {
-        const long long words = a.up_elems / 8;  // R is a multiple of 8
-        const long long w0 = words * mine / shares, w1 = words * (mine + 1) / shares;
-        const uint4* up = reinterpret_cast<const uint4*>(a.up + size_t(ad) * a.up_elems);
-        bool odd = false;
-#pragma unroll 4
-        for (long long w = w0 + tid - 64; w < w1; w += 128) odd |= not_finite(__ldg(up + w));
-        // warps 2 to 5 meet on their own barrier
-        uint32_t any;
-        asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-                     : "=r"(any)
-                     : "r"(uint32_t(odd))
-                     : "memory");
-        if (tid == 64) a.odd[size_t(seg) * kAdapterPieces + mine] = uint8_t(any);
+    if (const int shares = share >= 0 ? up_shares(v, ra, rb) : 0; share >= 0 && share < shares) {
+      const long long words = a.up_elems / 8;  // R is a multiple of 8
+      const long long w0 = words * share / shares, w1 = words * (share + 1) / shares;
+      const uint4* up = reinterpret_cast<const uint4*>(a.up + size_t(ad) * a.up_elems);
+      bool odd = false;
+      // sixteen reads in flight
+      for (long long w = w0 + tid - 64; w < w1; w += 16 * 128) {
+        uint4 x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = w + i * 128 < w1 ? __ldg(up + w + i * 128) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd |= not_finite(x[i]);
       }
+      // warps 2 to 5 meet on their own barrier
+      uint32_t any;
+      asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                   : "=r"(any)
+                   : "r"(uint32_t(odd))
+                   : "memory");
+      if (tid == 64) a.odd[size_t(seg) * kAdapterPieces + share] = uint8_t(any);
     }
     if (rows) {
       if ((ok = warp_all(mbar_wait(done, 0, st)))) {
@@ -304,15 +318,26 @@ cudaError_t adapters_down_tc(const LinearParams& p, const AdapterParams& a, cons
   d.rn = (a.R + 15) / 16 * 16;
   d.K = p.K;
   d.heads = p.heads;
-  // K slices: about two blocks an SM, at least four steps each; slots that hold nothing leave at once. Beside a product that
-  // leaves SMs free no more than those: its blocks take an SM each and would wait for these (452 x 4,096 -> 5,120 with two
-  // adapters 27 us with eight slices, 25 with two).
-  const long long most = free_sms > 0 ? free_sms : 2ll * num_sms;
+  // K slices of four steps at least; slots that hold nothing leave at once. Beside a product that leaves SMs free (its blocks take
+  // an SM each and would wait for these) two blocks on each of those: 452 x 4,096 -> 5,120 with two adapters 27 us with
+  // eight slices, 25 with four or two. Where two slices have no room there, the product waits for the sums anyway, and two blocks
+  // on every SM bring them soonest (512 x 4,096 -> 9,472 with two adapters of rank 256 220 us with one slice, 68 with
+  // more, 52 with the blocks below).
   const int nk = (p.K + 63) / 64;
   const long long units = static_cast<long long>(slots) * d.halves;
+  const bool beside = units * 2 <= 2ll * free_sms;
+  const long long most = 2ll * (beside ? free_sms : num_sms);
   d.splits = 1;
   while (d.splits < 8 && units * d.splits * 2 <= most && nk >= d.splits * 2 * 4) d.splits *= 2;
-  if (units * d.splits > INT32_MAX) return cudaErrorInvalidValue;
+  // Clusters that only look over `up`, as many a segment as give shares of 16 KB, where the SMs have room (beside a product one on
+  // each, as blocks go to empty SMs first, unless the shares are long without them: 512 x 4,096 -> 8,960, rank 32, 38 us with two and
+  // 31 with one, 256 x 1,536 -> 8,960, rank 128, 26 us with two and 36 with none).
+  const long long up_bytes = static_cast<long long>(p.O) * a.R * 2, room = (beside && up_bytes / (d.halves * d.splits) < 160 * 1024 ? free_sms : most) - units * d.splits;
+  const long long want = std::min<long long>(kAdapterPieces, up_bytes >> 14) - d.halves * d.splits;
+  const int more = int(std::max(0ll, std::min(want / d.splits, room / (static_cast<long long>(a.S) * d.splits))));
+  d.units = int(units);
+  const long long grid = (units + static_cast<long long>(more) * a.S) * d.splits;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const int stage = kXTile + d.rn * 128;
   const int per_rank = (nk + d.splits - 1) / d.splits;
   d.stages = std::min({kMaxStages, (108 * 1024) / stage, std::max(2, per_rank)});
@@ -325,7 +350,7 @@ cudaError_t adapters_down_tc(const LinearParams& p, const AdapterParams& a, cons
   d.mask = reinterpret_cast<__nv_bfloat16*>(ws + align256(rows_all * 2 * a.R * 2));
   d.odd = reinterpret_cast<uint8_t*>(ws + align256(rows_all * 2 * a.R * 2) + align256(rows_all * 8 * 2));
   if (rows > rows_all) return cudaErrorInvalidValue;
-  d.v = {a.start, a.which, d.odd, a.count, a.R, a.S, p.M, d.halves * d.splits, t, Divisor(1)};
+  d.v = {a.start, a.which, d.odd, a.count, a.R, a.S, p.M, d.halves * d.splits, more * d.splits, t, Divisor(1)};
   d.up = static_cast<const __nv_bfloat16*>(a.up);
   d.up_elems = static_cast<long long>(p.O) * a.R;
   d.scale = a.scale;
@@ -349,7 +374,7 @@ cudaError_t adapters_down_tc(const LinearParams& p, const AdapterParams& a, cons
   const size_t smem = size_t(d.stages) * stage + kBarBytes + 1024;
   const cudaError_t e = allow_smem<adapters_down_kernel>(226 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(adapters_down_kernel, dim3(unsigned(units * d.splits)), kThreads, smem, s, unsigned(d.splits), mx, md, d);
+  return launch_overlapped(adapters_down_kernel, dim3(unsigned(grid)), kThreads, smem, s, unsigned(d.splits), mx, md, d);
 }
 
 }  // namespace mcs

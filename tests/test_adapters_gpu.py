@@ -236,3 +236,24 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for w, out in zip(want, got):
         assert all(torch.equal(w, y) for y in out)
+
+
+@pytest.mark.parametrize("rows,dout,rank", [(256, 9000, 128), (700, 4096, 256), (60, 12000, 64), (6000, 512, 16)])
+def test_large_up_is_looked_over_to_its_end(rows, dout, rank):
+    """An element that is not finite anywhere in an adapter's `up` stays in its own rows."""
+    cuts = [0, rows // 3, rows // 3 + 2, rows]
+    c = Case("bf16", 1, rows, 256, dout, rank, cuts, [0, 1, 2])
+    c.check()
+    a = c.run()
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[cuts[1]:cuts[2]] = False
+    up = c.up[1].view(-1)
+    for at in (0, up.numel() // 3 + 5, up.numel() // 2 + 7, up.numel() * 63 // 64, up.numel() - 1):
+        old = up[at].item()
+        up[at] = float("inf")
+        b = c.run()
+        up[at] = old
+        assert torch.equal(a[:, keep], b[:, keep])
+        assert not torch.isfinite(b[:, ~keep].float()).all()
+    mcs.mcs_check_status()
+    assert torch.equal(c.run(), a)
