@@ -332,7 +332,8 @@ cudaError_t adapters_down_tc(const LinearParams& p, const AdapterParams& a, cons
   // Clusters that only look over `up`, as many a segment as give shares of 16 KB, where the SMs have room (beside a product one on
   // each, as blocks go to empty SMs first, unless the shares are long without them: 512 x 4,096 -> 8,960, rank 32, 38 us with two and
   // 31 with one, 256 x 1,536 -> 8,960, rank 128, 26 us with two and 36 with none).
-  const long long up_bytes = static_cast<long long>(p.O) * a.R * 2, room = (beside && up_bytes / (d.halves * d.splits) < 160 * 1024 ? free_sms : most) - units * d.splits;
+  const long long up_bytes = static_cast<long long>(p.O) * a.R * 2;
+  const long long room = (beside && up_bytes / (d.halves * d.splits) < 160 * 1024 ? free_sms : most) - units * d.splits;
   const long long want = std::min<long long>(kAdapterPieces, up_bytes >> 14) - d.halves * d.splits;
   const int more = int(std::max(0ll, std::min(want / d.splits, room / (static_cast<long long>(a.S) * d.splits))));
   d.units = int(units);

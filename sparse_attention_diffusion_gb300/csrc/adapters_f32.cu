@@ -10,7 +10,92 @@
 namespace mcs {
 namespace {
 
+// h = scale_a x down_a^T where many rows share an adapter: 64 rows and kCols columns of h a block, 4 x kCols / 16 a thread, 32 columns
+// of x at a time, the next ones on their way meanwhile.
+template <int kCols>
+__global__ void __launch_bounds__(256) adapters_f32_down_kernel(const LinearParams p, const AdapterParams a, float* h, const int hd) {
+  constexpr int kRows = 64, kK = 32, kPitch = kK + 4, kJ = kCols / 16;
+  __shared__ __align__(16) float xs[kRows][kPitch], ds[kCols][kPitch];
+  const int tid = threadIdx.x, lane = tid & 31, ty = tid >> 4, tx = tid & 15;
+  const long long m0 = static_cast<long long>(blockIdx.x) * kRows;
+  const int c0 = blockIdx.y * kCols;
+  grid_inputs_ready();
+  grid_let_next_start();
+  if (blockIdx.y == 0 && tid < 32) {
+    for (long long s = static_cast<long long>(blockIdx.x) * 32 + lane; s < a.S; s += static_cast<long long>(gridDim.x) * 32) {
+      int x, y;
+      if (!segment_rows(a.start, int(s), p.M, x, y) || a.which[s] >= a.count) raise_status(p.status, kStatusBounds);
+    }
+  }
+  const int m1 = int(min(static_cast<long long>(p.M), m0 + kRows));
+  const int row = tid >> 3, q4 = (tid & 7) * 4;  // loads: rows `row` and `row` + 32, four columns from q4 on
+  const long long head = static_cast<long long>(p.N) * hd;  // from one head's column to the next head's
+  const float* x[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = min(int(m0) + row + 32 * i, p.M - 1), b = m / p.N;
+    x[i] = static_cast<const float*>(p.x) + (p.heads > 0 ? b * p.heads * head + static_cast<long long>(m - b * p.N) * hd
+                                                         : static_cast<long long>(m) * p.K);
+  }
+  for (int s = max(0, segment_at(a.start, a.S, int(m0), lane)); s < a.S; ++s) {
+    if (a.start[s] >= m1) break;
+    int ra, rb;
+    segment_rows(a.start, s, p.M, ra, rb);
+    const int lo = max(ra, int(m0)), hi = min(rb, m1);
+    if (lo >= hi) continue;
+    const int ad = a.which[s];
+    if (ad < 0 || ad >= a.count) continue;
+    const float* down = static_cast<const float*>(a.down) + static_cast<size_t>(ad) * a.R * p.K;
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 xv[2], dv[2];
+    auto fetch = [&](int k0) {
+      const int k = k0 + q4, q = p.heads > 0 ? k / hd : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        xv[i] = k < p.K ? *reinterpret_cast<const float4*>(x[i] + (q * head + (k - q * hd))) : none;
+        const int c = row + 32 * i;
+        dv[i] = k < p.K && c < kCols && c0 + c < a.R ? __ldg(reinterpret_cast<const float4*>(down + static_cast<size_t>(c0 + c) * p.K + k)) : none;
+      }
+    };
+    float acc[4][kJ] = {};
+    fetch(0);
+    for (int k0 = 0; k0 < p.K; k0 += kK) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<float4*>(&xs[row + 32 * i][q4]) = xv[i];
+        if (row + 32 * i < kCols) *reinterpret_cast<float4*>(&ds[row + 32 * i][q4]) = dv[i];
+      }
+      __syncthreads();
+      if (k0 + kK < p.K) fetch(k0 + kK);
+#pragma unroll
+      for (int k = 0; k < kK; k += 4) {
+        float4 u[kJ];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) u[j] = *reinterpret_cast<const float4*>(&ds[tx + 16 * j][k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 w = *reinterpret_cast<const float4*>(&xs[ty * 4 + i][k]);
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+            acc[i][j] = fmaf(w.w, u[j].w, fmaf(w.z, u[j].z, fmaf(w.y, u[j].y, fmaf(w.x, u[j].x, acc[i][j]))));
+        }
+      }
+    }
+    const float sc = a.scale[ad];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = int(m0) + ty * 4 + i;
+      if (m < lo || m >= hi) continue;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+        if (const int c = c0 + tx + 16 * j; c < a.R) h[static_cast<size_t>(m) * a.R + c] = sc * acc[i][j];
+    }
+  }
+}
+
 // z = h up_a^T, 0 in rows without an adapter: 64 x 64 outputs a block, 4 x 4 a thread, 16 columns of R at a time.
+constexpr int kManyRows = 2048;
 constexpr int kTile = 64, kStep = 16, kLd = kStep + 4;
 __global__ void __launch_bounds__(256) adapters_f32_up_kernel(const LinearParams p, const AdapterParams a, const float* h, float* z) {
   __shared__ __align__(16) float hs[kTile][kLd], us[kTile][kLd];
@@ -98,10 +183,25 @@ cudaError_t linear_adapters_f32(const LinearParams& p, const AdapterParams& a, i
   float* h = static_cast<float*>(a.ws);
   float* z = h + (size_t(p.M) * a.R + 63) / 64 * 64;
   int32_t* of_row = reinterpret_cast<int32_t*>(z + (size_t(p.M) * p.O + 63) / 64 * 64);
-  cudaError_t e = adapters_down_rows(p, a, false, h, of_row, s);
+  const long long M = p.M, S = a.S;
+  // Second step row by row, whose threads read `up` again for every row: 70 rows with adapters of their own 31 us in all, 88 by
+  // tiles of 64 rows, which go through their segments one by one; 300 rows of 30 segments to 300 outputs 15 and 23.
+  const bool single = M <= 4 * S || (M <= 16 * S && M * p.O * a.R <= (16ll << 20));
+  // First step by tiles: rows that share adapters, and enough tiles to fill the GPU (x 1,536 -> 1,536, rank 64, 2,000 rows: 216 us in
+  // all, 134 four rows at a time; rank 32, 4,096 rows: 165 and 178; 74,156 x 128 -> 16, rank 72: 156 and 1,182).
+  const bool tiles = !single && M >= kManyRows && M >= 32 * S;
+  cudaError_t e;
+  if (tiles) {
+    auto go = [&](auto kern, int cols) {
+      const dim3 grid(unsigned((M + 63) / 64), unsigned((a.R + cols - 1) / cols));
+      return launch_overlapped(kern, grid, 256, 0, s, 0, p, a, h, p.heads > 0 ? p.K / p.heads : p.K);
+    };
+    e = a.R <= 16 ? go(adapters_f32_down_kernel<16>, 16) : a.R <= 32 ? go(adapters_f32_down_kernel<32>, 32) : go(adapters_f32_down_kernel<64>, 64);
+  } else {
+    e = adapters_down_rows(p, a, false, h, of_row, s);
+  }
   if (e != cudaSuccess) return e;
-  // a tile of 64 rows goes through its segments one by one (70 rows with adapters of their own: 88 us in all, 31 row by row)
-  if (p.M <= 4ll * a.S)
+  if (single)
     e = launch_overlapped(adapters_f32_up_rows_kernel, dim3(unsigned(p.M), (p.O + 255) / 256), 256, 0, s, 0, p, a, h, of_row, z);
   else
     e = launch_overlapped(adapters_f32_up_kernel, dim3((unsigned(p.M) + kTile - 1) / kTile, (p.O + kTile - 1) / kTile), 256, 0, s, 0, p, a, h, z);

@@ -257,3 +257,11 @@ def test_large_up_is_looked_over_to_its_end(rows, dout, rank):
         assert not torch.isfinite(b[:, ~keep].float()).all()
     mcs.mcs_check_status()
     assert torch.equal(c.run(), a)
+
+
+@pytest.mark.parametrize("rank,din,heads", [(4, 132, 0), (24, 640, 5), (64, 2432, 19), (136, 36, 0)])
+def test_f32_many_rows(rank, din, heads):
+    """fp32 with more rows than the first step takes one by one: ragged segments, rows without an adapter, heads."""
+    rows = 2600
+    for start, which in (([0, rows], [1]), ([3, 700, 700, 1301, 2599], [2, 1, -1, 0])):
+        Case("f32", 2, rows // 2, din, 40, rank, start, which, heads=heads, act="silu", gated=True).check()
