@@ -11,13 +11,17 @@ namespace mcs {
 namespace {
 
 // h = scale_a x down_a^T where many rows share an adapter: 64 rows and kCols columns of h a block, 4 x kCols / 16 a thread, 32 columns
-// of x at a time, the next ones on their way meanwhile.
+// of x at a time, the next ones on their way meanwhile. Where tiles are few a cluster of `splits` blocks shares K and adds its sums
+// through distributed shared memory, ranks in order.
 template <int kCols>
-__global__ void __launch_bounds__(256) adapters_f32_down_kernel(const LinearParams p, const AdapterParams a, float* h, const int hd) {
+__global__ void __launch_bounds__(256) adapters_f32_down_kernel(const LinearParams p, const AdapterParams a, float* h, const int hd, const int splits) {
   constexpr int kRows = 64, kK = 32, kPitch = kK + 4, kJ = kCols / 16;
-  __shared__ __align__(16) float xs[kRows][kPitch], ds[kCols][kPitch];
+  __shared__ __align__(16) float xs[kRows][kPitch], ds[kCols][kPitch], part[kRows][kCols + 1];
   const int tid = threadIdx.x, lane = tid & 31, ty = tid >> 4, tx = tid & 15;
-  const long long m0 = static_cast<long long>(blockIdx.x) * kRows;
+  const int tile = blockIdx.x / splits, rank = blockIdx.x - tile * splits;  // of the cluster {splits, 1, 1}
+  const long long m0 = static_cast<long long>(tile) * kRows;
+  const int nk = (p.K + kK - 1) / kK;
+  const int k_beg = int(static_cast<long long>(nk) * rank / splits) * kK, k_end = min(p.K, int(static_cast<long long>(nk) * (rank + 1) / splits) * kK);
   const int c0 = blockIdx.y * kCols;
   grid_inputs_ready();
   grid_let_next_start();
@@ -52,14 +56,14 @@ __global__ void __launch_bounds__(256) adapters_f32_down_kernel(const LinearPara
       const int k = k0 + q4, q = p.heads > 0 ? k / hd : 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        xv[i] = k < p.K ? *reinterpret_cast<const float4*>(x[i] + (q * head + (k - q * hd))) : none;
+        xv[i] = k < k_end ? *reinterpret_cast<const float4*>(x[i] + (q * head + (k - q * hd))) : none;
         const int c = row + 32 * i;
-        dv[i] = k < p.K && c < kCols && c0 + c < a.R ? __ldg(reinterpret_cast<const float4*>(down + static_cast<size_t>(c0 + c) * p.K + k)) : none;
+        dv[i] = k < k_end && c < kCols && c0 + c < a.R ? __ldg(reinterpret_cast<const float4*>(down + static_cast<size_t>(c0 + c) * p.K + k)) : none;
       }
     };
     float acc[4][kJ] = {};
-    fetch(0);
-    for (int k0 = 0; k0 < p.K; k0 += kK) {
+    fetch(k_beg);
+    for (int k0 = k_beg; k0 < k_end; k0 += kK) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(256) adapters_f32_down_kernel(const LinearPara
         if (row + 32 * i < kCols) *reinterpret_cast<float4*>(&ds[row + 32 * i][q4]) = dv[i];
       }
       __syncthreads();
-      if (k0 + kK < p.K) fetch(k0 + kK);
+      if (k0 + kK < k_end) fetch(k0 + kK);
 #pragma unroll
       for (int k = 0; k < kK; k += 4) {
         float4 u[kJ];
@@ -83,6 +87,25 @@ __global__ void __launch_bounds__(256) adapters_f32_down_kernel(const LinearPara
       }
     }
     const float sc = a.scale[ad];
+    if (splits > 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) part[ty * 4 + i][tx + 16 * j] = acc[i][j];
+      cluster_sync();
+      for (int e = rank * 256 + tid; e < kRows * kCols; e += splits * 256) {
+        const int r = e / kCols, c = e % kCols, m = int(m0) + r;
+        float sum = 0.f;
+        for (int q = 0; q < splits; ++q) {
+          float f;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(cluster_map(smem_u32(&part[r][c]), q)) : "memory");
+          sum += f;
+        }
+        if (m >= lo && m < hi && c0 + c < a.R) h[static_cast<size_t>(m) * a.R + c0 + c] = sc * sum;
+      }
+      cluster_sync();  // the sums have been read
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int m = int(m0) + ty * 4 + i;
@@ -187,14 +210,20 @@ cudaError_t linear_adapters_f32(const LinearParams& p, const AdapterParams& a, i
   // Second step row by row, whose threads read `up` again for every row: 70 rows with adapters of their own 31 us in all, 88 by
   // tiles of 64 rows, which go through their segments one by one; 300 rows of 30 segments to 300 outputs 15 and 23.
   const bool single = M <= 4 * S || (M <= 16 * S && M * p.O * a.R <= (16ll << 20));
-  // First step by tiles: rows that share adapters, and enough tiles to fill the GPU (x 1,536 -> 1,536, rank 64, 2,000 rows: 216 us in
-  // all, 134 four rows at a time; rank 32, 4,096 rows: 165 and 178; 74,156 x 128 -> 16, rank 72: 156 and 1,182).
+  // First step by tiles: rows that share adapters, and enough tiles to fill the GPU (1,024 x 1,536 -> 1,536, rank
+  // 16: 58 us in all, 52 four rows at a time; 2,000 rows, rank 64: 120 and 134; 4,096 rows, rank 32: 146 and 177; 74,156 x 128 ->
+  // 16, rank 72: 158 and 1,182).
   const bool tiles = !single && M >= kManyRows && M >= 32 * S;
   cudaError_t e;
   if (tiles) {
     auto go = [&](auto kern, int cols) {
-      const dim3 grid(unsigned((M + 63) / 64), unsigned((a.R + cols - 1) / cols));
-      return launch_overlapped(kern, grid, 256, 0, s, 0, p, a, h, p.heads > 0 ? p.K / p.heads : p.K);
+      const long long rows = (M + 63) / 64, across = (a.R + cols - 1) / cols;
+      // slices until there are eight blocks an SM, of four steps at least (2,482 x 3,200, rank 40: 330 us in all with one, 94 with
+      // eight; 5,658 x 3,720, rank 48: 484 with one, 213 with four blocks an SM, 189 with eight)
+      int splits = 1;
+      while (splits < 8 && rows * across * splits * 2 <= 8 * 152 && p.K >= splits * 2 * 4 * 32) splits *= 2;
+      return launch_overlapped(kern, dim3(unsigned(rows * splits), unsigned(across)), 256, 0, s, unsigned(splits), p, a, h,
+                               p.heads > 0 ? p.K / p.heads : p.K, splits);
     };
     e = a.R <= 16 ? go(adapters_f32_down_kernel<16>, 16) : a.R <= 32 ? go(adapters_f32_down_kernel<32>, 32) : go(adapters_f32_down_kernel<64>, 64);
   } else {
