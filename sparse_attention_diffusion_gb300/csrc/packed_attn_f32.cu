@@ -8,7 +8,10 @@
 // reads 12 shared-memory wavefronts for 64 multiplications a lane (16 clocks); the multiplications bound it.
 // Masked keys as in the bf16 kernel: scores by selection, V that not all rows see with what is not finite as 0.
 // Measured: one full sequence of 4,096 tokens, 8 heads, d = 128: 1.91 ms, 36 TFLOP/s (0.45 of the pipe); four causal ones of
-// 1,200 tokens and less, 20 heads on 4: 284 us; 77 tokens of 4 heads on 2: 9.9 us.
+// 1,200 tokens and less, 20 heads on 4: 253 us; 77 tokens of 4 heads on 2: 9.1 us; 32 single tokens over 4,000 keys and less of 4
+// heads, 16 heads, d = 128: 144 us, a fifth of the copy bandwidth, as a block waits for each tile (all of a tile's loads in
+// flight at once: 166 us with four. Four blocks an SM instead of two: 129, but three tokens each over 2,531 keys of 9 heads
+// 192 instead of 127).
 #include "common.cuh"
 #include "launch.cuh"
 #include "packed.h"
@@ -82,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
   const float* vb = static_cast<const float*>(p.v) + it.hk * p.vs.head + it.k0 * p.vs.token;
   for (int j0 = 0; j0 < it.nkeys; j0 += kKeys) {
     __syncthreads();  // the last tile's values have been read
+#pragma unroll 8
     for (int e = tid; e < kKeys * D / 4; e += kThreads) {
       const int r = e / (D / 4), c = e % (D / 4);
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -108,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
     }
     __syncthreads();  // the keys have been read: the values take their place
     bool found = false;
+#pragma unroll 8
     for (int e = tid; e < kKeys * D / 4; e += kThreads) {
       const int r = e / (D / 4), c = e % (D / 4);
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
