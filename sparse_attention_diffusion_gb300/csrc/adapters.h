@@ -56,7 +56,8 @@ struct RowTiles {
 
 // What the kernels read of the adapters. A zero row of a slab times an element of `up` that is not finite would be
 // NaN in another request's row. So the first kernel also looks through the adapters' `up`, each in shares,
-// and leaves a byte a share: such an adapter takes one step instead, NaN in its own rows times a column of w.
+// and leaves a byte a share: such an adapter takes one step instead, NaN in its own rows times zeros, which a copy from
+// behind w's columns brings (w's own columns may hold infinities, and other requests' rows are 0 in that step).
 struct AdapterView {
   const int32_t* start;
   const int32_t* which;

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (n < beg || n >= end || !ok) continue;
           const uint32_t last = n == end - 1 ? 8 : 0;
           const int col = (c >> 1) * 64;
-          if (odd) load(&map_w, 0, 0, &ad.mask, 0, 0, tt + seg, 1 | last);
+          if (odd) load(&map_w, nk * 64, 0, &ad.mask, 0, 0, tt + seg, 1 | last);  // zeros behind w's columns
           else load(&ad.up, col, which, &ad.h, col, 0, 2 * (tt + seg) + (c & 1), (min(64, ad.v.R - col) + 15) / 16 | last);
         }
       });

@@ -292,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for_segments(ad.v, row0, row1, lane, [&](int seg, int which, bool odd) {
             if (odd) {
               --more;
-              if (ok) load(&ad.mask, 0, rank * 128, rt + seg, &map_w, 0, 0, 1 | (more == 0 ? 8 : 0));
+              if (ok) load(&ad.mask, 0, rank * 128, rt + seg, &map_w, nk * 64, 0, 1 | (more == 0 ? 8 : 0));  // zeros behind w's columns
               return;
             }
             for (int c = 0; c < 2 * chunks; ++c) {
