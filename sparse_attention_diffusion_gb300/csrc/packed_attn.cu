@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool cut = p.chunk > 0, extra = it.tiles > 0 && odd[n % kFlags] != 0;
       const int h = it.hk * p.g + hh, all_see = visible_keys(it, p.causal, 0);
       float M = -INFINITY, total = 0.f, f[4] = {};
+      uint32_t far = 0;  // warps whose weight is 0 in fp32: only their infinities and NaN stay
       ml[tid] = make_float2(m, l);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -385,8 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            f[w] = x[w].y == 0.f ? 0.f : x[w].x == -INFINITY ? 1.f : fmaxf(ex2_approx(x[w].x - M), FLT_MIN);
+            f[w] = x[w].y == 0.f ? 0.f : x[w].x == -INFINITY ? 1.f : ex2_approx(x[w].x - M);
             total += x[w].y * f[w];
+            if (x[w].y != 0.f && f[w] == 0.f) far |= 1 << w;
           }
         }
         if (mine) {
@@ -394,12 +396,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           float o[8] = {};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            if (f[w] == 0.f) continue;  // no key, and what the sums hold then does not count
+            if (f[w] == 0.f) continue;  // no key, and what the sums hold then does not count, or far below the others
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float4 v = *reinterpret_cast<const float4*>(sums + (w * 32 + lane) * 128 + (((warp * 2 + i) ^ (lane & 7)) << 4));
               o[4 * i] = fmaf(f[w], v.x, o[4 * i]), o[4 * i + 1] = fmaf(f[w], v.y, o[4 * i + 1]);
               o[4 * i + 2] = fmaf(f[w], v.z, o[4 * i + 2]), o[4 * i + 3] = fmaf(f[w], v.w, o[4 * i + 3]);
+            }
+          }
+#pragma unroll 1
+          for (uint32_t left = far; left != 0; left &= left - 1) {
+            const uint8_t* row = sums + ((__ffs(left) - 1) * 32 + lane) * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float v = *reinterpret_cast<const float*>(row + (((warp * 2 + i / 4) ^ (lane & 7)) << 4) + i % 4 * 4);
+              o[i] += isfinite(v) ? 0.f : v;
             }
           }
           const float inv = cut ? 1.f : total == 0.f ? 0.f : 1.f / total;  // rows that see nothing give 0
@@ -652,8 +663,10 @@ __global__ void __launch_bounds__(256, 3) packed_join_kernel(const PackedParams 
       for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
       const float Mn = fmaxf(M, top), keep = M == -INFINITY ? 0.f : exp2f(M - Mn);
       // a chunk without a visible key has sum 0; one of NaN scores has maximum -inf but a sum that is NaN
-      // (and one far below M keeps the smallest weight, so that its infinities and NaN stay)
-      const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : fmaxf(exp2f(ml.x - Mn), FLT_MIN);
+      // (one whose weight leaves fp32's normal range adds nothing but its infinities and NaN, below)
+      float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : exp2f(ml.x - Mn);
+      uint32_t far = __ballot_sync(0xffffffffu, ml.y != 0.f && f < FLT_MIN);
+      f = f < FLT_MIN ? 0.f : f;
       float sum = ml.y * f;
   #pragma unroll
       for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -676,6 +689,13 @@ __global__ void __launch_bounds__(256, 3) packed_join_kernel(const PackedParams 
         float v[kE];
         read(c0 + c, v);
         add(c, v);
+      }
+  #pragma unroll 1
+      for (; far != 0; far &= far - 1) {
+        float v[kE];
+        read(c0 + __ffs(far) - 1, v);
+  #pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] += isfinite(v[e]) ? 0.f : v[e];
       }
       M = Mn;
     }
