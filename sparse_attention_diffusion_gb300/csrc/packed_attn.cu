@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(256, 3) packed_join_kernel(const PackedParams 
       for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
       l = l * keep + sum;
   #pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] *= keep;
+      for (int e = 0; e < kE; ++e) o[e] *= isfinite(o[e]) ? keep : 1.f;
       auto add = [&](int c, const float (&v)[kE]) {
         const float fc = __shfl_sync(0xffffffffu, f, c);
         if (fc != 0.f) {

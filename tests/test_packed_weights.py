@@ -44,7 +44,7 @@ def test_finite_values_of_no_weight_add_nothing(dtype, d, nq, kind, nk):
 
 
 @pytest.mark.parametrize("dtype,d,nq", [("bf16", 64, 1), ("bf16", 128, 1), ("bf16", 128, 100), ("f32", 128, 1)])
-@pytest.mark.parametrize("nk", [2048])
+@pytest.mark.parametrize("nk", [2048, 20480])
 @pytest.mark.parametrize("kind", ["first", "second"])
 def test_infinities_of_no_weight_stay(dtype, d, nq, nk, kind):
     """Pieces whose weight beside the others is 0 in fp32, though not in the formula, keep their infinities and NaN. (Within a
