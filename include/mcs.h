@@ -385,7 +385,7 @@ mcs_status mcs_linear_plan(const mcs_linear_desc *desc, int with_residual, int n
  * [Hk, Tk, d]. Sequence s holds queries q_start[s] .. q_start[s+1] - 1 and keys
  * k_start[s] .. k_start[s+1] - 1. Head h reads key head h / (H / Hk). Supported: d in
  * {64, 128}; H a multiple of Hk, H / Hk <= 64; S, Tq, Tk <= 2^30; H <= 2^20.
- * scale <= 0 selects 1/sqrt(d). */
+ * scale <= 0 selects 1/sqrt(d); 1.4427 scale has to be finite. */
 typedef struct {
   int S;
   int Tq, Tk;

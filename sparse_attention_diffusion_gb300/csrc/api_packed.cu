@@ -29,6 +29,7 @@ mcs_status check_packed(const mcs_packed_desc* d, mcs::PackedParams* p) {
   p->causal = d->causal != 0;
   p->max_q = d->max_q > 0 && d->max_q < d->Tq ? d->max_q : d->Tq;
   p->scale_log2 = (d->scale > 0.f ? d->scale : 1.f / std::sqrt(float(d->d))) * mcs::kLog2e;
+  if (!std::isfinite(p->scale_log2)) return MCS_ERR_INVALID_ARG;  // a score of 0 would become NaN
   return mcs::plan_packed(p, d->dtype == MCS_BF16) ? MCS_OK : MCS_ERR_UNSUPPORTED;
 }
 
