@@ -43,6 +43,9 @@ constexpr int kLaunchRegs = 128, kControlRegs = 48, kOutRegs = 96, kSoftmaxRegs 
 static_assert(128 * kControlRegs + 128 * kOutRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "an increase would wait forever");
 constexpr int kItems = 4;   // items found ahead
 constexpr int kFlags = 8;   // items whose V flags are kept (warp 15 is at most kItems ahead of the way out)
+// Waits that last as long as an item: of the way out for its sums, and of a chain without rows in it for the next. An item
+// of 2^30 keys is 2^23 tiles of 1.7 us, 14 s.
+constexpr uint64_t kItemLimitNs = 30ull * 1000ull * 1000ull * 1000ull;
 constexpr int kPatch = 32 * 128;  // a warp's rows x 128 bytes on their way out
 
 template <int D>
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The next item for a role; its slot is given back at once. n: items taken so far.
   auto take = [&](int n, PackedItem& it) -> bool {
     const int b = n % kItems;
-    if (!warp_all(mbar_wait_short(it_full + b, uint32_t(n / kItems) & 1))) return false;
+    if (!warp_all(mbar_wait_short<kItemLimitNs>(it_full + b, uint32_t(n / kItems) & 1))) return false;
     it = items[b];
     __syncwarp();
     if (lane == 0) mbar_arrive(it_empty + b);
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tmem + L::kColO + c * 128 + (uint32_t(w4 * 32) << 16);
         float2 ml = make_float2(-INFINITY, 0.f);
         if (some) {
-          if (!(ok = warp_all(mbar_wait_short(o_full + c, uint32_t(c ? live1++ : live0++) & 1)))) break;
+          if (!(ok = warp_all(mbar_wait_short<kItemLimitNs>(o_full + c, uint32_t(c ? live1++ : live0++) & 1)))) break;
           tc_fence_after();
           ml = stats[c * 128 + row];
         }

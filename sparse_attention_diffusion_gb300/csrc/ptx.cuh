@@ -76,6 +76,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
 
 // The same in fewer instructions, for kernels with many waits, which would not fit the instruction cache otherwise: the
 // clock is looked at after every 1,024 tries only, and other blocks' timeouts are not.
+template <uint64_t kLimitNs = kWaitLimitNs>
 __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
   uint64_t t0 = 0;
@@ -92,7 +93,7 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity) 
     if (ok != 0) return true;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitLimitNs) return false;
+    if (t - t0 > kLimitNs) return false;
   }
 }
 
