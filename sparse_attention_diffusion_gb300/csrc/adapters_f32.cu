@@ -118,7 +118,6 @@ __global__ void __launch_bounds__(256) adapters_f32_down_kernel(const LinearPara
 }
 
 // z = h up_a^T, 0 in rows without an adapter: 64 x 64 outputs a block, 4 x 4 a thread, 16 columns of R at a time.
-constexpr int kManyRows = 2048;
 constexpr int kTile = 64, kStep = 16, kLd = kStep + 4;
 __global__ void __launch_bounds__(256) adapters_f32_up_kernel(const LinearParams p, const AdapterParams a, const float* h, float* z) {
   __shared__ __align__(16) float hs[kTile][kLd], us[kTile][kLd];
@@ -210,10 +209,12 @@ cudaError_t linear_adapters_f32(const LinearParams& p, const AdapterParams& a, i
   // Second step row by row, whose threads read `up` again for every row: 70 rows with adapters of their own 31 us in all, 88 by
   // tiles of 64 rows, which go through their segments one by one; 300 rows of 30 segments to 300 outputs 15 and 23.
   const bool single = M <= 4 * S || (M <= 16 * S && M * p.O * a.R <= (16ll << 20));
-  // First step by tiles: rows that share adapters, and enough tiles to fill the GPU (1,024 x 1,536 -> 1,536, rank
-  // 16: 58 us in all, 52 four rows at a time; 2,000 rows, rank 64: 120 and 134; 4,096 rows, rank 32: 146 and 177; 74,156 x 128 ->
-  // 16, rank 72: 158 and 1,182).
-  const bool tiles = !single && M >= kManyRows && M >= 32 * S;
+  // First step by tiles: rows that share adapters, and enough of them, the fewer the higher the rank, as four rows at a time read
+  // `down` again for every four (two segments, to 512 outputs, in all, by tiles and four rows at a time: 2,100 x 1,536, rank 16, 44 and 43
+  // us, 2,000 x 1,536, rank 32, 55 and 57; rank 64: 1,400 rows 66 and 72, 1,600 68 and 76, of 4,096 columns 136 and 136; rank 128: 700
+  // rows of 4,096 columns 124 and 122, 1,000 126 and 148; rank 256: 300 and 400 rows of 4,096 columns 135 and 132, 145 and 157; 74,156 x
+  // 128 -> 16, rank 72: 158 and 1,182).
+  const bool tiles = !single && M >= 32 * S && (M >= 2048 || M * a.R >= 2048 * 48);
   cudaError_t e;
   if (tiles) {
     auto go = [&](auto kern, int cols) {
