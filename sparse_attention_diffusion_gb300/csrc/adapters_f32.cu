@@ -222,7 +222,7 @@ cudaError_t linear_adapters_f32(const LinearParams& p, const AdapterParams& a, i
       // slices until there are eight blocks an SM, of four steps at least (2,482 x 3,200, rank 40: 330 us in all with one, 94 with
       // eight; 5,658 x 3,720, rank 48: 484 with one, 213 with four blocks an SM, 189 with eight)
       int splits = 1;
-      while (splits < 8 && rows * across * splits * 2 <= 8 * 152 && p.K >= splits * 2 * 4 * 32) splits *= 2;
+      while (splits < 8 && rows * across * splits * 2 <= 8ll * num_sms && p.K >= splits * 2 * 4 * 32) splits *= 2;
       return launch_overlapped(kern, dim3(unsigned(rows * splits), unsigned(across)), 256, 0, s, unsigned(splits), p, a, h,
                                p.heads > 0 ? p.K / p.heads : p.K, splits);
     };

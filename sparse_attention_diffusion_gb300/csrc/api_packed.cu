@@ -85,8 +85,7 @@ mcs_status mcs_packed_attn(const mcs_packed_desc* desc, const void* q, const mcs
     for (int j = 0; j < i; ++j)
       if (overlap(out[i], out[j])) return MCS_ERR_INVALID_ARG;
   }
-  int sms = 0;
-  if ((st = mcs::current_device(&p.status, &sms)) != MCS_OK) return st;
+  if ((st = mcs::current_device(&p.status, &p.sms)) != MCS_OK) return st;
   p.q = q, p.k = k, p.v = v, p.o = o, p.lse = lse;
   p.q_start = q_start, p.k_start = k_start;
   p.part_o = static_cast<float*>(ws);

@@ -44,6 +44,7 @@ struct PackedParams {
   float* part_o;          // with chunk > 0: [slot][tile][Hk][rows][d] sums, not divided
   float2* part_ml;        // [slot][tile][Hk][rows] (maximum in log2 units, sum)
   uint32_t* status;
+  int sms;                // of the device
 };
 
 // Fills the tiles, chunks and item counts; false where they do not fit in 31 bits.

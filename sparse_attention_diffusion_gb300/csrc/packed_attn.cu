@@ -738,6 +738,8 @@ cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
 // rather have the short ones: 32 tokens over 4,000 keys and less of 4 heads 204 us so, 171 without). Otherwise two an SM, as every tile
 // of a sequence leaves its sums (seven chunks of 300 tokens and less: 49 us with one, 45 with two, 53 with four, 65 with eight).
 // Sequences of more than one tile go two tiles at a time.
+// The plan is made without a device (its workspace is asked for on the host) and so for the SMs of a whole one; with fewer the pieces are
+// smaller than they need be.
 bool plan_packed(PackedParams* p, bool bf16) {
   constexpr int kSms = 152;
   p->g = p->H / p->Hk;
@@ -794,7 +796,7 @@ cudaError_t packed_attn_tc(const PackedParams& p, cudaStream_t s) {
 
 cudaError_t packed_join(const PackedParams& p, bool bf16, cudaStream_t s) {
   // as many blocks a token as fill the GPU twice, a turn of eight heads each at least
-  const int turns = (p.H + 7) / 8, want = (2 * 152 + p.Tq - 1) / p.Tq, each = want < turns ? want : turns;
+  const int turns = (p.H + 7) / 8, want = (2 * p.sms + p.Tq - 1) / p.Tq, each = want < turns ? want : turns;
   auto go = [&](auto kern) { return launch_overlapped(kern, dim3(unsigned(p.Tq), unsigned(each)), 256, 0, s, 0, p, walk_of(p)); };
   if (bf16) return p.d == 128 ? go(packed_join_kernel<128, __nv_bfloat16>) : go(packed_join_kernel<64, __nv_bfloat16>);
   return p.d == 128 ? go(packed_join_kernel<128, float>) : go(packed_join_kernel<64, float>);
