@@ -34,6 +34,7 @@ struct PackedParams {
   int causal, max_q;
   float scale_log2;       // scale * log2(e)
   int tq, rows;           // tokens and rows (tq * g) of a tile (of two tiles: pair)
+  int part_rows;          // rows of a tile that can hold a token, for which there are partial sums
   int pair;               // bf16, two tiles of 128 rows an item
   int quarters;           // bf16, d = 64, items of 32 rows at most: every softmax warp a quarter of the keys
   int chunk;              // keys of a piece of a sequence, 0: sequences are not cut
@@ -41,8 +42,8 @@ struct PackedParams {
   long long items;        // slots of all heads (and tiles)
   Divisor by_heads, by_tiles, by_group, by_slots;
   int slots;
-  float* part_o;          // with chunk > 0: [slot][tile][Hk][rows][d] sums, not divided
-  float2* part_ml;        // [slot][tile][Hk][rows] (maximum in log2 units, sum)
+  float* part_o;          // with chunk > 0: [slot][tile][Hk][part_rows][d] sums, not divided
+  float2* part_ml;        // [slot][tile][Hk][part_rows] (maximum in log2 units, sum)
   uint32_t* status;
   int sms;                // of the device
 };
@@ -162,7 +163,7 @@ __device__ __forceinline__ bool packed_item(const PackedParams& p, const Divisor
   it->nkeys = p.chunk > 0 ? min(p.chunk, seen - int(k_first)) : seen;
   it->lim = t0 + 1 + nk - nq - int(k_first);
   it->tiles = (it->nkeys + 127) >> 7;
-  it->part = ((static_cast<long long>(slot) * p.tiles + iq) * p.Hk + it->hk) * p.rows;
+  it->part = ((static_cast<long long>(slot) * p.tiles + iq) * p.Hk + it->hk) * p.part_rows;
   return true;
 }
 #endif

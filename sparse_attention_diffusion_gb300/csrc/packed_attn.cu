@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(256, 3) packed_join_kernel(const PackedParams 
   for (int h = blockIdx.y * 8 + (threadIdx.x >> 5); h < p.H; h += 8 * gridDim.y) {
     const int hk = p.by_group.div(h), hh = h - hk * p.g;
     const long long row = (i - iq * p.tq) * p.g + hh;
-    auto at = [&](int c) { return ((static_cast<long long>(slot + c) * p.tiles + iq) * p.Hk + hk) * p.rows + row; };
+    auto at = [&](int c) { return ((static_cast<long long>(slot + c) * p.tiles + iq) * p.Hk + hk) * p.part_rows + row; };
     constexpr int kE = D / 32;
     float M = -INFINITY, l = 0.f, o[kE] = {};
     auto read = [&](int c, float (&v)[kE]) {
@@ -776,6 +776,7 @@ bool plan_packed(PackedParams* p, bool bf16) {
     p->by_tiles = Divisor(p->tiles);
   }
   p->rows = p->tq * p->g;
+  p->part_rows = std::min(p->tq, p->max_q) * p->g;
   p->items = slots * p->tiles * p->Hk;
   if (p->items >= (1ll << 31) - 65536) return false;
   p->slots = int(slots);
@@ -785,7 +786,7 @@ bool plan_packed(PackedParams* p, bool bf16) {
 
 size_t packed_workspace_bytes(const PackedParams& p) {
   if (p.chunk == 0) return 16;
-  return size_t(p.items) * p.rows * (size_t(p.d) * 4 + 8);
+  return size_t(p.items) * p.part_rows * (size_t(p.d) * 4 + 8);
 }
 
 cudaError_t packed_attn_tc(const PackedParams& p, cudaStream_t s) {
