@@ -411,7 +411,9 @@ typedef struct {
  * MCS_ERR_DEVICE_BOUNDS; o and lse are then undefined. Values of keys that a query does not see, another sequence's
  * or later ones, have no effect on it, infinities and NaN included.
  * BF16 runs on the tensor cores (weights are rounded to bf16 before the sum over the values, the
- * sum of the weights is not), F32 in fp32. Sums and statistics are fp32, one rounding. Outputs
+ * sum of the weights is not), F32 in fp32. Sums and statistics are fp32, one rounding. The tensor
+ * core adds 16 products at a time by truncation, which moves a sum by less than keys / 16 * 5.25 *
+ * 2^-23 of sum |w v| over at most 2^18 keys; spans of longer sequences are added to nearest. Outputs
  * may not overlap inputs. ws: at least mcs_packed_attn_workspace_size(desc) bytes (0 for an
  * invalid description; host only); its contents on entry are ignored; calls that may run at the
  * same time need one each. Equal calls give equal bits. */

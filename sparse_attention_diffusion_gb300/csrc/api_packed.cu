@@ -16,8 +16,8 @@ using mcs::from_cuda;
 using mcs::overlap;
 using mcs::Range;
 
-// The checks of a description; fills its sizes and the plan.
-mcs_status check_packed(const mcs_packed_desc* d, mcs::PackedParams* p) {
+// The checks of a description; fills its sizes and the plan. own_keys: every sequence's keys are as many as its queries.
+mcs_status check_packed(const mcs_packed_desc* d, mcs::PackedParams* p, bool own_keys) {
   if (d == nullptr) return MCS_ERR_INVALID_ARG;
   if (d->S < 1 || d->Tq < 1 || d->Tk < 1 || d->H < 1 || d->Hk < 1 || d->H % d->Hk != 0) return MCS_ERR_INVALID_ARG;
   if (d->max_q < 0 || !std::isfinite(d->scale)) return MCS_ERR_INVALID_ARG;
@@ -30,7 +30,7 @@ mcs_status check_packed(const mcs_packed_desc* d, mcs::PackedParams* p) {
   p->max_q = d->max_q > 0 && d->max_q < d->Tq ? d->max_q : d->Tq;
   p->scale_log2 = (d->scale > 0.f ? d->scale : 1.f / std::sqrt(float(d->d))) * mcs::kLog2e;
   if (!std::isfinite(p->scale_log2)) return MCS_ERR_INVALID_ARG;  // a score of 0 would become NaN
-  return mcs::plan_packed(p, d->dtype == MCS_BF16) ? MCS_OK : MCS_ERR_UNSUPPORTED;
+  return mcs::plan_packed(p, d->dtype == MCS_BF16, own_keys && p->max_q < p->Tk ? p->max_q : p->Tk) ? MCS_OK : MCS_ERR_UNSUPPORTED;
 }
 
 // Strides of a [heads, tokens, d] view in elements (NULL: contiguous); false unless rows are apart and each stride
@@ -55,7 +55,7 @@ extern "C" {
 
 size_t mcs_packed_attn_workspace_size(const mcs_packed_desc* desc) {
   mcs::PackedParams p{};
-  return check_packed(desc, &p) == MCS_OK ? mcs::packed_workspace_bytes(p) : 0;
+  return check_packed(desc, &p, false) == MCS_OK ? mcs::packed_workspace_bytes(p) : 0;
 }
 
 mcs_status mcs_packed_attn(const mcs_packed_desc* desc, const void* q, const mcs_strides* qs, const void* k,
@@ -63,7 +63,7 @@ mcs_status mcs_packed_attn(const mcs_packed_desc* desc, const void* q, const mcs
                            const int32_t* k_start, void* o, const mcs_strides* os, float* lse, void* ws, size_t ws_bytes,
                            mcs_stream stream) {
   mcs::PackedParams p{};
-  mcs_status st = check_packed(desc, &p);
+  mcs_status st = check_packed(desc, &p, q_start == k_start);
   if (st != MCS_OK) return st;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !mcs::aligned16_or_null(lse)) return MCS_ERR_INVALID_ARG;
   if (!aligned16(q_start) || !aligned16(k_start)) return MCS_ERR_INVALID_ARG;

@@ -18,6 +18,12 @@
 
 namespace mcs {
 
+// The tensor core adds into its fp32 sums by truncation, a step of 16 keys after another: the sums of 2^20 keys with equal weights came
+// out 0.5 % too small, of 2^22 2.6 %. So no sum takes more than 2^18 keys: pieces of sequences have 2^17 at most, and a kernel that
+// may meet longer sequences whole empties its sums every kSumTiles tiles into fp32 memory of its block (a bank), adding to nearest.
+constexpr int kSumKeys = 1 << 17, kSumTiles = kSumKeys / 128;
+constexpr int kBanks = 152;  // blocks that may have one
+
 struct PackedStrides {
   long long head, token;  // elements
 };
@@ -39,6 +45,7 @@ struct PackedParams {
   int quarters;           // bf16, d = 64, items of 32 rows at most: every softmax warp a quarter of the keys
   int chunk;              // keys of a piece of a sequence, 0: sequences are not cut
   int tiles;              // with chunk > 0: query tiles of the longest sequence
+  int banks;              // blocks that need a bank each: [bank][2][128 rows][d] in part_o; 0: none
   long long items;        // slots of all heads (and tiles)
   Divisor by_heads, by_tiles, by_group, by_slots;
   int slots;
@@ -48,8 +55,8 @@ struct PackedParams {
   int sms;                // of the device
 };
 
-// Fills the tiles, chunks and item counts; false where they do not fit in 31 bits.
-bool plan_packed(PackedParams* p, bool bf16);
+// Fills the tiles, chunks and item counts for sequences of up to `longest` keys; false where they do not fit in 31 bits.
+bool plan_packed(PackedParams* p, bool bf16, int longest);
 size_t packed_workspace_bytes(const PackedParams& p);
 cudaError_t packed_attn_tc(const PackedParams& p, cudaStream_t s);
 cudaError_t packed_attn_pair(const PackedParams& p, cudaStream_t s);

@@ -740,7 +740,8 @@ cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
 // Sequences of more than one tile go two tiles at a time.
 // The plan is made without a device (its workspace is asked for on the host) and so for the SMs of a whole one; with fewer the pieces are
 // smaller than they need be.
-bool plan_packed(PackedParams* p, bool bf16) {
+// On the tensor cores no piece has more than kSumKeys, and sequences of one tile that may be longer than twice as many are cut too.
+bool plan_packed(PackedParams* p, bool bf16, int longest) {
   constexpr int kSms = 152;
   p->g = p->H / p->Hk;
   int rows = bf16 ? 128 : 64;
@@ -771,6 +772,11 @@ bool plan_packed(PackedParams* p, bool bf16) {
     if (bf16 && tiles == 1) chunk = std::max(chunk, std::min(round, 8ll * piece));
     if (chunk < 2 * piece) chunk = 2 * piece;
     p->chunk = int(chunk < (1 << 30) ? chunk : (1 << 30));
+    if (bf16) p->chunk = std::min(p->chunk, kSumKeys);
+  } else if (bf16 && !p->pair && longest > 2 * kSumKeys) {
+    p->chunk = kSumKeys;
+  }
+  if (p->chunk > 0) {
     p->tiles = int(tiles);
     slots = p->Tk / p->chunk + p->S;
     p->by_tiles = Divisor(p->tiles);
@@ -779,13 +785,14 @@ bool plan_packed(PackedParams* p, bool bf16) {
   p->part_rows = std::min(p->tq, p->max_q) * p->g;
   p->items = slots * p->tiles * p->Hk;
   if (p->items >= (1ll << 31) - 65536) return false;
+  p->banks = p->pair && p->chunk == 0 && longest > 2 * kSumKeys ? int(std::min<long long>(p->items, kBanks)) : 0;
   p->slots = int(slots);
   p->by_slots = Divisor(p->slots);
   return true;
 }
 
 size_t packed_workspace_bytes(const PackedParams& p) {
-  if (p.chunk == 0) return 16;
+  if (p.chunk == 0) return std::max<size_t>(16, size_t(p.banks) * 256 * p.d * 4);
   return size_t(p.items) * p.part_rows * (size_t(p.d) * 4 + 8);
 }
 

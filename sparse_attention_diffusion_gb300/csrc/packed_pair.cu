@@ -26,6 +26,9 @@
 // (0.86 to 0.87 of the sustained rate of plain products); three full sequences of 7,716, 4,031 and 1,626 tokens, 12 heads: 338
 // us, 1,426 TFLOP/s, tensor pipe 64 % active; 16 causal prompts of 6 to 839 tokens, 32 heads on 8: 50 us, pipe 26 %. There the instructions count: with 62 KB of them, unrolled masks and
 // 40 for every wait, a quarter of the fetches missed the instruction cache and the same prompts took 99 us.
+#include <algorithm>
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "common.cuh"
 #include "launch.cuh"
@@ -48,7 +51,7 @@ constexpr int kFlags = 8;   // items whose V flags are kept (warp 15 is at most 
 constexpr uint64_t kItemLimitNs = 30ull * 1000ull * 1000ull * 1000ull;
 constexpr int kPatch = 32 * 128;  // a warp's rows x 128 bytes on their way out
 
-template <int D>
+template <int D, bool kLong>
 struct Cfg {
   static constexpr int kStages = (D == 128) ? 4 : 8;  // K and V tiles
   static constexpr int kTile = (D / 64) * kRegion;
@@ -61,18 +64,42 @@ struct Cfg {
   static constexpr int kSteal = (kBar + kNumBars * 8 + 15) / 16 * 16;  // the answer to a request for a block
   static constexpr int kMisc = kSteal + 16;
   static constexpr int kItem = (kMisc + 16 + kFlags * 4 + 15) / 16 * 16;
-  static constexpr int kBytes = kItem + kItems * int(sizeof(PackedItem));
+  static constexpr int kScale = kItem + kItems * int(sizeof(PackedItem));  // [2][128] the bank's factor (kLong)
+  static constexpr int kBytes = kScale + (kLong ? 2 * 128 * 4 : 0);
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kColS = 0, kColO = 256;  // of A; B's lie 128 behind
 };
-static_assert(Cfg<128>::kAlloc <= 227 * 1024 && Cfg<64>::kAlloc <= 227 * 1024, "shared memory");
+static_assert(Cfg<128, true>::kAlloc <= 227 * 1024 && Cfg<64, true>::kAlloc <= 227 * 1024, "shared memory");
+
+// A chain's sums of a row, added to its bank, whose own sums are taken times `keep`. first: it holds nothing yet.
+template <int D>
+__device__ __forceinline__ void empty_sums(uint32_t tO, float4* bank, float keep, bool first) {
+#pragma unroll 1
+  for (int q = 0; q < D / 32; ++q) {
+    uint32_t o[32];
+    tmem_ld32(tO + q * 32, o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float4 b = first ? make_float4(0.f, 0.f, 0.f, 0.f) : bank[q * 8 + i];
+      b.x = (isfinite(b.x) ? b.x * keep : b.x) + __uint_as_float(o[4 * i]);
+      b.y = (isfinite(b.y) ? b.y * keep : b.y) + __uint_as_float(o[4 * i + 1]);
+      b.z = (isfinite(b.z) ? b.z * keep : b.z) + __uint_as_float(o[4 * i + 2]);
+      b.w = (isfinite(b.w) ? b.w * keep : b.w) + __uint_as_float(o[4 * i + 3]);
+      bank[q * 8 + i] = b;
+    }
+  }
+}
 
 // kCut: an item's keys are one piece of its sequence's, its sums leave in fp32 for packed_join.
-template <int D, bool kCut>
+// kLong: items may have more than 2^18 keys. Every kSumTiles tiles the softmax's threads add their rows' sums to the block's bank in
+// global memory (P V of the tile before is done when they hold the scores) and the next P V begins anew; the sums of weights
+// go with them, in registers. The way out adds the bank before it gives O back, so the next item cannot meet it.
+template <int D, bool kCut, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const PackedParams p, const PackedWalk wk) {
-  using L = Cfg<D>;
+  static_assert(!(kCut && kLong), "pieces are short");
+  using L = Cfg<D, kLong>;
   constexpr int R = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -95,6 +122,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* odd = tmem_slot + 4;  // [kFlags] the item's V held something that is not finite and not seen by all
   float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
+  [[maybe_unused]] float* bank_scale = reinterpret_cast<float*>(smem + L::kScale);
+  // a row of a chain in this block's bank
+  [[maybe_unused]] auto bank_row = [&](int c, int row) {
+    return reinterpret_cast<float4*>(p.part_o + ((static_cast<size_t>(blockIdx.x) * 2 + c) * 128 + row) * D);
+  };
   PackedItem* items = reinterpret_cast<PackedItem*>(smem + L::kItem);
 
   const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
@@ -156,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++cnt;
         return true;
       };
-      PackedBlocks blocks(p, wk, lane, steal, steal_slot);
+      std::conditional_t<kLong, PackedDealt, PackedBlocks> blocks(p, wk, lane, steal, steal_slot);
       PackedItem it{}, following{};  // the first turn finds an item and loads nothing
       for (bool begun = false;; it = following, begun = true) {
         if (begun) {
@@ -235,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j >= 0) {
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
-                tc_mma_ts_lo(tO, tS + ks * 8, vlo + kstep_mnmajor(ks), kIdescPV, (j > 0 || ks > 0) ? 1u : 0u);
+                tc_mma_ts_lo(tO, tS + ks * 8, vlo + kstep_mnmajor(ks), kIdescPV, ((kLong ? j % kSumTiles : j) > 0 || ks > 0) ? 1u : 0u);
               tc_commit(empty + sv);
               // The other one's turn: it takes 300 clocks to begin, two S products are in the queue by then (with all
               // of them 345 us instead of 344 for three clips, from P V on 345).
@@ -371,6 +403,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) u[i] = 0;
               }
+              if (kLong && some && tiles_of(it, c) > kSumTiles) {
+                const float4* bank = bank_row(c, row) + q * (kPass / 4) + x * 8;
+                const float f = bank_scale[c * 128 + row];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 b = bank[i];
+                  u[4 * i] = __float_as_uint(__uint_as_float(u[4 * i]) + (isfinite(b.x) ? b.x * f : b.x));
+                  u[4 * i + 1] = __float_as_uint(__uint_as_float(u[4 * i + 1]) + (isfinite(b.y) ? b.y * f : b.y));
+                  u[4 * i + 2] = __float_as_uint(__uint_as_float(u[4 * i + 2]) + (isfinite(b.z) ? b.z * f : b.z));
+                  u[4 * i + 3] = __float_as_uint(__uint_as_float(u[4 * i + 3]) + (isfinite(b.w) ? b.w * f : b.w));
+                }
+              }
               if constexpr (!kCut) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) u[i] = pack_bf16x2(__uint_as_float(u[2 * i]) * inv, __uint_as_float(u[2 * i + 1]) * inv);
@@ -445,9 +489,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = mine ? visible_keys(it, p.causal, t) : it.nkeys;
       const bool busy = w4 * 32 < ntok * p.g;
       float m = -INFINITY, l = 0.f;
+      [[maybe_unused]] float bank_m = -INFINITY, bank_l = 0.f;
       for (int j = 0; j < T; ++j, ++tile) {
         if (!(ok = warp_all(mbar_wait_short(s_full + c, uint32_t(tile) & 1)))) break;
         tc_fence_after();
+        if (kLong && busy && j > 0 && j % kSumTiles == 0) {
+          const float keep = bank_m == m ? 1.f : ex2_approx(bank_m - m);
+          empty_sums<D>(tO, bank_row(c, row), keep, j == kSumTiles);
+          bank_l = bank_l * keep + l;
+          bank_m = m, l = 0.f;
+        }
         uint32_t pk[64];
         bool need = false;
         float alpha = 1.f;
@@ -502,6 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the last item's rows have been read
       if (!(ok = warp_all(mbar_wait_short(o_free + c, (uint32_t(live) & 1) ^ 1)))) break;
       ++live;
+      if (kLong && T > kSumTiles) {
+        const float f = bank_m == m ? 1.f : ex2_approx(bank_m - m);
+        l += bank_l * f;
+        bank_scale[c * 128 + row] = f;
+      }
       stats[c * 128 + row] = make_float2(m, l);
       mbar_arrive(o_full + c);
     }
@@ -516,20 +572,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kCut>
+template <int D, bool kCut, bool kLong = false>
 cudaError_t launch_two(const PackedParams& p, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   if (!(make_view_map(&mq, p.q, p.H, p.Tq, D, p.qs, p.g, p.tq / 2) && make_view_map(&mk, p.k, p.Hk, p.Tk, D, p.ks, 1, 128) &&
         make_view_map(&mv, p.v, p.Hk, p.Tk, D, p.vs, 1, 128)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem_and_regs<packed_pair_kernel<D, kCut>>(Cfg<D>::kAlloc, kLaunchRegs);
+  constexpr int kSmem = Cfg<D, kLong>::kAlloc;
+  const cudaError_t e = allow_smem_and_regs<packed_pair_kernel<D, kCut, kLong>>(kSmem, kLaunchRegs);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(packed_pair_kernel<D, kCut>, dim3(unsigned(p.items)), kThreads, Cfg<D>::kAlloc, s, 0, mq, mk, mv, p, walk_of(p));
+  const long long blocks = kLong ? std::min(p.banks, p.sms) : p.items;
+  return launch_overlapped(packed_pair_kernel<D, kCut, kLong>, dim3(unsigned(blocks)), kThreads, kSmem, s, 0, mq, mk, mv, p, walk_of(p));
 }
 
 }  // namespace
 
 cudaError_t packed_attn_pair(const PackedParams& p, cudaStream_t s) {
+  if (p.banks > 0) return p.d == 128 ? launch_two<128, false, true>(p, s) : launch_two<64, false, true>(p, s);
   if (p.chunk == 0) return p.d == 128 ? launch_two<128, false>(p, s) : launch_two<64, false>(p, s);
   const cudaError_t e = p.d == 128 ? launch_two<128, true>(p, s) : launch_two<64, true>(p, s);
   return e != cudaSuccess ? e : packed_join(p, true, s);

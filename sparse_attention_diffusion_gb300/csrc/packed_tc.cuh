@@ -143,6 +143,31 @@ struct PackedBlocks {
   }
 };
 
+// The same with the items dealt out in advance, for kernels whose blocks are numbered up to kBanks.
+struct PackedDealt {
+  long long at = blockIdx.x;
+  PackedLane sequence;
+  __device__ __forceinline__ PackedDealt(const PackedParams& p, const PackedWalk& wk, int lane, uint64_t*, uint32_t) {
+    if (p.S <= 32) sequence = packed_lane(p, wk.by_tq, wk.by_chunk, lane);
+  }
+  __device__ __forceinline__ bool next(const PackedParams& p, const PackedWalk& wk, int lane, PackedItem& it) {
+    while (true) {
+      const long long i = at;
+      if (i >= p.items) {
+        it.tiles = -1;
+        return true;
+      }
+      at += gridDim.x;
+      if (const long long s = i * 32 + lane; s < p.S) {  // there are more items than sequences
+        int a, b, c, d;
+        if (!packed_sequence(p, int(s), a, b, c, d)) raise_status(p.status, kStatusBounds);
+      }
+      __syncwarp();
+      if (packed_item(p, wk.by_tq, wk.by_chunk, sequence, i, lane, &it)) return true;
+    }
+  }
+};
+
 // Tiled map over a [heads, tokens, d] bf16 view, box = 64 columns x box_heads x box_tokens, 128-byte swizzle.
 bool make_view_map(CUtensorMap* m, const void* base, int heads, int tokens, int d, const PackedStrides& s, int box_heads, int box_tokens) {
   auto enc = tensor_map_encoder();
