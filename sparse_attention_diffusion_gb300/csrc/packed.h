@@ -71,7 +71,7 @@ struct PackedItem {
   int lim;        // keys that its first token sees, from k0 on (not clamped); all see nkeys without a mask
   int hk;         // key head
   int tiles;      // of 128 keys; -1: no more items
-  int pad;
+  int whole;      // it has all keys that its rows see
   long long part; // row in the partial sums
 };
 // Keys from the item's first that token t of it sees.
@@ -168,6 +168,7 @@ __device__ __forceinline__ bool packed_item(const PackedParams& p, const Divisor
   if (p.chunk > 0 && k_first >= seen) return false;
   it->k0 = k0 + int(k_first);
   it->nkeys = p.chunk > 0 ? min(p.chunk, seen - int(k_first)) : seen;
+  it->whole = it->nkeys == seen;
   it->lim = t0 + 1 + nk - nq - int(k_first);
   it->tiles = (it->nkeys + 127) >> 7;
   it->part = ((static_cast<long long>(slot) * p.tiles + iq) * p.Hk + it->hk) * p.part_rows;

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       // 32 columns at a time: a warp leaves its sums of them, and adds the four warps' of eight
-      const bool cut = p.chunk > 0, extra = it.tiles > 0 && odd[n % kFlags] != 0;
+      const bool cut = !it.whole, extra = it.tiles > 0 && odd[n % kFlags] != 0;
       const int h = it.hk * p.g + hh, all_see = visible_keys(it, p.causal, 0);
       float M = -INFINITY, total = 0.f, f[4] = {};
       uint32_t far = 0;  // warps whose weight is 0 in fp32: only their infinities and NaN stay
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (busy) {
         const int h = it.hk * p.g + hh;
-        const bool cut = p.chunk > 0;
+        const bool cut = !it.whole;
         const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;  // rows that see nothing give 0
         // elements of V that are not finite and that only some rows see (left out of the products)
         const bool extra = it.tiles > 0 && odd[n % kFlags] != 0;
@@ -634,6 +634,7 @@ __global__ void __launch_bounds__(256, 3) packed_join_kernel(const PackedParams 
   if (!mine) return;
   const int i = tok - q0, iq = wk.by_tq.div(i), last = min((iq + 1) * p.tq, nq);
   const int seen = p.causal ? max(0, min(nk, last + nk - nq)) : nk;
+  if (!p.pair && seen > 0 && seen <= p.chunk) return;  // one piece, which has left by itself
   const int chunks = wk.by_chunk.div(seen + p.chunk - 1), slot = wk.by_chunk.div(k0) + s;
   for (int h = blockIdx.y * 8 + (threadIdx.x >> 5); h < p.H; h += 8 * gridDim.y) {
     const int hk = p.by_group.div(h), hh = h - hk * p.g;

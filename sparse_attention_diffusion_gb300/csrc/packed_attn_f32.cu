@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 2) packed_attn_f32_kernel(const Pack
   for (int i = 0; i < kR; ++i) {
     const int r = ty * kR + i, t = p.by_group.div(r), h = it.hk * p.g + r - t * p.g;
     if (r >= p.rows || t >= it.ntok) continue;
-    const bool cut = p.chunk > 0;
+    const bool cut = !it.whole;
     const float inv = cut ? 1.f : 1.f / l[i];
     float v[kC * 4];
 #pragma unroll
