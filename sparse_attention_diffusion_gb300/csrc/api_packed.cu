@@ -88,7 +88,8 @@ mcs_status mcs_packed_attn(const mcs_packed_desc* desc, const void* q, const mcs
   if ((st = mcs::current_device(&p.status, &p.sms)) != MCS_OK) return st;
   p.q = q, p.k = k, p.v = v, p.o = o, p.lse = lse;
   p.q_start = q_start, p.k_start = k_start;
-  p.part_o = static_cast<float*>(ws);
+  p.taken = static_cast<uint32_t*>(ws);
+  p.part_o = static_cast<float*>(ws) + (p.banks > 0 ? mcs::kTakenBytes / 4 : 0);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + size_t(p.items) * p.part_rows * p.d);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return from_cuda(bf16 ? mcs::packed_attn_tc(p, s) : mcs::packed_attn_f32(p, s));

@@ -23,6 +23,7 @@ namespace mcs {
 // may meet longer sequences whole empties its sums every kSumTiles tiles into fp32 memory of its block (a bank), adding to nearest.
 constexpr int kSumKeys = 1 << 17, kSumTiles = kSumKeys / 128;
 constexpr int kBanks = 152;  // blocks that may have one
+constexpr int kTakenBytes = 256;  // before the banks: the items' counter
 
 struct PackedStrides {
   long long head, token;  // elements
@@ -51,6 +52,7 @@ struct PackedParams {
   int slots;
   float* part_o;          // with chunk > 0: [slot][tile][Hk][part_rows][d] sums, not divided
   float2* part_ml;        // [slot][tile][Hk][part_rows] (maximum in log2 units, sum)
+  uint32_t* taken;        // with banks: items that blocks have taken after their own
   uint32_t* status;
   int sms;                // of the device
 };

@@ -793,7 +793,7 @@ bool plan_packed(PackedParams* p, bool bf16, int longest) {
 }
 
 size_t packed_workspace_bytes(const PackedParams& p) {
-  if (p.chunk == 0) return std::max<size_t>(16, size_t(p.banks) * 256 * p.d * 4);
+  if (p.chunk == 0) return p.banks > 0 ? kTakenBytes + size_t(p.banks) * 256 * p.d * 4 : 16;
   return size_t(p.items) * p.part_rows * (size_t(p.d) * 4 + 8);
 }
 

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++cnt;
         return true;
       };
-      std::conditional_t<kLong, PackedDealt, PackedBlocks> blocks(p, wk, lane, steal, steal_slot);
+      std::conditional_t<kLong, PackedCounted, PackedBlocks> blocks(p, wk, lane, steal, steal_slot);
       PackedItem it{}, following{};  // the first turn finds an item and loads nothing
       for (bool begun = false;; it = following, begun = true) {
         if (begun) {
@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float f = bank_scale[c * 128 + row];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  const float4 b = bank[i];
+                  float4 b;  // one after the other: all eight at once would not fit the registers
+                  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w) : "l"(bank + i) : "memory");
                   u[4 * i] = __float_as_uint(__uint_as_float(u[4 * i]) + (isfinite(b.x) ? b.x * f : b.x));
                   u[4 * i + 1] = __float_as_uint(__uint_as_float(u[4 * i + 1]) + (isfinite(b.y) ? b.y * f : b.y));
                   u[4 * i + 2] = __float_as_uint(__uint_as_float(u[4 * i + 2]) + (isfinite(b.z) ? b.z * f : b.z));
@@ -572,6 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Sets the items' counter to 0 once the kernels before are done with the workspace.
+__global__ void packed_none_taken_kernel(uint32_t* taken) {
+  grid_inputs_ready();
+  grid_let_next_start();
+  *taken = 0;
+}
+
 template <int D, bool kCut, bool kLong = false>
 cudaError_t launch_two(const PackedParams& p, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
@@ -579,6 +587,10 @@ cudaError_t launch_two(const PackedParams& p, cudaStream_t s) {
         make_view_map(&mv, p.v, p.Hk, p.Tk, D, p.vs, 1, 128)))
     return cudaErrorInvalidValue;
   constexpr int kSmem = Cfg<D, kLong>::kAlloc;
+  if constexpr (kLong) {
+    const cudaError_t e = launch_overlapped(packed_none_taken_kernel, dim3(1), 1, 0, s, 0, p.taken);
+    if (e != cudaSuccess) return e;
+  }
   const cudaError_t e = allow_smem_and_regs<packed_pair_kernel<D, kCut, kLong>>(kSmem, kLaunchRegs);
   if (e != cudaSuccess) return e;
   const long long blocks = kLong ? std::min(p.banks, p.sms) : p.items;

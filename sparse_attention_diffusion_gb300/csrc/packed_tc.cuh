@@ -143,11 +143,12 @@ struct PackedBlocks {
   }
 };
 
-// The same with the items dealt out in advance, for kernels whose blocks are numbered up to kBanks.
-struct PackedDealt {
+// The same for kernels whose blocks are numbered up to kBanks: after its own item a block takes the next one of a counter in the
+// workspace (dealt out in advance, nine chunks of 5,000 tokens and less over 90,000 keys and less took 3.2 ms instead of 2.8).
+struct PackedCounted {
   long long at = blockIdx.x;
   PackedLane sequence;
-  __device__ __forceinline__ PackedDealt(const PackedParams& p, const PackedWalk& wk, int lane, uint64_t*, uint32_t) {
+  __device__ __forceinline__ PackedCounted(const PackedParams& p, const PackedWalk& wk, int lane, uint64_t*, uint32_t) {
     if (p.S <= 32) sequence = packed_lane(p, wk.by_tq, wk.by_chunk, lane);
   }
   __device__ __forceinline__ bool next(const PackedParams& p, const PackedWalk& wk, int lane, PackedItem& it) {
@@ -157,7 +158,9 @@ struct PackedDealt {
         it.tiles = -1;
         return true;
       }
-      at += gridDim.x;
+      uint32_t taken = 0;
+      if (lane == 0) taken = atomicAdd(p.taken, 1u);
+      at = static_cast<long long>(gridDim.x) + __shfl_sync(0xffffffffu, taken, 0);
       if (const long long s = i * 32 + lane; s < p.S) {  // there are more items than sequences
         int a, b, c, d;
         if (!packed_sequence(p, int(s), a, b, c, d)) raise_status(p.status, kStatusBounds);

@@ -154,3 +154,87 @@ def test_own_keys_need_no_cut():
     want = torch.softmax(z, -1) @ v[1, i * n:i * n + n].double()
     size = torch.softmax(z, -1) @ v[1, i * n:i * n + n].double().abs()
     assert ((got[0][0][1, i * n:i * n + n].double() - want).abs() <= 2.0 ** -8 * (want.abs() + size) + 2.0 ** -14 * size).all()
+
+
+def reference(q, k, v, qs, ks, causal):
+    """float64 on the GPU, a head of a sequence at a time: o, lse, weight and spread as the oracle's."""
+    H, Tq, d = q.shape
+    g = H // k.shape[0]
+    o, w = (torch.zeros((H, Tq, d), dtype=torch.float64, device="cuda") for _ in range(2))
+    lse, spread = torch.full((H, Tq), -torch.inf, dtype=torch.float64, device="cuda"), torch.zeros((H, Tq), dtype=torch.float64, device="cuda")
+    for a, b, ka, kb in zip(qs, qs[1:], ks, ks[1:]):
+        nq, nk = b - a, kb - ka
+        if nq == 0 or nk == 0:
+            continue
+        hide = torch.arange(nk, device="cuda")[None, :] > torch.arange(nq, device="cuda")[:, None] + nk - nq
+        for h in range(H):
+            qh, kh, vh = q[h, a:b].double(), k[h // g, ka:kb].double(), v[h // g, ka:kb].double()
+            z = qh @ kh.T / d ** 0.5
+            if causal:
+                z.masked_fill_(hide, -torch.inf)
+            lse[h, a:b] = torch.logsumexp(z, -1)
+            p = torch.softmax(z, -1)
+            seen = torch.isfinite(lse[h, a:b])[:, None]
+            o[h, a:b], w[h, a:b] = torch.where(seen, p @ vh, 0.0), torch.where(seen, p @ vh.abs(), 0.0)
+            spread[h, a:b] = (qh.abs() @ kh.abs().T).amax(-1) / d ** 0.5
+    return o, lse, w, spread
+
+
+@pytest.mark.parametrize("d,H,Hk", [(64, 8, 8), (128, 12, 6)])
+@pytest.mark.parametrize("S,at", [(40, 7), (9, 8)])
+def test_chunks_of_many_requests(d, H, Hk, S, at):
+    """Prompts that go on over 2^18 and more kept keys in all, one of them over more than one span; on both sides of 32 sequences,
+    back to back over one workspace whatever it holds, and captured with lengths that change."""
+    g = torch.Generator(device="cuda").manual_seed(35)
+
+    def lengths(long):
+        nq = [(137 * i) % 600 if i % 5 else 0 for i in range(S)]
+        nk = [(5501 * i) % 9000 if i % 7 else 0 for i in range(S)]
+        nq[at], nk[at] = 650, long
+        return nq, nk
+
+    def bounds(n):
+        out = [0]
+        for x in n:
+            out.append(out[-1] + x)
+        return out
+
+    kinds = [tuple(map(bounds, lengths(n))) for n in (280_000, 131_073, 600)]
+    Tq, Tk = kinds[0][0][-1], kinds[0][1][-1]
+    q = (1.5 * torch.randn((H, Tq, d), generator=g, device="cuda")).bfloat16()
+    k, v = (torch.randn((Hk, Tk, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    desc = mcs.packed_desc(S, Tq, Tk, H, Hk, d, q.dtype, True, 650)
+    ws = mcs.packed_attn_workspace(desc)
+    assert ws.numel() >= 100 * 256 * d * 4  # a bank for each of many blocks
+    at_ = lambda s: torch.tensor(s, dtype=torch.int32, device="cuda")
+    qd, kd = at_(kinds[0][0]), at_(kinds[0][1])
+    new = lambda: (torch.full_like(q, 7.0), torch.full((H, Tq), 7.0, device="cuda"))
+    run = lambda o, lse: mcs.mcs_packed_attn(desc, q, k, v, qd, kd, o, lse, ws)
+    got = []
+    for _ in range(3):
+        ws.fill_(255)
+        got.append(new())
+        run(*got[-1])
+        got.append(new())
+        run(*got[-1])
+    mcs.mcs_check_status()
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
+    go = new()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(*go)
+    for qs, ks in kinds:
+        qd.copy_(at_(qs)), kd.copy_(at_(ks))
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        ro, rl, w, spread = reference(q, k, v, qs, ks, True)
+        seen = torch.isfinite(rl)
+        ds = spread * (d / 16 * 5.25 * 2.0 ** -23 + 2.0 ** -22)
+        sums = SPAN + 2.0 ** -14
+        bo = 2.0 ** -8 * (w + ro.abs()) + w * (2 * ds[..., None] + 2 * sums) + 1e-30
+        assert ((go[0].double() - ro).abs() <= bo)[seen].all()
+        assert ((go[1].double() - rl).abs() <= ds + 2.0 ** -13 + rl.abs() * 2.0 ** -22)[seen].all()
+        assert (go[0][~seen] == 0).all() and torch.isneginf(go[1][~seen]).all()
+    mcs.mcs_check_status()
