@@ -301,7 +301,7 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 }  // namespace
 
 // bf16: slabs, masks and the bytes of `up`'s shares, for row tiles of any height up to 256 (h and the rows' adapters are
-// smaller). fp32: h, the adapters' part of the sums and the
+// smaller): which kernel and tile a product takes depends on the device, and this is asked for without one. fp32: h, the adapters' part of the sums and the
 // rows' adapters.
 size_t adapters_workspace_bytes(const LinearParams& p, const AdapterParams& a, bool bf16) {
   if (!bf16) return align256(size_t(p.M) * a.R * 4) + align256(size_t(p.M) * p.O * 4) + align256(size_t(p.M) * 4);

@@ -1,5 +1,6 @@
-// Projections with low-rank adapters, fp32: h = scale_a x down_a^T and then h up_a^T on the CUDA cores, for the
-// fp32 product's epilogue to add to its sums. Both read and compute R / in of what the product does.
+// Projections with low-rank adapters, fp32: h = scale_a x down_a^T and then z = h up_a^T on the CUDA cores, for the
+// fp32 product's epilogue to add to its sums. They compute R / in and R / out of what the product does; the first reads all of x,
+// the second writes as much as the product, which reads it back: 4 M in + 8 M out bytes beside the product's 4 M (in + out).
 #include "adapters.h"
 #include "common.cuh"
 #include "launch.cuh"

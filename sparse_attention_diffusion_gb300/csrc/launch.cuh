@@ -5,6 +5,13 @@
 // and its writes are visible, and then grid_let_next_start(). The second call
 // comes after the first and after any tensor-memory allocation, so that a waiting
 // successor can never hold what a running kernel still needs.
+//
+// The second kernel of a pair that one call launches directly behind each other may read what the call was given (not what the
+// first kernel makes) before it waits: the first one lets it start only after its own wait, so everything that the call follows
+// is done by then. This holds as long as (1) nothing is launched between the two, (2) every thread of the first that lets
+// the second start has waited before, and (3) some thread of every block of the second waits before the block ends, so that
+// whatever follows the second, which may overwrite the workspace, finds both done. Three kernels do so: packed_join_kernel (the
+// bounds of the sequences), linear_pair_kernel and linear_few_kernel with adapters (x and w).
 #pragma once
 #include <atomic>
 #include <cstdint>

@@ -134,8 +134,8 @@ __device__ __forceinline__ void final_sums(const LinearParams& p, const FewArgs&
 // kTurns: two accumulators take turns and their sums are kept in registers; otherwise all stay until the end.
 // kAdapt: with kAdapterSteps the segments of a tile with an adapter add their k steps, shared among the slices, after
 // those of w, into a slice's last accumulator (adapters.h); with kAdapterRows a row's adapter is added to its sums on
-// their way out. Only what reads h waits for the kernel before, which makes it: that one has waited for what it follows
-// itself, so x and w are there.
+// their way out. Only what reads h waits for the kernel before, which makes it; x and w are there (launch.cuh, the second
+// kernel of a pair).
 template <int kAct, bool kTurns, int kAdapt>
 __global__ void __launch_bounds__(kThreads, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,

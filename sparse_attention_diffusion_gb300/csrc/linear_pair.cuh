@@ -199,8 +199,8 @@ __device__ __forceinline__ void store_odd(const LinearParams& p, int rows, int s
 // 2.33).
 // kAdapt: the segments of a tile with an adapter add their k steps after those of w, into the row's last accumulator
 // (adapters.h); the producers leave a word a stage that says how many 16-column products it takes and whether it is
-// the tile's last. Only they wait for the kernel before, which makes the slabs, and only when they come to them: that one
-// has waited for what it follows itself, so x and w are there.
+// the tile's last. Only they wait for the kernel before, which makes the slabs, and only when they come to them; x and w are
+// there (launch.cuh, the second kernel of a pair).
 template <int kAct, int kPieces, bool kBack, int kAdapt>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,

@@ -20,11 +20,11 @@
 // (an infinity or a NaN stays one whatever finite numbers are added).
 //
 // Cut sequences (chunk > 0): an item is one chunk of a sequence's keys, its sums leave as fp32 with the row's
-// maximum and sum, and a second launch joins them.
+// maximum and sum, and a second launch joins them. A sequence of one chunk leaves at once.
 //
 // This kernel is for sequences of one tile, single tokens over kept keys above all; longer ones go two tiles at a time
 // (packed_pair.cu). Measured: 64 tokens over 88 to 16,343 keys of 8 heads, d = 128: 263 to 266 us = 6.74 to 6.81 TB/s, as fast as
-// the measured copy (302 us with items dealt out in advance and larger pieces); one token over 4,000 keys 11.4 us.
+// the measured copy (302 us with items dealt out in advance and larger pieces); one token over 4,000 keys 11.5 to 11.9 us.
 #include <algorithm>
 #include <cfloat>
 
@@ -622,9 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (four sums a turn 11.4 us, eight 11.9, sixteen 12.9).
 template <int D, typename T>
 __global__ void __launch_bounds__(256, 3) packed_join_kernel(const PackedParams p, const PackedWalk wk) {
-  // The lengths are read before the wait for the pieces: the first kernel has waited for its own predecessor before it let
-  // this one start, so they are there. Every block waits, those without work too, as the next call may overwrite the
-  // workspace once this grid is done.
+  // The lengths are read before the wait for the pieces (launch.cuh, the second kernel of a pair). Every block waits, those
+  // without work too, as the next call may overwrite the workspace once this grid is done.
   const int lane = threadIdx.x & 31, tok = blockIdx.x;
   const int s = packed_find(p.q_start, p.S, wk.by_one, 0, tok, lane);
   int q0 = 0, nq = 0, k0 = 0, nk = 0;
@@ -736,12 +735,15 @@ cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
 // 2,000 keys and less 83 us with eight, 93 with sixteen, eight over 30,000 and less 74 and 101), unless they would be shorter than
 // eight tiles: then one round of pieces, or pieces of eight tiles (16 tokens over 4,000 keys and less of 16 heads, d = 64, 34 us in pieces
 // of two tiles, 24 so; three over 20,000 and less of 8 heads, d = 128, 22 and 17; the CUDA cores
-// rather have the short ones: 32 tokens over 4,000 keys and less of 4 heads 204 us so, 171 without). Otherwise two an SM, as every tile
+// rather have the short ones: 32 tokens over 4,000 keys and less of 4 heads 185 us so, 145 without, 64 over 2,000 of 8 heads 314 and
+// 302, though four over 9,000, d = 64, 33 and 36). Otherwise two an SM, as every tile
 // of a sequence leaves its sums (seven chunks of 300 tokens and less: 49 us with one, 45 with two, 53 with four, 65 with eight).
 // Sequences of more than one tile go two tiles at a time.
 // The plan is made without a device (its workspace is asked for on the host) and so for the SMs of a whole one; with fewer the pieces are
 // smaller than they need be.
 // On the tensor cores no piece has more than kSumKeys, and sequences of one tile that may be longer than twice as many are cut too.
+// The rules know the keys of all sequences together, not the longest: one of 16,384 keys among 64 whose others have 64 is not cut (123 us,
+// of which its bytes take 12), nor are eight tokens over 100,000 keys beside a prompt of 4,096 (1,422 us; alone 470 and 134).
 bool plan_packed(PackedParams* p, bool bf16, int longest) {
   constexpr int kSms = 152;
   p->g = p->H / p->Hk;

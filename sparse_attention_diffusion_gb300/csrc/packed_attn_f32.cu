@@ -1,5 +1,5 @@
-// Softmax attention over packed sequences on the CUDA cores, fp32: fp32 inputs have to match the
-// 64-bit result to 1e-5, which products of shorter numbers do not. The items of packed.h with 64 rows a tile,
+// Softmax attention over packed sequences on the CUDA cores, fp32. (Products of three bf16 parts on the tensor cores, as the
+// fp32 matrix product takes them, are as exact; they are not made here.) The items of packed.h with 64 rows a tile,
 // a block each; 16 rows where those are too few for the GPU.
 //
 // 256 threads as 16 x 16: a thread has 4 rows (or one) x 4 keys of the scores and as many x D / 16 columns of the sums, in packed
@@ -9,7 +9,7 @@
 // Masked keys as in the bf16 kernel: scores by selection, V that not all rows see with what is not finite as 0.
 // Measured: one full sequence of 4,096 tokens, 8 heads, d = 128: 1.91 ms, 36 TFLOP/s (0.45 of the pipe); four causal ones of
 // 1,200 tokens and less, 20 heads on 4: 253 us; 77 tokens of 4 heads on 2: 9.1 us; 32 single tokens over 4,000 keys and less of 4
-// heads, 16 heads, d = 128: 144 us, a fifth of the copy bandwidth, as a block waits for each tile (all of a tile's loads in
+// heads, 16 heads, d = 128: 145 us, a fifth of the copy bandwidth, as a block waits for each tile (all of a tile's loads in
 // flight at once: 166 us with four. Four blocks an SM instead of two: 129, but three tokens each over 2,531 keys of 9 heads
 // 192 instead of 127).
 #include "common.cuh"

@@ -614,7 +614,7 @@ def mcs_linear_plan(desc, residual=False, num_sms=152):
 # ---------------------------------------------------------------- requests of different lengths
 def packed_desc(S, Tq, Tk, H, Hk, d, dtype, causal=True, max_q=0, scale=0.0) -> mcs_packed_desc:
     """S sequences laid one behind the other: queries [H, Tq, d], keys and values [Hk, Tk, d], H a multiple of Hk; no
-    sequence has more than max_q queries (0: Tq)."""
+    sequence has more than max_q queries (0: Tq; time and workspace depend on it, so give 1 for single tokens)."""
     dt = MCS_BF16 if dtype in (torch.bfloat16, "bf16", MCS_BF16) else MCS_F32
     return mcs_packed_desc(int(S), int(Tq), int(Tk), int(H), int(Hk), int(d), dt, 1 if causal else 0, int(max_q), float(scale))
 
@@ -655,7 +655,8 @@ def mcs_packed_attn(desc, q, k, v, q_start, k_start, o, lse, ws, stream=None):
 
 
 def adapters_desc(count, rank, segments) -> mcs_adapters:
-    """A set of `count` low-rank adapters of one rank, for the rows of `segments` segments."""
+    """A set of `count` low-rank adapters of one rank, for the rows of `segments` segments. Time and workspace depend on
+    `segments`, also where many of them are empty."""
     return mcs_adapters(int(count), int(rank), int(segments))
 
 
