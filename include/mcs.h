@@ -395,7 +395,7 @@ typedef struct {
   int causal;      /* 0: every query sees its sequence's keys; else the last query sees all of them, each query
                       before it one key less */
   int max_q;       /* no sequence has more queries; 0: Tq. Time and workspace depend on it: with 1 for single tokens 64 of
-                      them over 4,000 keys and less take 76 us, with 0 110 (32 heads on 8, d = 128) */
+                      them over 4,000 keys and less take 76 us, with 0 109 (32 heads on 8, d = 128) */
   float scale;
 } mcs_packed_desc;
 
@@ -419,8 +419,8 @@ typedef struct {
  * may not overlap inputs. ws: at least mcs_packed_attn_workspace_size(desc) bytes (0 for an
  * invalid description; host only); its contents on entry are ignored; calls that may run at the
  * same time need one each. Equal calls give equal bits. Which way a call goes follows from its
- * description alone, not from the lengths, which lie on the device: long sequences under few queries
- * are cut by the keys that a sequence has on average, Tk / S, so a long one among many short ones
+ * description (and from whether q_start and k_start are the same array), not from the lengths, which
+ * lie on the device: long sequences under few queries are cut by the keys that a sequence has on average, Tk / S, so a long one among many short ones
  * and single tokens beside long prompts take longer than in calls of their own. The workspace holds
  * max_q rows' sums for every piece. */
 size_t mcs_packed_attn_workspace_size(const mcs_packed_desc *desc);
@@ -450,7 +450,7 @@ mcs_status mcs_packed_attn(const mcs_packed_desc *desc, const void *q, const mcs
  * same time need one each. Equal calls give equal bits. Which way a call goes and how much workspace
  * it takes (BF16: some 1 KB * rank a segment) follow from `segments`, not from the segments that have
  * rows: a table padded with empty ones costs both (256 x 4,096 -> 4,096 with two adapters of rank 32
- * 22 us with a table of 2, 44 of 64). */
+ * 21 us with a table of 2, 43 of 64). */
 typedef struct {
   int count;       /* adapters */
   int rank;

@@ -742,8 +742,8 @@ cudaError_t launch_tc(const PackedParams& p, cudaStream_t s) {
 // The plan is made without a device (its workspace is asked for on the host) and so for the SMs of a whole one; with fewer the pieces are
 // smaller than they need be.
 // On the tensor cores no piece has more than kSumKeys, and sequences of one tile that may be longer than twice as many are cut too.
-// The rules know the keys of all sequences together, not the longest: one of 16,384 keys among 64 whose others have 64 is not cut (123 us,
-// of which its bytes take 12), nor are eight tokens over 100,000 keys beside a prompt of 4,096 (1,422 us; alone 470 and 134).
+// The rules know the keys of all sequences together, not the longest: one of 16,384 keys among 64 whose others have 64 is not cut (122 us,
+// of which its bytes take 12), nor are eight tokens over 100,000 keys beside a prompt of 4,096 (1,440 us; alone 477 and 135).
 bool plan_packed(PackedParams* p, bool bf16, int longest) {
   constexpr int kSms = 152;
   p->g = p->H / p->Hk;
