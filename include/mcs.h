@@ -420,9 +420,9 @@ typedef struct {
  * invalid description; host only); its contents on entry are ignored; calls that may run at the
  * same time need one each. Equal calls give equal bits. Which way a call goes follows from its
  * description (and from whether q_start and k_start are the same array), not from the lengths, which
- * lie on the device: long sequences under few queries are cut by the keys that a sequence has on average, Tk / S, so a long one among many short ones
- * and single tokens beside long prompts take longer than in calls of their own. The workspace holds
- * max_q rows' sums for every piece. */
+ * lie on the device: long sequences under few queries are cut by the keys that a sequence has on
+ * average, Tk / S, so a long one among many short ones and single tokens beside long prompts take
+ * longer than in calls of their own. The workspace holds max_q rows' sums for every piece. */
 size_t mcs_packed_attn_workspace_size(const mcs_packed_desc *desc);
 mcs_status mcs_packed_attn(const mcs_packed_desc *desc, const void *q, const mcs_strides *qs, const void *k,
                            const mcs_strides *ks, const void *v, const mcs_strides *vs, const int32_t *q_start,
